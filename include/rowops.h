@@ -412,6 +412,165 @@ rowops_status_t rowops_fused_residual_rmsnorm(const void* x, const void* residua
                                               const void* w, float eps, int64_t M, int64_t N, int64_t ld,
                                               rowops_dtype_t dtype, cudaStream_t stream);
 
+/*
+ * Group norm with an activation, channels last. x holds B samples of S
+ * positions (height x width, or any other order of them) of C channels;
+ * positions start `ld` elements apart, samples S * ld. The channels form G
+ * groups of L = C / G neighbours; over the m = S * L elements of a sample's group
+ *   mean = sum x / m;  var = sum (x - mean)^2 / m (biased);  rstd = 1 / sqrt(var + eps)
+ *   y = act((x - mean) rstd w_c + b_c)
+ * (No counterpart on the source pages: the group form of their LayerNorm ->
+ * affine -> GELU, rowops_layernorm_gelu.)
+ *
+ *   x, y    device pointers to B * S rows of `ld` elements; y may equal x.
+ *   w, b    device pointers to C entries of `dtype`, or NULL (1, 0); apart from y.
+ *   eps     as for rowops_layernorm_gelu.
+ *   act     a rowops_act_t; the GELUs are those of rowops_gelu.
+ *   stats   NULL, or B * G pairs of floats, 8-byte aligned: (mean, rstd) of every
+ *           group, for the backward pass; apart from x, y, w, b and the workspace.
+ *   workspace, workspace_bytes   device memory, 256-byte aligned, at least
+ *           rowops_groupnorm_act_workspace_bytes(B, S, C, G, dtype) bytes
+ *           (overwritten), apart from the other tensors; calls sharing it must be
+ *           ordered on one stream.
+ * C is at most 8192 (ROWOPS_ERR_UNSUPPORTED beyond) and a multiple of G. B == 0
+ * or S == 0 is a no-op. A NaN or an infinity in a group makes that group of that
+ * sample NaN. The variance is merged from centred partial sums, so a mean far
+ * from zero costs it no precision.
+ */
+typedef enum rowops_act {
+    ROWOPS_ACT_NONE = 0,
+    ROWOPS_ACT_SILU = 1,      /* z / (1 + exp(-z)) */
+    ROWOPS_ACT_GELU = 2,      /* exact */
+    ROWOPS_ACT_GELU_TANH = 3, /* tanh approximation */
+} rowops_act_t;
+
+size_t rowops_groupnorm_act_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rowops_dtype_t dtype);
+rowops_status_t rowops_groupnorm_act(const void* x, void* y, const void* w, const void* b, float eps, int64_t B,
+                                     int64_t S, int64_t C, int64_t G, int64_t ld, rowops_act_t act, float* stats,
+                                     rowops_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream);
+
+/*
+ * Backward of rowops_groupnorm_act. With xh = (x - mean) rstd, z = xh w + b,
+ * dz = dy act'(z), dxh = dz w and means over the m elements of a sample's group:
+ *   dx = rstd (dxh - mean(dxh) - xh mean(dxh xh))
+ *   dw = sum over samples and positions of dz xh,  db = of dz
+ *   x, dy, dx   device pointers to B * S rows of `ld` elements; dx overlaps
+ *               neither x nor dy.
+ *   w, b, act   as in the forward call.
+ *   stats       the (mean, rstd) pairs that the forward call wrote.
+ *   dw, db      device pointers to C floats each, 4-byte aligned, apart from
+ *               each other and from all else. Added up in a fixed order.
+ *   workspace, workspace_bytes   as above, with
+ *               rowops_groupnorm_act_backward_workspace_bytes.
+ * B == 0 or S == 0 writes zeros to dw and db.
+ */
+size_t rowops_groupnorm_act_backward_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G,
+                                                     rowops_dtype_t dtype);
+rowops_status_t rowops_groupnorm_act_backward(const void* x, const void* dy, const void* w, const void* b,
+                                              const float* stats, void* dx, float* dw, float* db, int64_t B,
+                                              int64_t S, int64_t C, int64_t G, int64_t ld, rowops_act_t act,
+                                              rowops_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                              cudaStream_t stream);
+
+/*
+ * Fused bias + dropout + residual:
+ *   y[i, j] = residual[i, j] + keep(i, j) (x[i, j] + bias[j]) / (1 - p)
+ * in fp32, rounded once. The mask keep(i, j) is a function of the position, the
+ * seed and the offset alone, whatever the layout or type, and is never stored:
+ * the backward pass makes it again. Philox4x32-10 with key `seed` (low word
+ * first) and counter (j / 8, i, low word, high word of the offset) gives four
+ * words; element j takes the 16 bits of word (j mod 8) / 2, the lower half where
+ * j is even, and is kept where they are at least q = round(65536 p). The
+ * probability is thus held in steps of 2^-16, and 1 / (1 - p) is that of the
+ * step, 65536 / (65536 - q), so the mean is kept exactly. A dropped element
+ * contributes exactly 0, whatever x holds there. p == 1 drops everything.
+ * (No counterpart on the source pages, which name dropout's place only.)
+ *
+ *   x, y       device pointers to M rows of `ld` elements; y may equal x.
+ *   residual   as x, or NULL; y may equal it.
+ *   bias       device pointer to N elements of `dtype`, or NULL; apart from y.
+ *   p          in [0, 1].
+ *   seed, offset   a call draws from (seed, offset): use another offset for
+ *              each call that shall have a mask of its own.
+ *   device_offset  NULL, or an 8-byte aligned device pointer to a number that the
+ *              kernel adds to `offset` (mod 2^64): a captured graph replays with
+ *              new masks when the caller changes it between replays.
+ * M is at most 2^32 (ROWOPS_ERR_UNSUPPORTED beyond). 16-byte aligned rows and N a
+ * multiple of the 16-byte vector take vector accesses, other layouts single
+ * elements.
+ */
+rowops_status_t rowops_bias_dropout_residual(const void* x, const void* residual, const void* bias, void* y, float p,
+                                             uint64_t seed, uint64_t offset, const uint64_t* device_offset,
+                                             int64_t M, int64_t N, int64_t ld, rowops_dtype_t dtype,
+                                             cudaStream_t stream);
+
+/*
+ * Backward of rowops_bias_dropout_residual, with the forward call's p, seed,
+ * offset and device_offset (its number unchanged since):
+ *   dx[i, j] = keep(i, j) dy[i, j] / (1 - p);  dbias[j] = sum_i dx[i, j]
+ * (the residual's gradient is dy). dbias in fp32, from the unrounded dx, added
+ * up in a fixed order.
+ *   dy, dx   device pointers to M rows of `ld` elements; dx may equal dy.
+ *   dbias    device pointer to N floats, apart from all else, or NULL.
+ *   workspace, workspace_bytes   needed with dbias only: device memory, 256-byte
+ *            aligned, at least
+ *            rowops_bias_dropout_residual_backward_workspace_bytes(M, N, dtype)
+ *            bytes (overwritten), apart from the other tensors; calls sharing it
+ *            must be ordered on one stream.
+ * M == 0 writes zeros to dbias.
+ */
+size_t rowops_bias_dropout_residual_backward_workspace_bytes(int64_t M, int64_t N, rowops_dtype_t dtype);
+rowops_status_t rowops_bias_dropout_residual_backward(const void* dy, void* dx, float* dbias, float p, uint64_t seed,
+                                                      uint64_t offset, const uint64_t* device_offset, int64_t M,
+                                                      int64_t N, int64_t ld, rowops_dtype_t dtype, void* workspace,
+                                                      size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Balance loss of a router over E experts, with the experts' counts. For T rows
+ * of logits and the K experts chosen for each, over the n rows that take part:
+ *   p_t = softmax(logits_t);  counts[e] = how often e was chosen
+ *   loss = coef E sum_e (counts[e] / (n K)) (sum_t p_te / n)
+ * n = 0 gives 0. Rows follow rowops_softmax: -inf logits have p = 0, a row of
+ * -inf alone adds nothing to the sums, a NaN makes the loss NaN. (No counterpart
+ * on the source pages: rowops_softmax followed by column sums.)
+ *
+ *   logits    device pointer to T rows of `ld` elements of `dtype`.
+ *   experts   device pointer to T * K indices, back to back, of index_bytes (4
+ *             or 8) bytes each. One outside [0, E) counts for no expert (a
+ *             dropped choice); one that occurs twice in a row counts twice.
+ *   mask      NULL, or T bytes: a row whose byte is 0 takes no part (padding):
+ *             its logits and choices are not read.
+ *   loss      device pointer to one float.
+ *   counts    device pointer to E + 1 int64: the experts' counts, then n. For
+ *             the backward pass, and for the dispatch of the tokens.
+ *   workspace, workspace_bytes   device memory, 256-byte aligned, at least
+ *             rowops_router_balance_loss_workspace_bytes(T, E, dtype) bytes
+ *             (overwritten; 0 for small problems: NULL will do), apart from the
+ *             other tensors; calls sharing it must be ordered on one stream.
+ * E is at most 1024 and T * K below 2^31 (ROWOPS_ERR_UNSUPPORTED beyond). Sums in
+ * a fixed order. T == 0 writes a loss of 0 and counts of 0.
+ */
+size_t rowops_router_balance_loss_workspace_bytes(int64_t T, int64_t E, rowops_dtype_t dtype);
+rowops_status_t rowops_router_balance_loss(const void* logits, const void* experts, int index_bytes,
+                                           const uint8_t* mask, float coef, float* loss, int64_t* counts, int64_t T,
+                                           int64_t E, int64_t K, int64_t ld, rowops_dtype_t dtype, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Gradient of rowops_router_balance_loss with respect to the logits (the counts
+ * are constants):
+ *   dlogits_te = dloss coef E / (n^2 K) p_te (counts[e] - sum_j counts[j] p_tj)
+ * and 0 in the rows that take no part.
+ *   logits, mask, coef, K   as in the forward call; counts as it wrote them.
+ *   dloss     device pointer to one float: the loss's own gradient.
+ *   dlogits   device pointer to T rows of `ld` elements; may equal logits.
+ */
+rowops_status_t rowops_router_balance_loss_backward(const void* logits, const int64_t* counts, const float* dloss,
+                                                    const uint8_t* mask, float coef, void* dlogits, int64_t T,
+                                                    int64_t E, int64_t K, int64_t ld, rowops_dtype_t dtype,
+                                                    cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

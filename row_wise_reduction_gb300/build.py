@@ -49,6 +49,10 @@ SOURCES = [
     "gelu.cu",
     "ln_gelu_bwd.cu",
     "ln_gelu_flat.cu",
+    "groupnorm_f32.cu",
+    "groupnorm_bf16.cu",
+    "dropout.cu",
+    "router_balance.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -1,0 +1,24 @@
+// Philox4x32-10, the counter-based generator of Salmon, Moraes, Dror and Shaw,
+// "Parallel Random Numbers: As Easy as 1, 2, 3" (SC 2011): ten rounds of two
+// 32 x 32 -> 64 bit products on a 128-bit counter, keyed with 64 bits. A block
+// of four words depends on its counter and key alone, so any thread can make
+// any block at any time and nothing has to be stored.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace rowops {
+
+__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint2 k) {
+#pragma unroll
+    for (int round = 0; round < 10; ++round) {
+        const uint64_t a = uint64_t(0xD2511F53u) * c.x, b = uint64_t(0xCD9E8D57u) * c.z;
+        c = make_uint4(uint32_t(b >> 32) ^ c.y ^ k.x, uint32_t(b), uint32_t(a >> 32) ^ c.w ^ k.y, uint32_t(a));
+        k.x += 0x9E3779B9u;
+        k.y += 0xBB67AE85u;
+    }
+    return c;
+}
+
+}  // namespace rowops

@@ -1,6 +1,7 @@
 // C ABI of librowops.so: argument validation, kernel selection and launch.
 // The operations themselves are documented in include/rowops.h.
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <initializer_list>
@@ -1023,6 +1024,263 @@ rowops_status_t rowops_online_softmax_status(const void* workspace, cudaStream_t
         return finish(cudaErrorUnknown);
     if (word == 0u) return ROWOPS_OK;
     return word == unsigned(ROWOPS_ERR_TIMEOUT) ? ROWOPS_ERR_TIMEOUT : ROWOPS_ERR_CUDA;
+}
+
+namespace {
+// [a, a + an) and [b, b + bn) share no byte (a NULL range shares none)
+bool apart(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return !a || !b || !an || !bn || pa + an <= pb || pb + bn <= pa;
+}
+
+struct Range {
+    const void* p;
+    size_t n;
+};
+
+// `one` is apart from each of `others`
+bool apart_from(Range one, std::initializer_list<Range> others) {
+    for (const Range& o : others)
+        if (!apart(one.p, one.n, o.p, o.n)) return false;
+    return true;
+}
+
+// bytes of M rows (M > 0) that check_rows has passed
+size_t rows_bytes(int64_t M, int64_t N, int64_t ld, int es) { return size_t(((M - 1) * ld + N) * es); }
+
+rowops_status_t zero(float* p, int64_t n, cudaStream_t stream) {
+    return finish(cudaMemsetAsync(p, 0, size_t(n) * 4, stream));
+}
+
+// Group norm: the shape's checks; M = B S rows.
+rowops_status_t check_groups(int64_t B, int64_t S, int64_t C, int64_t G, rowops_dtype_t dtype, int64_t* M) {
+    if (!valid_dtype(dtype) || B < 0 || S < 0 || C < 1 || G < 1 || C % G != 0) return ROWOPS_ERR_INVALID_VALUE;
+    if (C > kGnMaxChannels || B > INT32_MAX || (S > 0 && B > INT64_MAX / 16 / kGnMaxChannels / S))
+        return ROWOPS_ERR_UNSUPPORTED;
+    *M = B * S;
+    return ROWOPS_OK;
+}
+
+bool valid_act(rowops_act_t act) { return act >= ROWOPS_ACT_NONE && act <= ROWOPS_ACT_GELU_TANH; }
+
+rowops_status_t make_mask(float p, uint64_t seed, uint64_t offset, const uint64_t* device_offset, DropoutMask* m) {
+    if (!(p >= 0.f && p <= 1.f) || !aligned(device_offset, 8)) return ROWOPS_ERR_INVALID_VALUE;
+    *m = DropoutMask{unsigned(std::lrint(double(p) * 65536.0)), seed, offset, device_offset};
+    return ROWOPS_OK;
+}
+
+// Rows of 16-byte vectors for the operators that go by them or by elements.
+bool vector_rows(const Tuning& tn, int64_t N, int64_t ld, int es, std::initializer_list<const void*> ptrs) {
+    if (tn.family == Family::Looped || N % (16 / es) != 0 || (ld * es) % 16 != 0) return false;
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return false;
+    return true;
+}
+}  // namespace
+
+size_t rowops_groupnorm_act_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rowops_dtype_t dtype) {
+    int64_t M = 0;
+    if (check_groups(B, S, C, G, dtype, &M) != ROWOPS_OK || M == 0) return 0;
+    const GnArgs a = gn_plan(B, S, C, G, C, elem_bytes(dtype), 0.f);
+    return size_t(B) * a.chunks * size_t(G) * 8;  // a mean and a sum of squares for every chunk's groups
+}
+
+rowops_status_t rowops_groupnorm_act(const void* x, void* y, const void* w, const void* b, float eps, int64_t B,
+                                     int64_t S, int64_t C, int64_t G, int64_t ld, rowops_act_t act, float* stats,
+                                     rowops_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+    int64_t M = 0;
+    rowops_status_t st = check_groups(B, S, C, G, dtype, &M);
+    if (st == ROWOPS_OK) st = check_rows(x, y, M, C, ld, dtype);
+    if (st != ROWOPS_OK) return st;
+    if (!(eps >= 0.f) || eps == INFINITY || !valid_act(act)) return ROWOPS_ERR_INVALID_VALUE;
+    if (M == 0) return ROWOPS_OK;
+    const int es = elem_bytes(dtype);
+    const size_t row = size_t(C) * es, rows = rows_bytes(M, C, ld, es), sb = size_t(B) * G * 8;
+    if (!aligned(w, es) || !aligned(b, es) || !aligned(stats, 8)) return ROWOPS_ERR_INVALID_VALUE;
+    if (!apart_from({y, rows}, {{w, row}, {b, row}}) ||
+        !apart_from({stats, sb}, {{x, rows}, {y, rows}, {w, row}, {b, row}}))
+        return ROWOPS_ERR_INVALID_VALUE;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < rowops_groupnorm_act_workspace_bytes(B, S, C, G, dtype))
+        return ROWOPS_ERR_WORKSPACE;
+    if (!apart_from({workspace, workspace_bytes}, {{x, rows}, {y, rows}, {w, row}, {b, row}, {stats, sb}}))
+        return ROWOPS_ERR_INVALID_VALUE;
+    const Tuning tn = tuning();
+    LaunchCfg cfg;
+    if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
+    const bool vec = vector_rows(tn, C, ld, es, {x, y});
+    const GnForwardLaunch fn = dtype == ROWOPS_F32 ? gn_forward_f32(vec, act) : gn_forward_bf16(vec, act);
+    return finish(fn(x, y, w, b, stats, workspace, gn_plan(B, S, C, G, ld, es, eps), cfg));
+}
+
+size_t rowops_groupnorm_act_backward_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G,
+                                                     rowops_dtype_t dtype) {
+    int64_t M = 0;
+    if (check_groups(B, S, C, G, dtype, &M) != ROWOPS_OK || M == 0) return 0;
+    const GnArgs a = gn_plan(B, S, C, G, C, elem_bytes(dtype), 0.f);
+    return size_t(B) * a.chunks * (size_t(C) + size_t(G)) * 8;  // two sums for every chunk's channels and groups
+}
+
+rowops_status_t rowops_groupnorm_act_backward(const void* x, const void* dy, const void* w, const void* b,
+                                              const float* stats, void* dx, float* dw, float* db, int64_t B,
+                                              int64_t S, int64_t C, int64_t G, int64_t ld, rowops_act_t act,
+                                              rowops_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                              cudaStream_t stream) {
+    int64_t M = 0;
+    rowops_status_t st = check_groups(B, S, C, G, dtype, &M);
+    if (st == ROWOPS_OK) st = check_rows(x, dx, M, C, ld, dtype);
+    if (st == ROWOPS_OK) st = check_rows(dy, dx, M, C, ld, dtype);
+    if (st != ROWOPS_OK) return st;
+    if (!valid_act(act) || !dw || !db || !aligned(dw, 4) || !aligned(db, 4)) return ROWOPS_ERR_INVALID_VALUE;
+    const int es = elem_bytes(dtype);
+    const size_t row = size_t(C) * es, rows = M > 0 ? rows_bytes(M, C, ld, es) : 0, sb = size_t(B) * G * 8;
+    const size_t sums = size_t(C) * 4;
+    if (!aligned(w, es) || !aligned(b, es) || (M > 0 && !stats) || !aligned(stats, 8)) return ROWOPS_ERR_INVALID_VALUE;
+    const Range in[] = {{x, rows}, {dy, rows}, {w, row}, {b, row}, {stats, M > 0 ? sb : 0}};
+    for (const Range& r : in)  // nothing that is read is written
+        if (!apart_from(r, {{dx, rows}, {dw, sums}, {db, sums}})) return ROWOPS_ERR_INVALID_VALUE;
+    if (!apart_from({dw, sums}, {{db, sums}, {dx, rows}}) || !apart(db, sums, dx, rows))
+        return ROWOPS_ERR_INVALID_VALUE;
+    if (M == 0) {
+        st = zero(dw, C, stream);
+        return st == ROWOPS_OK ? zero(db, C, stream) : st;
+    }
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < rowops_groupnorm_act_backward_workspace_bytes(B, S, C, G, dtype))
+        return ROWOPS_ERR_WORKSPACE;
+    for (const Range& r : in)
+        if (!apart(workspace, workspace_bytes, r.p, r.n)) return ROWOPS_ERR_INVALID_VALUE;
+    if (!apart_from({workspace, workspace_bytes}, {{dx, rows}, {dw, sums}, {db, sums}}))
+        return ROWOPS_ERR_INVALID_VALUE;
+    const Tuning tn = tuning();
+    LaunchCfg cfg;
+    if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
+    const bool vec = vector_rows(tn, C, ld, es, {x, dy, dx});
+    const GnBackwardLaunch fn = dtype == ROWOPS_F32 ? gn_backward_f32(vec, act) : gn_backward_bf16(vec, act);
+    return finish(fn(x, dy, w, b, stats, dx, dw, db, workspace, gn_plan(B, S, C, G, ld, es, 0.f), cfg));
+}
+
+rowops_status_t rowops_bias_dropout_residual(const void* x, const void* residual, const void* bias, void* y, float p,
+                                             uint64_t seed, uint64_t offset, const uint64_t* device_offset,
+                                             int64_t M, int64_t N, int64_t ld, rowops_dtype_t dtype,
+                                             cudaStream_t stream) {
+    DropoutMask mask;
+    rowops_status_t st = make_mask(p, seed, offset, device_offset, &mask);
+    if (st == ROWOPS_OK) st = check_rows(x, y, M, N, ld, dtype);
+    if (st == ROWOPS_OK && residual) st = check_rows(residual, y, M, N, ld, dtype);
+    if (st != ROWOPS_OK) return st;
+    if (M > int64_t(1) << 32) return ROWOPS_ERR_UNSUPPORTED;
+    if (M == 0) return ROWOPS_OK;
+    const int es = elem_bytes(dtype);
+    const size_t rows = rows_bytes(M, N, ld, es);
+    if (!aligned(bias, es) || !apart_from({y, rows}, {{bias, size_t(N) * es}, {device_offset, 8}}))
+        return ROWOPS_ERR_INVALID_VALUE;
+    const Tuning tn = tuning();
+    LaunchCfg cfg;
+    if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
+    const bool vec = vector_rows(tn, N, ld, es, {x, y, residual});
+    const DropoutLaunch fn = dtype == ROWOPS_F32 ? dropout_f32() : dropout_bf16();
+    return finish(fn(x, residual, bias, y, nullptr, 0, nullptr, M, N, ld, mask, vec, cfg));
+}
+
+size_t rowops_bias_dropout_residual_backward_workspace_bytes(int64_t M, int64_t N, rowops_dtype_t dtype) {
+    if (!valid_dtype(dtype) || M < 0 || N < 1 || N >= (int64_t(1) << 31)) return 0;
+    // a partial row for each of at most bwd_max_partials(N) chunks of rows
+    return size_t(std::min<int64_t>(M, bwd_max_partials(N))) * size_t(N) * sizeof(float);
+}
+
+rowops_status_t rowops_bias_dropout_residual_backward(const void* dy, void* dx, float* dbias, float p, uint64_t seed,
+                                                      uint64_t offset, const uint64_t* device_offset, int64_t M,
+                                                      int64_t N, int64_t ld, rowops_dtype_t dtype, void* workspace,
+                                                      size_t workspace_bytes, cudaStream_t stream) {
+    DropoutMask mask;
+    rowops_status_t st = make_mask(p, seed, offset, device_offset, &mask);
+    if (st == ROWOPS_OK) st = check_rows(dy, dx, M, N, ld, dtype);
+    if (st != ROWOPS_OK) return st;
+    if (M > int64_t(1) << 32) return ROWOPS_ERR_UNSUPPORTED;
+    if (!aligned(dbias, 4)) return ROWOPS_ERR_INVALID_VALUE;
+    if (M == 0) return dbias ? zero(dbias, N, stream) : ROWOPS_OK;
+    const int es = elem_bytes(dtype);
+    const size_t rows = rows_bytes(M, N, ld, es), sums = size_t(N) * 4;
+    if (!apart(dx, rows, device_offset, 8) ||
+        !apart_from({dbias, sums}, {{dy, rows}, {dx, rows}, {device_offset, 8}}))
+        return ROWOPS_ERR_INVALID_VALUE;
+    if (dbias) {
+        if (!workspace || !aligned(workspace, 256) ||
+            workspace_bytes < rowops_bias_dropout_residual_backward_workspace_bytes(M, N, dtype))
+            return ROWOPS_ERR_WORKSPACE;
+        if (!apart_from({workspace, workspace_bytes}, {{dy, rows}, {dx, rows}, {dbias, sums}, {device_offset, 8}}))
+            return ROWOPS_ERR_INVALID_VALUE;
+    }
+    const Tuning tn = tuning();
+    LaunchCfg cfg;
+    if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
+    const bool vec = vector_rows(tn, N, ld, es, {dy, dx});
+    const int most = int(std::min<int64_t>(M, bwd_max_partials(N)));
+    const DropoutLaunch fn = dtype == ROWOPS_F32 ? dropout_f32() : dropout_bf16();
+    return finish(fn(dy, nullptr, nullptr, dx, static_cast<float*>(workspace), most, dbias, M, N, ld, mask, vec, cfg));
+}
+
+size_t rowops_router_balance_loss_workspace_bytes(int64_t T, int64_t E, rowops_dtype_t dtype) {
+    if (!valid_dtype(dtype) || T < 0 || T > INT32_MAX || E < 1 || E > kBalanceMaxExperts) return 0;
+    if (T * E * elem_bytes(dtype) <= kBalanceOneCluster) return 0;
+    return size_t(kBalanceMaxClusters) * (2 * size_t(E) + 1) * 4;
+}
+
+rowops_status_t rowops_router_balance_loss(const void* logits, const void* experts, int index_bytes,
+                                           const uint8_t* mask, float coef, float* loss, int64_t* counts, int64_t T,
+                                           int64_t E, int64_t K, int64_t ld, rowops_dtype_t dtype, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream) {
+    rowops_status_t st = check_rows(logits, logits, T, E, ld, dtype);
+    if (st != ROWOPS_OK) return st;
+    if (K < 1 || (index_bytes != 4 && index_bytes != 8) || !std::isfinite(coef)) return ROWOPS_ERR_INVALID_VALUE;
+    if (!loss || !counts || !aligned(loss, 4) || !aligned(counts, 8)) return ROWOPS_ERR_INVALID_VALUE;
+    if (E > kBalanceMaxExperts || T > INT32_MAX / K) return ROWOPS_ERR_UNSUPPORTED;
+    const size_t cb = size_t(E + 1) * 8;
+    if (!apart(loss, 4, counts, cb)) return ROWOPS_ERR_INVALID_VALUE;
+    if (T == 0) {
+        if (cudaMemsetAsync(counts, 0, cb, stream) != cudaSuccess) return finish(cudaErrorUnknown);
+        return zero(loss, 1, stream);
+    }
+    if (!experts || !aligned(experts, index_bytes)) return ROWOPS_ERR_INVALID_VALUE;
+    const int es = elem_bytes(dtype);
+    const Range in[] = {{logits, rows_bytes(T, E, ld, es)}, {experts, size_t(T * K) * index_bytes}, {mask, size_t(T)}};
+    for (const Range& r : in)
+        if (!apart_from(r, {{loss, 4}, {counts, cb}})) return ROWOPS_ERR_INVALID_VALUE;
+    if (const size_t need = rowops_router_balance_loss_workspace_bytes(T, E, dtype)) {
+        if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ROWOPS_ERR_WORKSPACE;
+        if (!apart_from({workspace, workspace_bytes}, {in[0], in[1], in[2], {loss, 4}, {counts, cb}}))
+            return ROWOPS_ERR_INVALID_VALUE;
+    }
+    const Tuning tn = tuning();
+    LaunchCfg cfg;
+    if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
+    const bool vec = vector_rows(tn, E, ld, es, {logits});
+    const BalanceLaunch fn = dtype == ROWOPS_F32 ? balance_f32() : balance_bf16();
+    return finish(fn(logits, experts, index_bytes == 8, mask, T, int(E), int(K), ld, coef, loss, counts, workspace,
+                     vec, cfg));
+}
+
+rowops_status_t rowops_router_balance_loss_backward(const void* logits, const int64_t* counts, const float* dloss,
+                                                    const uint8_t* mask, float coef, void* dlogits, int64_t T,
+                                                    int64_t E, int64_t K, int64_t ld, rowops_dtype_t dtype,
+                                                    cudaStream_t stream) {
+    rowops_status_t st = check_rows(logits, dlogits, T, E, ld, dtype);
+    if (st != ROWOPS_OK) return st;
+    if (K < 1 || !std::isfinite(coef)) return ROWOPS_ERR_INVALID_VALUE;
+    if (E > kBalanceMaxExperts || T > INT32_MAX / K) return ROWOPS_ERR_UNSUPPORTED;
+    if (T == 0) return ROWOPS_OK;
+    if (!counts || !dloss || !aligned(counts, 8) || !aligned(dloss, 4)) return ROWOPS_ERR_INVALID_VALUE;
+    const int es = elem_bytes(dtype);
+    if (!apart_from({dlogits, rows_bytes(T, E, ld, es)}, {{counts, size_t(E + 1) * 8}, {dloss, 4}, {mask, size_t(T)}}))
+        return ROWOPS_ERR_INVALID_VALUE;
+    const Tuning tn = tuning();
+    LaunchCfg cfg;
+    if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
+    const bool vec = vector_rows(tn, E, ld, es, {logits, dlogits});
+    const BalanceBackwardLaunch fn = dtype == ROWOPS_F32 ? balance_backward_f32() : balance_backward_bf16();
+    return finish(fn(logits, counts, dloss, mask, dlogits, T, int(E), int(K), ld, coef, vec, cfg));
 }
 
 }  // extern "C"

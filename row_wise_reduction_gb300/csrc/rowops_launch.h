@@ -223,6 +223,79 @@ ReduceLaunch reduce_reg_bf16(int tpr_index, int vpt, int op);
 ReduceLaunch reduce_looped_f32(int op);
 ReduceLaunch reduce_looped_bf16(int op);
 
+// Bias + dropout + residual (r, b may be NULL), and with db (N floats) the
+// column sums of the dropped-out rows, by way of at most max_partials rows of N
+// floats in `part`. drop: round(65536 p).
+struct DropoutMask {
+    unsigned drop;
+    uint64_t seed, offset;
+    const uint64_t* device_offset;  // NULL, or added to offset
+};
+using DropoutLaunch = cudaError_t (*)(const void* x, const void* r, const void* b, void* y, float* part,
+                                      int max_partials, float* db, int64_t M, int64_t N, int64_t ld,
+                                      const DropoutMask& mask, bool vec, const LaunchCfg& cfg);
+DropoutLaunch dropout_f32();
+DropoutLaunch dropout_bf16();
+
+// Balance loss of a router. Problems of at most kBalanceOneCluster bytes of
+// logits are one cluster's and need no workspace; others leave at most
+// kBalanceMaxClusters rows of E floats and E + 1 ints in it.
+constexpr int kBalanceMaxExperts = 1024;
+constexpr int kBalanceMaxClusters = 128;
+constexpr int64_t kBalanceOneCluster = int64_t(512) << 10;
+using BalanceLaunch = cudaError_t (*)(const void* logits, const void* experts, bool wide, const uint8_t* mask,
+                                      int64_t rows, int E, int K, int64_t ld, float coef, float* loss,
+                                      int64_t* counts, void* ws, bool vec, const LaunchCfg& cfg);
+BalanceLaunch balance_f32();
+BalanceLaunch balance_bf16();
+using BalanceBackwardLaunch = cudaError_t (*)(const void* logits, const int64_t* counts, const float* dloss,
+                                              const uint8_t* mask, void* dlogits, int64_t rows, int E, int K,
+                                              int64_t ld, float coef, bool vec, const LaunchCfg& cfg);
+BalanceBackwardLaunch balance_backward_f32();
+BalanceBackwardLaunch balance_backward_bf16();
+
+// Group norm + activation on channels-last data and its backward; GnArgs'
+// chunks, chunk_rows and rows as gn_plan sets them (the workspace's layout
+// follows from them).
+constexpr int kGnMaxChannels = 8192;
+struct GnArgs {
+    int64_t S, ld;
+    int B, C, G, L;      // L = C / G channels of a group
+    int tx, tiles;       // channel vectors side by side, and how many times
+    int chunks;          // of a sample, in the pass that leaves sums
+    int64_t chunk_rows;  // positions of such a chunk
+    int64_t rows;        // positions of a CTA of the pass that writes
+    float eps;
+};
+// Chunks of a sample: four CTAs for each of 152 SMs over all samples, of at
+// least 16 KiB, and at most 65536 group sums a sample (a CTA of the second pass
+// reads all of its sample's).
+inline GnArgs gn_plan(int64_t B, int64_t S, int64_t C, int64_t G, int64_t ld, int es, float eps) {
+    GnArgs a{};
+    a.S = S, a.ld = ld, a.B = int(B), a.C = int(C), a.G = int(G), a.L = int(C / G), a.eps = eps;
+    const int64_t least = (16384 + C * es - 1) / (C * es);
+    auto split = [&](int64_t ctas, int64_t most) {
+        int64_t n = (ctas + B - 1) / B;
+        const int64_t fit = (S + least - 1) / least;
+        n = n < fit ? n : fit;
+        n = n < most ? n : most;
+        return (S + n - 1) / n;  // positions of a chunk
+    };
+    a.chunk_rows = split(608, 65536 / G);
+    a.chunks = int((S + a.chunk_rows - 1) / a.chunk_rows);
+    a.rows = split(1216, 65535);
+    return a;
+}
+using GnForwardLaunch = cudaError_t (*)(const void* x, void* y, const void* w, const void* b, float* stats, void* ws,
+                                        GnArgs a, const LaunchCfg& cfg);
+using GnBackwardLaunch = cudaError_t (*)(const void* x, const void* dy, const void* w, const void* b,
+                                         const float* stats, void* dx, float* dw, float* db, void* ws, GnArgs a,
+                                         const LaunchCfg& cfg);
+GnForwardLaunch gn_forward_f32(bool vec, int act);
+GnForwardLaunch gn_forward_bf16(bool vec, int act);
+GnBackwardLaunch gn_backward_f32(bool vec, int act);
+GnBackwardLaunch gn_backward_bf16(bool vec, int act);
+
 // dynamic shared memory of the row-pipeline kernels
 inline size_t tma_row_bytes(int64_t N, int es) { return size_t((N * es + 127) / 128 * 128); }
 inline size_t tma_ring_smem(int64_t N, int es, int nbuf) { return kTmaRingHeader + size_t(nbuf) * tma_row_bytes(N, es); }

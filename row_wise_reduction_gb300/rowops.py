@@ -38,6 +38,16 @@ __all__ = [
     "rowops_bias_residual_gelu",
     "rowops_rmsnorm",
     "rowops_fused_residual_rmsnorm",
+    "rowops_groupnorm_act",
+    "rowops_groupnorm_act_workspace_bytes",
+    "rowops_groupnorm_act_backward",
+    "rowops_groupnorm_act_backward_workspace_bytes",
+    "rowops_bias_dropout_residual",
+    "rowops_bias_dropout_residual_backward",
+    "rowops_bias_dropout_residual_backward_workspace_bytes",
+    "rowops_router_balance_loss",
+    "rowops_router_balance_loss_workspace_bytes",
+    "rowops_router_balance_loss_backward",
     "rowops_status_string",
     "rowops_reload_tuning",
     "ROWOPS_F32",
@@ -127,6 +137,23 @@ def library() -> ctypes.CDLL:
         L.rowops_layernorm_gelu_backward.restype = ctypes.c_int
         L.rowops_layernorm_gelu_backward.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _i64,
                                                      _i64, _i64, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
+        u64, size, i32, f32 = ctypes.c_uint64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+        for name, res, args in (
+            ("groupnorm_act_workspace_bytes", size, [_i64] * 4 + [i32]),
+            ("groupnorm_act", i32, [_vp] * 4 + [f32] + [_i64] * 5 + [i32, _vp, i32, _vp, size, _vp]),
+            ("groupnorm_act_backward_workspace_bytes", size, [_i64] * 4 + [i32]),
+            ("groupnorm_act_backward", i32, [_vp] * 8 + [_i64] * 5 + [i32, i32, _vp, size, _vp]),
+            ("bias_dropout_residual", i32, [_vp] * 4 + [f32, u64, u64, _vp] + [_i64] * 3 + [i32, _vp]),
+            ("bias_dropout_residual_backward_workspace_bytes", size, [_i64] * 2 + [i32]),
+            ("bias_dropout_residual_backward", i32,
+             [_vp] * 3 + [f32, u64, u64, _vp] + [_i64] * 3 + [i32, _vp, size, _vp]),
+            ("router_balance_loss_workspace_bytes", size, [_i64] * 2 + [i32]),
+            ("router_balance_loss", i32,
+             [_vp, _vp, i32, _vp, f32, _vp, _vp] + [_i64] * 4 + [i32, _vp, size, _vp]),
+            ("router_balance_loss_backward", i32, [_vp] * 4 + [f32, _vp] + [_i64] * 4 + [i32, _vp]),
+        ):
+            f = getattr(L, "rowops_" + name)
+            f.restype, f.argtypes = res, args
         _bind_calls(L)  # before _lib: a thread that sees _lib set finds _calls set too
         _lib = L
     return _lib
@@ -562,3 +589,337 @@ def rowops_gelu(x: torch.Tensor, y: Optional[torch.Tensor] = None, approximate: 
                                _dtype_code(x), _stream(stream))
     _check("rowops_gelu", st)
     return y
+
+
+# ---------------------------------------------------------------------------
+# Training operators: group norm + activation, bias + dropout + residual, the
+# router's balance loss. Their calls run on the device of their tensors, and
+# what they allocate is allocated on the stream that they run on.
+# ---------------------------------------------------------------------------
+def _elsewhere(fn, stream, dev, *args, **kwargs):
+    """``fn`` with the tensors' device and ``stream`` current."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            return fn(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, dev: int):
+    """(tensor, pointer, bytes) of a workspace of at least ``need`` bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the call's tensors")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+_ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def _act(act: str) -> int:
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError('act must be "none", "silu", "gelu" or "gelu_tanh"')
+    return code
+
+
+def _positions(x: torch.Tensor, name: str):
+    """(B, S, C, ld) of a channels-last (B, S, C) CUDA tensor whose B * S
+    positions are one stride apart."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be 3-D (samples, positions, channels)")
+    B, S, C = x.shape
+    sb, ss, sc = x.stride()
+    if C > 1 and sc != 1:
+        raise ValueError(f"{name} must have unit channel stride")
+    ld = ss if S > 1 else sb if B > 1 else max(C, ss)
+    if B > 1 and S > 0 and sb != S * ld:
+        raise ValueError(f"{name}'s samples must follow one another at the stride of its positions")
+    return B, S, C, ld
+
+
+def _like_positions(x: torch.Tensor, ld: int, t: Optional[torch.Tensor], name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty_strided(x.shape, (x.shape[1] * ld, ld, 1), dtype=x.dtype, device=x.device)
+    if t.dtype is not x.dtype or t.get_device() != x.get_device() or t.shape != x.shape:
+        raise ValueError(f"{name} must match x in shape, dtype and device")
+    if x.shape[0] * x.shape[1] > 1 and _positions(t, name)[3] != ld:
+        raise ValueError(f"x and {name} must share the stride of their positions")
+    return t
+
+
+def _floats(t: Optional[torch.Tensor], n: int, dev: int, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(n, dtype=torch.float32, device=dev)
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {n} entries")
+    return t
+
+
+def _group_stats(stats: torch.Tensor, B: int, groups: int, dev: int) -> int:
+    if (stats.dtype is not torch.float32 or stats.numel() != 2 * B * groups or not stats.is_contiguous()
+            or stats.get_device() != dev):
+        raise ValueError("stats must be a contiguous float32 CUDA tensor of shape (B, groups, 2)")
+    return stats.data_ptr()
+
+
+def rowops_groupnorm_act_workspace_bytes(B: int, S: int, C: int, groups: int, dtype: torch.dtype) -> int:
+    return int(library().rowops_groupnorm_act_workspace_bytes(B, S, C, groups, _DTYPE_CODES.get(dtype, -1)))
+
+
+def rowops_groupnorm_act(
+    x: torch.Tensor,
+    groups: int,
+    w: Optional[torch.Tensor] = None,
+    b: Optional[torch.Tensor] = None,
+    eps: float = 1e-5,
+    act: str = "silu",
+    y: Optional[torch.Tensor] = None,
+    stats: Optional[torch.Tensor] = None,
+    *,
+    workspace: Optional[torch.Tensor] = None,
+    stream=None,
+) -> torch.Tensor:
+    """Group norm -> affine -> activation of channels-last ``x`` (B, S, C):
+    samples, positions, channels (a channels-last image tensor of shape (B, C,
+    H, W) is ``t.permute(0, 2, 3, 1).flatten(1, 2)``). ``act``: "none", "silu",
+    "gelu" (exact) or "gelu_tanh". ``stats``: a float32 (B, groups, 2) tensor that
+    takes (mean, rstd) for the backward pass. ``workspace``: a CUDA tensor of at
+    least ``rowops_groupnorm_act_workspace_bytes(...)`` bytes, allocated per call
+    when omitted."""
+    dev = x.get_device()
+    if stream is not None or (dev >= 0 and dev != _current_device()):
+        return _elsewhere(rowops_groupnorm_act, stream, dev, x, groups, w, b, eps, act, y, stats, workspace=workspace)
+    B, S, C, ld = _positions(x, "x")
+    code = _dtype_code(x)
+    y = _like_positions(x, ld, y, "y")
+    L = _lib or library()
+    ws, wp, wn = _scratch(workspace, L.rowops_groupnorm_act_workspace_bytes(B, S, C, groups, code), dev)
+    st = L.rowops_groupnorm_act(
+        x.data_ptr(), y.data_ptr(), _affine(w, x, C, dev, "w"), _affine(b, x, C, dev, "b"), eps, B, S, C, groups, ld,
+        _act(act), None if stats is None else _group_stats(stats, B, groups, dev), code, wp, wn,
+        _current_raw_stream(dev))
+    _check("rowops_groupnorm_act", st)
+    return y
+
+
+def rowops_groupnorm_act_backward_workspace_bytes(B: int, S: int, C: int, groups: int, dtype: torch.dtype) -> int:
+    return int(library().rowops_groupnorm_act_backward_workspace_bytes(B, S, C, groups, _DTYPE_CODES.get(dtype, -1)))
+
+
+def rowops_groupnorm_act_backward(
+    x: torch.Tensor,
+    dy: torch.Tensor,
+    stats: torch.Tensor,
+    groups: int,
+    w: Optional[torch.Tensor] = None,
+    b: Optional[torch.Tensor] = None,
+    act: str = "silu",
+    dx: Optional[torch.Tensor] = None,
+    dw: Optional[torch.Tensor] = None,
+    db: Optional[torch.Tensor] = None,
+    *,
+    workspace: Optional[torch.Tensor] = None,
+    stream=None,
+):
+    """Gradients of rowops_groupnorm_act for the upstream gradient ``dy`` and the
+    ``stats`` that the forward call wrote: ``(dx, dw, db)``, dx as x, dw and db
+    float32 (C,)."""
+    dev = x.get_device()
+    if stream is not None or (dev >= 0 and dev != _current_device()):
+        return _elsewhere(rowops_groupnorm_act_backward, stream, dev, x, dy, stats, groups, w, b, act, dx, dw, db,
+                          workspace=workspace)
+    B, S, C, ld = _positions(x, "x")
+    code = _dtype_code(x)
+    _like_positions(x, ld, dy, "dy")
+    dx = _like_positions(x, ld, dx, "dx")
+    dw = _floats(dw, C, dev, "dw")
+    db = _floats(db, C, dev, "db")
+    L = _lib or library()
+    ws, wp, wn = _scratch(workspace, L.rowops_groupnorm_act_backward_workspace_bytes(B, S, C, groups, code), dev)
+    st = L.rowops_groupnorm_act_backward(
+        x.data_ptr(), dy.data_ptr(), _affine(w, x, C, dev, "w"), _affine(b, x, C, dev, "b"),
+        _group_stats(stats, B, groups, dev), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), B, S, C, groups, ld,
+        _act(act), code, wp, wn, _current_raw_stream(dev))
+    _check("rowops_groupnorm_act_backward", st)
+    return dx, dw, db
+
+
+_U64 = (1 << 64) - 1
+
+
+def _device_offset(t: Optional[torch.Tensor], dev: int):
+    if t is None:
+        return None
+    if t.dtype is not torch.int64 or t.numel() != 1 or t.get_device() != dev:
+        raise ValueError("device_offset must be an int64 CUDA tensor of one entry")
+    return t.data_ptr()
+
+
+def rowops_bias_dropout_residual(
+    x: torch.Tensor,
+    residual: Optional[torch.Tensor] = None,
+    bias: Optional[torch.Tensor] = None,
+    p: float = 0.1,
+    seed: int = 0,
+    offset: int = 0,
+    y: Optional[torch.Tensor] = None,
+    *,
+    device_offset: Optional[torch.Tensor] = None,
+    stream=None,
+) -> torch.Tensor:
+    """y = residual + dropout(x + bias, p) for every row of ``x`` (bias per
+    column; residual laid out like x; either may be None). The mask is a function
+    of (seed, offset) and the position, never stored: give each call an
+    ``offset`` of its own and the backward pass the same one. ``device_offset``:
+    an int64 tensor of one entry that is added to ``offset`` when the kernel
+    runs, so that a captured graph replays with new masks."""
+    dev = x.get_device()
+    if stream is not None or (dev >= 0 and dev != _current_device()):
+        return _elsewhere(rowops_bias_dropout_residual, stream, dev, x, residual, bias, p, seed, offset, y,
+                          device_offset=device_offset)
+    M, N, ld, y, code, dev = _xy(x, y)
+    if residual is not None:
+        _out_like(x, residual)  # same shape, dtype, device and row stride
+    st = (_lib or library()).rowops_bias_dropout_residual(
+        x.data_ptr(), None if residual is None else residual.data_ptr(), _affine(bias, x, N, dev, "bias"),
+        y.data_ptr(), p, seed & _U64, offset & _U64, _device_offset(device_offset, dev), M, N, ld, code,
+        _current_raw_stream(dev))
+    _check("rowops_bias_dropout_residual", st)
+    return y
+
+
+def rowops_bias_dropout_residual_backward_workspace_bytes(M: int, N: int, dtype: torch.dtype) -> int:
+    return int(library().rowops_bias_dropout_residual_backward_workspace_bytes(M, N, _DTYPE_CODES.get(dtype, -1)))
+
+
+def rowops_bias_dropout_residual_backward(
+    dy: torch.Tensor,
+    p: float = 0.1,
+    seed: int = 0,
+    offset: int = 0,
+    dx: Optional[torch.Tensor] = None,
+    dbias: Optional[torch.Tensor] = None,
+    bias_grad: bool = True,
+    *,
+    device_offset: Optional[torch.Tensor] = None,
+    workspace: Optional[torch.Tensor] = None,
+    stream=None,
+):
+    """Gradients of rowops_bias_dropout_residual for the upstream gradient ``dy``
+    and the forward call's p, seed and offsets: ``(dx, dbias)``, dx as dy (and
+    may be ``dy``), dbias float32 (N,), or None without ``bias_grad``. The
+    residual's gradient is dy itself."""
+    dev = dy.get_device()
+    if stream is not None or (dev >= 0 and dev != _current_device()):
+        return _elsewhere(rowops_bias_dropout_residual_backward, stream, dev, dy, p, seed, offset, dx, dbias,
+                          bias_grad, device_offset=device_offset, workspace=workspace)
+    M, N, ld, dx, code, dev = _xy(dy, dx)
+    L = _lib or library()
+    ws, wp, wn = None, None, 0
+    if bias_grad:
+        dbias = _floats(dbias, N, dev, "dbias")
+        need = L.rowops_bias_dropout_residual_backward_workspace_bytes(M, N, code)
+        ws, wp, wn = _scratch(workspace, need, dev)
+    elif dbias is not None:
+        raise ValueError("dbias is given but bias_grad is false")
+    st = L.rowops_bias_dropout_residual_backward(
+        dy.data_ptr(), dx.data_ptr(), None if dbias is None else dbias.data_ptr(), p, seed & _U64, offset & _U64,
+        _device_offset(device_offset, dev), M, N, ld, code, wp, wn, _current_raw_stream(dev))
+    _check("rowops_bias_dropout_residual_backward", st)
+    return dx, dbias
+
+
+def rowops_router_balance_loss_workspace_bytes(T: int, E: int, dtype: torch.dtype) -> int:
+    return int(library().rowops_router_balance_loss_workspace_bytes(T, E, _DTYPE_CODES.get(dtype, -1)))
+
+
+def _row_mask(mask: Optional[torch.Tensor], T: int, dev: int):
+    if mask is None:
+        return None
+    if (mask.dtype not in (torch.bool, torch.uint8) or mask.numel() != T or not mask.is_contiguous()
+            or mask.get_device() != dev):
+        raise ValueError("mask must be a contiguous bool or uint8 CUDA tensor of one entry a row")
+    return mask.data_ptr()
+
+
+def _counts(counts: Optional[torch.Tensor], E: int, dev: int) -> torch.Tensor:
+    if counts is None:
+        return torch.empty(E + 1, dtype=torch.int64, device=dev)
+    if (counts.dtype is not torch.int64 or counts.numel() != E + 1 or not counts.is_contiguous()
+            or counts.get_device() != dev):
+        raise ValueError("counts must be a contiguous int64 CUDA tensor of E + 1 entries")
+    return counts
+
+
+def rowops_router_balance_loss(
+    logits: torch.Tensor,
+    experts: torch.Tensor,
+    coef: float = 0.01,
+    mask: Optional[torch.Tensor] = None,
+    loss: Optional[torch.Tensor] = None,
+    counts: Optional[torch.Tensor] = None,
+    *,
+    workspace: Optional[torch.Tensor] = None,
+    stream=None,
+):
+    """Balance loss of a router from its ``logits`` (T, E) and the chosen
+    ``experts`` (T, K) (int32 or int64): ``(loss, counts)``, loss float32 (1,),
+    counts int64 (E + 1,): the experts' counts and, last, the rows that took
+    part. ``mask``: bool or uint8 (T,), rows with 0 take no part."""
+    dev = logits.get_device()
+    if stream is not None or (dev >= 0 and dev != _current_device()):
+        return _elsewhere(rowops_router_balance_loss, stream, dev, logits, experts, coef, mask, loss, counts,
+                          workspace=workspace)
+    T, E, ld = _rows(logits, "logits")
+    code = _dtype_code(logits)
+    if experts.dim() != 2 or experts.shape[0] != T or not experts.is_contiguous() or experts.get_device() != dev:
+        raise ValueError("experts must be a contiguous (T, K) tensor on the device of the logits")
+    width = {torch.int64: 8, torch.int32: 4}.get(experts.dtype)
+    if width is None:
+        raise TypeError(f"experts must be int32 or int64, not {experts.dtype}")
+    loss = _floats(loss, 1, dev, "loss")
+    counts = _counts(counts, E, dev)
+    L = _lib or library()
+    ws, wp, wn = _scratch(workspace, L.rowops_router_balance_loss_workspace_bytes(T, E, code), dev)
+    st = L.rowops_router_balance_loss(
+        logits.data_ptr(), experts.data_ptr(), width, _row_mask(mask, T, dev), coef, loss.data_ptr(),
+        counts.data_ptr(), T, E, experts.shape[1], ld, code, wp, wn, _current_raw_stream(dev))
+    _check("rowops_router_balance_loss", st)
+    return loss, counts
+
+
+def rowops_router_balance_loss_backward(
+    logits: torch.Tensor,
+    counts: torch.Tensor,
+    top_k: int,
+    dloss: torch.Tensor,
+    coef: float = 0.01,
+    mask: Optional[torch.Tensor] = None,
+    dlogits: Optional[torch.Tensor] = None,
+    *,
+    stream=None,
+) -> torch.Tensor:
+    """Gradient of rowops_router_balance_loss with respect to the logits, for the
+    forward call's ``counts``, coef and mask, the choices per row ``top_k`` and
+    the loss's own gradient ``dloss`` (float32, one entry, on the GPU).
+    ``dlogits`` may be ``logits``."""
+    dev = logits.get_device()
+    if stream is not None or (dev >= 0 and dev != _current_device()):
+        return _elsewhere(rowops_router_balance_loss_backward, stream, dev, logits, counts, top_k, dloss, coef, mask,
+                          dlogits)
+    T, E, ld, dlogits, code, dev = _xy(logits, dlogits)
+    if dloss.dtype is not torch.float32 or dloss.numel() != 1 or dloss.get_device() != dev:
+        raise ValueError("dloss must be a float32 CUDA tensor of one entry")
+    st = (_lib or library()).rowops_router_balance_loss_backward(
+        logits.data_ptr(), _counts(counts, E, dev).data_ptr(), dloss.data_ptr(), _row_mask(mask, T, dev), coef,
+        dlogits.data_ptr(), T, E, top_k, ld, code, _current_raw_stream(dev))
+    _check("rowops_router_balance_loss_backward", st)
+    return dlogits
