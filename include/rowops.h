@@ -74,6 +74,9 @@
  *                                 two row groups of 256 threads, or four of 128, covers a row
  *                                 with at most 32 columns a thread) or in registers (one row
  *                                 group of up to 1024 threads per CTA)
+ *   ROWOPS_GROUPNORM=fused|two_pass  group norm and its backward: one kernel that holds a sample's
+ *                                 groups in the shared memory of a cluster wherever they fit, or
+ *                                 two passes (default: whichever a model of the time prefers)
  *   ROWOPS_WAIT_LIMIT_NS=<ns>     limit of every device-side wait (default 2 s)
  *   ROWOPS_TEST_STALL_ROW=<row>   test hook for the timeout path: the wait that concerns this
  *                                 row is made to run out (the row pipeline's bulk copy of it is
@@ -430,8 +433,8 @@ rowops_status_t rowops_fused_residual_rmsnorm(const void* x, const void* residua
  *           group, for the backward pass; apart from x, y, w, b and the workspace.
  *   workspace, workspace_bytes   device memory, 256-byte aligned, at least
  *           rowops_groupnorm_act_workspace_bytes(B, S, C, G, dtype) bytes
- *           (overwritten), apart from the other tensors; calls sharing it must be
- *           ordered on one stream.
+ *           (overwritten; 0 where one kernel does it: NULL will do), apart from the
+ *           other tensors; calls sharing it must be ordered on one stream.
  * C is at most 8192 (ROWOPS_ERR_UNSUPPORTED beyond) and a multiple of G. B == 0
  * or S == 0 is a no-op. A NaN or an infinity in a group makes that group of that
  * sample NaN. The variance is merged from centred partial sums, so a mean far

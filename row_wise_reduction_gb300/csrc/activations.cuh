@@ -51,4 +51,64 @@ __device__ __forceinline__ float act_grad(float z) {
     }
 }
 
+// Pairs, with packed arithmetic.
+//
+// e = 2^a and q = 1 / (1 + e) of two values from one reciprocal, that of the
+// product (1 + e_x) (1 + e_y). a is kept to 60, so the product stays finite and
+// q at 2^-60 where it is smaller: what is built from q, z q or z q (1 - q), is
+// then off by at most |z| 2^-60. One and a half special-function results a value
+// instead of two, which an SM makes 16 of a cycle: a pass that reads from L2 and
+// the backward pass, which evaluates the slope twice, would be bound by them.
+__device__ __forceinline__ float2 sigmoids2(float2 a, float2& e) {
+    e = make_float2(ex2_approx(fminf(a.x, 60.f)), ex2_approx(fminf(a.y, 60.f)));
+    const float2 d = f2_add(e, f2(1.f));
+    const float r = rcp_approx(d.x * d.y);
+    return f2_mul(make_float2(d.y, d.x), f2(r));
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_of2(float2 z) {
+    if constexpr (ACT == ROWOPS_ACT_SILU) {
+        float2 e;
+        return f2_mul(z, sigmoids2(f2_mul(z, f2(-kLog2eF)), e));
+    } else if constexpr (ACT == ROWOPS_ACT_GELU) {
+        return gelu_erf2(z);
+    } else if constexpr (ACT == ROWOPS_ACT_GELU_TANH) {
+        return gelu_tanh_approx2(z);
+    } else {
+        return z;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_grad2(float2 z) {
+    if constexpr (ACT == ROWOPS_ACT_SILU) {
+        float2 e;
+        const float2 q = sigmoids2(f2_mul(z, f2(-kLog2eF)), e);
+        return f2_fma(f2_mul(z, q), f2_mul(e, q), q);
+    } else if constexpr (ACT == ROWOPS_ACT_GELU) {
+        using F = GeluErfFit;
+        const float2 z2 = f2_mul(z, z);
+        float2 p = f2_fma(z2, f2(F::q6), f2(F::q5));
+        p = f2_fma(z2, p, f2(F::q4));
+        p = f2_fma(z2, p, f2(F::q3));
+        p = f2_fma(z2, p, f2(F::q2));
+        p = f2_fma(z2, p, f2(F::q1));
+        p = f2_fma(z2, p, f2(F::q0));
+        const float2 h = f2_mul(z2, f2(-0.5f * kLog2eF));
+        const float2 phi = f2_mul(make_float2(ex2_approx(h.x), ex2_approx(h.y)), f2(0.3989422804014327f));
+        float2 e;
+        return f2_fma(z, phi, sigmoids2(f2_mul(p, z), e));
+    } else if constexpr (ACT == ROWOPS_ACT_GELU_TANH) {
+        constexpr float c0 = float(-2.0 * 0.79788456 * kLog2e), c1 = float(-2.0 * 0.79788456 * 0.044715 * kLog2e);
+        constexpr float d0 = float(2.0 * 0.79788456), d1 = float(6.0 * 0.79788456 * 0.044715);
+        const float2 z2 = f2_mul(z, z);
+        float2 e;
+        const float2 q = sigmoids2(f2_mul(f2_fma(z2, f2(c1), f2(c0)), z), e);
+        return f2_fma(f2_mul(f2_mul(e, q), q), f2_mul(z, f2_fma(z2, f2(d1), f2(d0))), q);
+    } else {
+        return f2(1.f);
+    }
+}
+
 }  // namespace rowops

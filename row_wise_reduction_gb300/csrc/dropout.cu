@@ -196,11 +196,7 @@ cudaError_t launch(const void* x, const void* r, const void* b, void* y, float* 
     kern<<<dim3(unsigned(gx), unsigned(gy)), kWarps * 32, 0, cfg.stream>>>(
         static_cast<const T*>(x), static_cast<const T*>(r), static_cast<const T*>(b), static_cast<T*>(y), part, a);
     cudaError_t e = cudaGetLastError();
-    if (SUM && e == cudaSuccess) {
-        column_partials_kernel<<<unsigned((a.N + 31) / 32), dim3(32, 32), 0, cfg.stream>>>(part, int(gy), a.N, a.N,
-                                                                                          db);
-        e = cudaGetLastError();
-    }
+    if (SUM && e == cudaSuccess) e = reduce_partials(part, gy, a.N, a.N, db, nullptr, cfg);
     return e;
 }
 

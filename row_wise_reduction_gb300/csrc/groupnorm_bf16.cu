@@ -1,5 +1,5 @@
 // Group norm + activation and its backward, bf16.
-#include "groupnorm_kernels.cuh"
+#include "groupnorm_inst.cuh"
 
 namespace rowops {
 GnForwardLaunch gn_forward_bf16(bool vec, int act) { return gn_forward_table<bf16_t>(vec, act); }

@@ -1,5 +1,5 @@
 // Group norm + activation and its backward, fp32.
-#include "groupnorm_kernels.cuh"
+#include "groupnorm_inst.cuh"
 
 namespace rowops {
 GnForwardLaunch gn_forward_f32(bool vec, int act) { return gn_forward_table<float>(vec, act); }

@@ -1,0 +1,430 @@
+// Group norm + activation and its backward in one kernel that reads every
+// tensor once: a cluster of CTAs holds a slab -- a sample's positions of a block
+// of whole groups -- in shared memory between the two passes. CTA `rank` of
+// the cluster takes positions [rank R, (rank + 1) R).
+//
+// Vectors: the slab comes in as boxes of rows by tensor copies (a block of groups
+// is often narrower than a row, 80 to 640 bytes of it, which costs per-thread
+// copies and stores several times the instructions and shared-memory wavefronts
+// that it moves data with), is worked on box by box as it arrives, and the
+// results go out the same way from the same boxes. Rows that are no whole vectors
+// come and go by single elements.
+//
+// The exchange: every CTA writes its groups' sums into the shared memory of
+// all CTAs of the cluster and then meets them at one cluster barrier; each adds
+// up what it got in order of rank. Sums are joined as (mean, squares about it) about
+// one of their own members, so no more than the count of members cancels.
+#pragma once
+
+#include "groupnorm_kernels.cuh"
+#include "row_pipeline.cuh"
+
+namespace rowops {
+
+__device__ __forceinline__ void tensor_load(void* dst, const RowsMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tensor_store(const RowsMap* map, int x, int y, const void* src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(smem_addr(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tensor_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// What a thread of the fused kernels works on.
+template <typename T, int VEC>
+struct GnTile {
+    using V = Vec<T, VEC>;
+    int rank, block, t, tx, ty;
+    int64_t sample;
+    int rows;        // positions of the CTA
+    int64_t at;      // element offset of the thread's channels at the CTA's first position
+    bool active, in;
+    __device__ __forceinline__ GnTile(const GnArgs& a, const GnFused& f) {
+        rank = int(blockIdx.x) & (f.cluster - 1);
+        block = int(blockIdx.x) >> f.cluster_log2;
+        sample = int64_t(blockIdx.z) * gridDim.y + blockIdx.y;
+        in = sample < a.B;
+        t = threadIdx.x;
+        ty = t * f.inv_tx >> 16;
+        tx = t - ty * f.tx;
+        active = ty < f.ty;
+        const int64_t r0 = int64_t(rank) * f.rows, left = a.S - r0;
+        rows = int(left < f.rows ? (left > 0 ? left : 0) : f.rows);
+        at = (sample * a.S + r0) * a.ld + int64_t(block) * f.W + tx * VEC;
+    }
+    // f(word in the tile at `tile`, position) over the thread's positions of box q
+    template <typename F>
+    __device__ __forceinline__ void box(const GnFused& f, int q, F g) const {
+        if (!active) return;
+        const int r0 = q * f.box, n = min(f.box, rows - r0);
+#pragma unroll 4
+        for (int i = ty; i < n; i += f.ty) g(q * f.pitch + i * f.tx + tx, r0 + i);
+    }
+};
+
+// Copies in: thread 0 asks for every box of every tensor, each box on its own barrier.
+template <typename T, int VEC, int N>
+__device__ __forceinline__ void gn_fetch(const GnTile<T, VEC>& k, const GnArgs& a, const GnFused& f,
+                                         const RowsMap* const (&maps)[N], const T* const (&from)[N],
+                                         typename Vec<T, VEC>::Word* tile, uint64_t* bars, bool stall) {
+    if constexpr (VEC > 1) {
+        if (k.t == 0) {
+            for (int q = 0; q < f.boxes; ++q) mbar_init(&bars[q], 1);
+            mbar_init_fence();
+            const int x = k.block * f.W * int(sizeof(T)) / 8, y = int(k.sample * a.S) + k.rank * f.rows;
+            for (int q = 0; q * f.box < k.rows; ++q) {
+                mbar_expect_tx(&bars[q], unsigned(N * f.box * f.W * sizeof(T)) + (stall && q == 0 ? 16u : 0u));
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    tensor_load(tile + (i * f.boxes + q) * f.pitch, maps[i], x, y + q * f.box, &bars[q]);
+            }
+        }
+    } else {
+        if (k.active) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll 8
+                for (int r = k.ty; r < k.rows; r += f.ty)
+                    tile[i * f.pitch + r * f.tx + k.tx] = from[i][k.at + r * a.ld];
+        }
+    }
+}
+
+// Box q's wait; false where it ran out.
+template <int VEC>
+__device__ __forceinline__ bool gn_arrived(uint64_t* bars, int q, unsigned long long wait_ns) {
+    if constexpr (VEC > 1) return mbar_wait(&bars[q], 0, wait_ns);
+    else return true;
+}
+
+// Sums over `lanes` consecutive lanes (a power of two).
+__device__ __forceinline__ float2 lanes_sum(float2 s, int lanes) {
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    }
+    return s;
+}
+
+// f(item, lane of its team) for items shared out to teams of `team` lanes, the whole
+// CTA in step (f holds shuffles); items at or past n: live is false.
+template <typename F>
+__device__ __forceinline__ void by_teams(int n, int team_log2, F f) {
+    for (int i0 = 0; i0 < n << team_log2; i0 += kGnBlock) {
+        const int i = i0 + int(threadIdx.x), item = i >> team_log2;
+        f(item < n ? item : 0, i & ((1 << team_log2) - 1), item < n);
+    }
+}
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnBlock, 3)
+    gn_fused_kernel(const __grid_constant__ RowsMap mx, const __grid_constant__ RowsMap my, const T* x, T* y,
+                    const T* w, const T* b, float2* stats_out, const __grid_constant__ GnArgs a,
+                    const __grid_constant__ GnFused f, unsigned* err, unsigned long long wait_ns, int64_t stall_row) {
+    using V = Vec<T, VEC>;
+    constexpr int P = V::P;
+    extern __shared__ __align__(128) char smem[];
+    const cg::cluster_group cl = cg::this_cluster();
+    const GnTile<T, VEC> k(a, f);
+    if (!k.in) return;  // the whole cluster's sample
+    if (f.cluster > 1) cl.barrier_arrive();  // met before the first write to another CTA
+    const int Gb = f.W / a.L;
+    typename V::Word* tile = reinterpret_cast<typename V::Word*>(smem);
+    float* pm = reinterpret_cast<float*>(smem + f.tile);      // [ty][W] the threads' means
+    float* pq = pm + f.ty * f.W;                              // [ty][W] and squares
+    float2* col = reinterpret_cast<float2*>(pq + f.ty * f.W);  // [W] the channels'
+    float2* gs = col + f.W;                                   // [Gb] mean, rstd
+    float2* got = gs + Gb;                                    // [cluster][Gb]: every CTA's mean, squares
+    uint64_t* bars = reinterpret_cast<uint64_t*>(got + f.cluster * Gb);  // [boxes]
+    float* count = reinterpret_cast<float*>(bars + f.boxes);  // [ty] positions of the threads
+    const RowsMap* const maps[1] = {&mx};
+    const T* const from[1] = {x};
+    const int64_t r0 = k.sample * a.S + int64_t(k.rank) * f.rows;
+    gn_fetch<T, VEC, 1>(k, a, f, maps, from, tile, bars, stall_row >= r0 && stall_row < r0 + k.rows);
+    const int c = k.tx * VEC, cb = k.block * f.W + c;
+    float2 mul[P], shift[P];
+    if (k.active) {
+        load_affine<T, VEC>(w, cb, 1.f, mul);
+        load_affine<T, VEC>(b, cb, 0.f, shift);
+    }
+    __syncthreads();  // the barriers are set up
+
+    Shifted<P> sums;
+    sums.clear();
+    int n = 0;
+    bool fail = false;
+    for (int q = 0; q * f.box < k.rows; ++q) {
+        fail |= !gn_arrived<VEC>(bars, q, wait_ns);
+        if (q == 0 && k.active && k.ty < k.rows) {
+            float2 v[P];
+            V::get(tile[k.ty * f.tx + k.tx], v);
+            sums.start(v);
+        }
+        k.box(f, q, [&](int at, int) {
+            float2 v[P];
+            V::get(tile[at], v);
+            sums.add(v);
+            ++n;
+        });
+    }
+    if (k.active) {
+        sums.template leave<VEC>(n, pm + k.ty * f.W + c, pq + k.ty * f.W + c);
+        if (k.tx == 0) count[k.ty] = float(n);
+    }
+    fail = __syncthreads_or(fail);
+    // the channels: means and squares about them, about the first thread's mean
+    const float inv_rows = k.rows ? 1.f / float(k.rows) : 0.f;
+    by_teams(f.W, f.parts_log2, [&](int ch, int lane, bool live) {
+        const float ref = pm[ch];
+        float2 s = f2(0.f);
+        for (int r = lane; r < f.ty; r += 1 << f.parts_log2) {
+            const float m = count[r], d = pm[r * f.W + ch] - ref;
+            s.x = fmaf(m, d, s.x);
+            s.y += fmaf(m * d, d, pq[r * f.W + ch]);
+        }
+        s = lanes_sum(s, 1 << f.parts_log2);
+        const float off = s.x * inv_rows, q = fmaf(-s.x, off, s.y);
+        if (live && lane == 0) col[ch] = make_float2(ref + off, q < 0.f ? 0.f : q);
+    });
+    __syncthreads();
+    if (f.cluster > 1) cl.barrier_wait();
+    by_teams(Gb, f.team_log2, [&](int g, int lane, bool live) {
+        const float2* cg_ = col + g * a.L;
+        const float ref = cg_[0].x, m = float(k.rows);
+        float2 s = f2(0.f);
+        for (int i = lane; i < a.L; i += 1 << f.team_log2) {
+            const float d = cg_[i].x - ref;
+            s.x += d;
+            s.y += fmaf(m * d, d, cg_[i].y);
+        }
+        s = lanes_sum(s, 1 << f.team_log2);
+        const float off = s.x * a.inv_L, q = fmaf(-m * s.x, off, s.y);
+        const float2 mine = k.rows ? make_float2(ref + off, q < 0.f ? 0.f : q) : f2(0.f);
+        if (live)
+            for (int r = lane; r < f.cluster; r += 1 << f.team_log2)
+                *in_cta(cl, &got[k.rank * Gb + g], r, f.cluster) = mine;
+    });
+    if (f.cluster > 1) cl.sync();
+    else __syncthreads();
+    by_teams(Gb, f.cluster_log2, [&](int g, int r, bool live) {
+        const int64_t left = a.S - int64_t(r) * f.rows;
+        const float m = float(left < f.rows ? (left > 0 ? left : 0) : f.rows);
+        const float ref = got[g].x;
+        const float2 v = got[r * Gb + g];
+        const float d = v.x - ref;
+        const float2 s = lanes_sum(make_float2(m * d, fmaf(m * float(a.L) * d, d, v.y)), f.cluster);
+        const float off = s.x * a.inv_S, q = fmaf(-float(a.L) * s.x, off, s.y);
+        if (live && r == 0) {
+            gs[g] = make_float2(ref + off, rsqrtf((q < 0.f ? 0.f : q) * a.inv_m + a.eps));
+            if (stats_out && k.rank == 0) stats_out[k.sample * a.G + k.block * Gb + g] = gs[g];
+        }
+    });
+    __syncthreads();
+    float2 mean[P];
+    if (k.active) {
+        const Groups<VEC> g(c, a);
+        float2 rstd[P];
+        each_channel<VEC>(mean, [&](int e) { return -gs[g.g[e]].x; });
+        each_channel<VEC>(rstd, [&](int e) { return gs[g.g[e]].y; });
+#pragma unroll
+        for (int j = 0; j < P; ++j) mul[j] = f2_mul(mul[j], rstd[j]);
+    }
+    T* py = y + k.at;
+    for (int q = 0; q * f.box < k.rows; ++q) {
+        const bool whole = VEC > 1 && (q + 1) * f.box <= k.rows;  // goes out as a box
+        k.box(f, q, [&](int at, int r) {
+            float2 v[P];
+            V::get(tile[at], v);
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] = act_of2<ACT>(f2_fma(f2_add(v[j], mean[j]), mul[j], shift[j]));
+            if (whole) V::keep(&tile[at], v);
+            else if (!fail) V::put(py + r * a.ld, v);
+        });
+        if (whole) {
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (k.t == 0 && !fail)
+                tensor_store(&my, k.block * f.W * int(sizeof(T)) / 8, int(k.sample * a.S) + k.rank * f.rows + q * f.box,
+                             tile + q * f.pitch);
+        }
+    }
+    if (VEC > 1 && k.t == 0) {
+        tensor_stores_read();
+        if (fail) {
+            atomicExch(err, kDeviceErrTimeout);
+            for (int q = 0; q * f.box < k.rows; ++q) mbar_wait(&bars[q], 0, wait_ns);  // copies still in flight
+        }
+    }
+}
+
+// chan: a row of 2 C sums (dz xh, then dz) for every CTA of a sample.
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnBlock, 2)
+    gn_bwd_fused_kernel(const __grid_constant__ RowsMap mx, const __grid_constant__ RowsMap md,
+                        const __grid_constant__ RowsMap mo, const T* x, const T* dy, T* dx, const T* w, const T* b,
+                        const float2* stats, float* chan, const __grid_constant__ GnArgs a,
+                        const __grid_constant__ GnFused f, unsigned* err, unsigned long long wait_ns,
+                        int64_t stall_row) {
+    using E = Elem<T>;
+    using V = Vec<T, VEC>;
+    constexpr int P = V::P;
+    extern __shared__ __align__(128) char smem[];
+    const cg::cluster_group cl = cg::this_cluster();
+    const GnTile<T, VEC> k(a, f);
+    if (!k.in) return;
+    if (f.cluster > 1) cl.barrier_arrive();
+    const int Gb = f.W / a.L;
+    typename V::Word* tx = reinterpret_cast<typename V::Word*>(smem);
+    typename V::Word* td = tx + f.boxes * f.pitch;
+    float2* red = reinterpret_cast<float2*>(smem + f.tile);  // [ty][W]: the threads' A, Q
+    float2* col = red + f.ty * f.W;                          // [W]: the channels', times w
+    float2* gs = col + f.W;                                  // [Gb]: -c1, -c2
+    float2* got = gs + Gb;                                   // [cluster][Gb]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(got + f.cluster * Gb);  // [boxes]
+    const RowsMap* const maps[2] = {&mx, &md};
+    const T* const from[2] = {x, dy};
+    const int64_t r0 = k.sample * a.S + int64_t(k.rank) * f.rows;
+    gn_fetch<T, VEC, 2>(k, a, f, maps, from, tx, bars, stall_row >= r0 && stall_row < r0 + k.rows);
+    const int c = k.tx * VEC, cb = k.block * f.W + c;
+    GnSlope<T, VEC, ACT> slope;
+    if (k.active) slope.load(w, b, stats + k.sample * a.G + k.block * Gb, c, cb, a);
+    __syncthreads();
+
+    float2 sa[P], sq[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) sa[j] = sq[j] = f2(0.f);
+    bool fail = false;
+    for (int q = 0; q * f.box < k.rows; ++q) {
+        fail |= !gn_arrived<VEC>(bars, q, wait_ns);
+        k.box(f, q, [&](int at, int) { slope.add(tx[at], td[at], sa, sq); });
+    }
+    if (k.active) slope.leave(sa, sq, red + k.ty * f.W + c);
+    fail = __syncthreads_or(fail);
+    float* cw = chan + (k.sample * f.cluster + k.rank) * 2 * a.C + k.block * f.W;
+    by_teams(f.W, f.parts_log2, [&](int ch, int lane, bool live) {
+        float2 s = f2(0.f);
+        for (int r = lane; r < f.ty; r += 1 << f.parts_log2) s = f2_add(s, red[r * f.W + ch]);
+        s = lanes_sum(s, 1 << f.parts_log2);
+        if (live && lane == 0) {
+            cw[ch] = s.y;
+            cw[a.C + ch] = s.x;
+            const float wv = w ? E::load(w + k.block * f.W + ch) : 1.f;
+            col[ch] = make_float2(wv * s.x, wv * s.y);
+        }
+    });
+    __syncthreads();
+    if (f.cluster > 1) cl.barrier_wait();
+    by_teams(Gb, f.team_log2, [&](int g, int lane, bool live) {
+        float2 s = f2(0.f);
+        for (int i = lane; i < a.L; i += 1 << f.team_log2) s = f2_add(s, col[g * a.L + i]);
+        s = lanes_sum(s, 1 << f.team_log2);
+        if (live)
+            for (int r = lane; r < f.cluster; r += 1 << f.team_log2)
+                *in_cta(cl, &got[k.rank * Gb + g], r, f.cluster) = s;
+    });
+    if (f.cluster > 1) cl.sync();
+    else __syncthreads();
+    by_teams(Gb, f.cluster_log2, [&](int g, int r, bool live) {
+        const float2 s = lanes_sum(got[r * Gb + g], f.cluster);
+        if (live && r == 0) gs[g] = make_float2(-s.x / a.m, -s.y / a.m);
+    });
+    __syncthreads();
+    if (k.active) slope.means(gs, c, a);
+    T* po = dx + k.at;
+    for (int q = 0; q * f.box < k.rows; ++q) {
+        const bool whole = VEC > 1 && (q + 1) * f.box <= k.rows;
+        k.box(f, q, [&](int at, int r) {
+            float2 v[P];
+            slope.of(tx[at], td[at], v);
+            if (whole) V::keep(&tx[at], v);
+            else if (!fail) V::put(po + r * a.ld, v);
+        });
+        if (whole) {
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (k.t == 0 && !fail)
+                tensor_store(&mo, k.block * f.W * int(sizeof(T)) / 8, int(k.sample * a.S) + k.rank * f.rows + q * f.box,
+                             tx + q * f.pitch);
+        }
+    }
+    if (VEC > 1 && k.t == 0) {
+        tensor_stores_read();
+        if (fail) {
+            atomicExch(err, kDeviceErrTimeout);
+            for (int q = 0; q * f.box < k.rows; ++q) mbar_wait(&bars[q], 0, wait_ns);
+        }
+    }
+}
+
+// ---- launchers -------------------------------------------------------------
+inline cudaError_t gn_cluster_launch(const void* kern, const GnFused& f, int64_t B, const LaunchCfg& cfg,
+                                     void** args) {
+    cudaError_t e = allow_smem(kern, f.smem, cfg);
+    if (e == cudaSuccess && f.cluster > 8)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    const unsigned by = unsigned(B < 32768 ? B : 32768);
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(f.blocks * f.cluster), by, unsigned((B + by - 1) / by));
+    lc.blockDim = dim3(kGnBlock);
+    lc.dynamicSmemBytes = f.smem;
+    lc.stream = cfg.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(f.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelExC(&lc, kern, args);
+}
+
+template <typename T, int VEC>
+cudaError_t gn_map(RowsMap* m, const void* p, const GnArgs& a, const GnFused& f) {
+    if (VEC == 1) return cudaSuccess;
+    return rows_map(m, p, a.C * int64_t(sizeof(T)), int64_t(a.B) * a.S, a.ld * int64_t(sizeof(T)),
+                    f.W * int(sizeof(T)), f.box);
+}
+
+template <typename T, int VEC, int ACT>
+cudaError_t gn_forward_fused(const void* x, void* y, const void* w, const void* b, float* stats, GnArgs a,
+                             const GnFused& f0, const LaunchCfg& cfg) {
+    auto kern = gn_fused_kernel<T, VEC, ACT>;
+    GnFused f = f0;
+    RowsMap mx, my;
+    cudaError_t e = gn_map<T, VEC>(&mx, x, a, f);
+    if (e == cudaSuccess) e = gn_map<T, VEC>(&my, y, a, f);
+    if (e != cudaSuccess) return e;
+    unsigned* err = cfg.dev_error;
+    unsigned long long wait_ns = cfg.wait_ns;
+    int64_t stall = cfg.stall_row;
+    void* args[] = {&mx, &my, &x, &y, &w, &b, &stats, &a, &f, &err, &wait_ns, &stall};
+    return gn_cluster_launch(reinterpret_cast<const void*>(kern), f, a.B, cfg, args);
+}
+
+template <typename T, int VEC, int ACT>
+cudaError_t gn_backward_fused(const void* x, const void* dy, const void* w, const void* b, const float* stats,
+                              void* dx, float* dw, float* db, void* ws, GnArgs a, const GnFused& f0,
+                              const LaunchCfg& cfg) {
+    auto kern = gn_bwd_fused_kernel<T, VEC, ACT>;
+    GnFused f = f0;
+    RowsMap mx, md, mo;
+    cudaError_t e = gn_map<T, VEC>(&mx, x, a, f);
+    if (e == cudaSuccess) e = gn_map<T, VEC>(&md, dy, a, f);
+    if (e == cudaSuccess) e = gn_map<T, VEC>(&mo, dx, a, f);
+    if (e != cudaSuccess) return e;
+    float* chan = static_cast<float*>(ws);
+    unsigned* err = cfg.dev_error;
+    unsigned long long wait_ns = cfg.wait_ns;
+    int64_t stall = cfg.stall_row;
+    void* args[] = {&mx, &md, &mo, &x, &dy, &dx, &w, &b, &stats, &chan, &a, &f, &err, &wait_ns, &stall};
+    e = gn_cluster_launch(reinterpret_cast<const void*>(kern), f, a.B, cfg, args);
+    return e == cudaSuccess ? gn_reduce_channels(chan, int64_t(a.B) * f.cluster, a.C, dw, db, cfg) : e;
+}
+
+}  // namespace rowops

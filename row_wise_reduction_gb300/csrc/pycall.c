@@ -12,6 +12,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
+#include <string.h>
 
 typedef int (*softmax_fn)(const void*, void*, int64_t, int64_t, int64_t, int, void*);
 typedef int (*ln_fn)(const void*, void*, const void*, const void*, float, int64_t, int64_t, int64_t, int, void*);
@@ -98,12 +99,136 @@ static PyObject* layernorm_gelu_erf(PyObject* self, PyObject* const* a, Py_ssize
     return ln_call(g_ln_erf, "layernorm_gelu_erf", a, n);
 }
 
+/*
+ * The training operators' entry points and workspace queries: the same
+ * marshalling, one function each.
+ */
+static int as_f32(PyObject* o, float* out) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) return -1;
+    *out = (float)v;
+    return 0;
+}
+
+static int as_u64(PyObject* o, uint64_t* out) {
+    *out = PyLong_AsUnsignedLongLongMask(o);
+    return (*out == (uint64_t)-1 && PyErr_Occurred()) ? -1 : 0;
+}
+
+#define MOST_ARGS 20
+typedef struct {
+    void* p[MOST_ARGS];
+    int64_t i[MOST_ARGS];
+    uint64_t u[MOST_ARGS];
+    float f[MOST_ARGS];
+} args_t;
+
+/* Arguments by a form: p pointer or None, i integer, u 64 bits (taken mod 2^64), f float; each
+ * lands at its own position of the array of its kind. */
+static int take(const char* name, const char* form, PyObject* const* a, Py_ssize_t n, args_t* v) {
+    Py_ssize_t k;
+    if (!nargs_ok(n, (Py_ssize_t)strlen(form), name)) return -1;
+    for (k = 0; k < n; ++k) {
+        int bad = form[k] == 'p' ? as_ptr(a[k], &v->p[k])
+                : form[k] == 'i' ? as_i64(a[k], &v->i[k])
+                : form[k] == 'u' ? as_u64(a[k], &v->u[k]) : as_f32(a[k], &v->f[k]);
+        if (bad) return -1;
+    }
+    return 0;
+}
+
+/* the addresses, in the order of bind_training's arguments */
+static void* g_training[9];
+
+typedef size_t (*gn_bytes_fn)(int64_t, int64_t, int64_t, int64_t, int);
+typedef size_t (*rows_bytes_fn)(int64_t, int64_t, int);
+typedef int (*gn_fn)(const void*, void*, const void*, const void*, float, int64_t, int64_t, int64_t, int64_t, int64_t,
+                     int, float*, int, void*, size_t, void*);
+typedef int (*gn_bwd_fn)(const void*, const void*, const void*, const void*, const float*, void*, float*, float*,
+                         int64_t, int64_t, int64_t, int64_t, int64_t, int, int, void*, size_t, void*);
+typedef int (*drop_fn)(const void*, const void*, const void*, void*, float, uint64_t, uint64_t, const void*, int64_t,
+                       int64_t, int64_t, int, void*);
+typedef int (*drop_bwd_fn)(const void*, void*, float*, float, uint64_t, uint64_t, const void*, int64_t, int64_t,
+                           int64_t, int, void*, size_t, void*);
+typedef int (*balance_fn)(const void*, const void*, int, const void*, float, float*, void*, int64_t, int64_t, int64_t,
+                          int64_t, int, void*, size_t, void*);
+typedef int (*balance_bwd_fn)(const void*, const void*, const float*, const void*, float, void*, int64_t, int64_t,
+                              int64_t, int64_t, int, void*);
+
+static PyObject* bind_training(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    int k;
+    (void)self;
+    if (!nargs_ok(n, 9, "bind_training")) return NULL;
+    for (k = 0; k < 9; ++k)
+        if (as_ptr(a[k], &g_training[k])) return NULL;
+    Py_RETURN_NONE;
+}
+
+#define CALL(name, slot, form, expr)                                                                          \
+    static PyObject* name(PyObject* self, PyObject* const* a, Py_ssize_t n) {                                 \
+        args_t v;                                                                                             \
+        int r;                                                                                                \
+        (void)self;                                                                                           \
+        if (!g_training[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");          \
+        if (take(#name, form, a, n, &v)) return NULL;                                                         \
+        Py_BEGIN_ALLOW_THREADS                                                                                \
+        r = (expr);                                                                                           \
+        Py_END_ALLOW_THREADS                                                                                  \
+        return PyLong_FromLong(r);                                                                            \
+    }
+#define BYTES(name, slot, form, expr)                                                                         \
+    static PyObject* name(PyObject* self, PyObject* const* a, Py_ssize_t n) {                                 \
+        args_t v;                                                                                             \
+        (void)self;                                                                                           \
+        if (!g_training[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");          \
+        if (take(#name, form, a, n, &v)) return NULL;                                                         \
+        return PyLong_FromSize_t(expr);                                                                       \
+    }
+
+BYTES(groupnorm_act_workspace_bytes, 0, "iiiii",
+      ((gn_bytes_fn)g_training[0])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
+CALL(groupnorm_act, 1, "ppppfiiiiiipipip",
+     ((gn_fn)g_training[1])(v.p[0], v.p[1], v.p[2], v.p[3], v.f[4], v.i[5], v.i[6], v.i[7], v.i[8], v.i[9],
+                            (int)v.i[10], (float*)v.p[11], (int)v.i[12], v.p[13], (size_t)v.i[14], v.p[15]))
+BYTES(groupnorm_act_backward_workspace_bytes, 2, "iiiii",
+      ((gn_bytes_fn)g_training[2])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
+CALL(groupnorm_act_backward, 3, "ppppppppiiiiiiipip",
+     ((gn_bwd_fn)g_training[3])(v.p[0], v.p[1], v.p[2], v.p[3], (float*)v.p[4], v.p[5], (float*)v.p[6],
+                                (float*)v.p[7], v.i[8], v.i[9], v.i[10], v.i[11], v.i[12], (int)v.i[13],
+                                (int)v.i[14], v.p[15], (size_t)v.i[16], v.p[17]))
+CALL(bias_dropout_residual, 4, "ppppfuupiiiip",
+     ((drop_fn)g_training[4])(v.p[0], v.p[1], v.p[2], v.p[3], v.f[4], v.u[5], v.u[6], v.p[7], v.i[8], v.i[9],
+                              v.i[10], (int)v.i[11], v.p[12]))
+BYTES(bias_dropout_residual_backward_workspace_bytes, 5, "iii",
+      ((rows_bytes_fn)g_training[5])(v.i[0], v.i[1], (int)v.i[2]))
+CALL(bias_dropout_residual_backward, 6, "pppfuupiiiipip",
+     ((drop_bwd_fn)g_training[6])(v.p[0], v.p[1], (float*)v.p[2], v.f[3], v.u[4], v.u[5], v.p[6], v.i[7], v.i[8],
+                                  v.i[9], (int)v.i[10], v.p[11], (size_t)v.i[12], v.p[13]))
+CALL(router_balance_loss, 7, "ppipfppiiiiipip",
+     ((balance_fn)g_training[7])(v.p[0], v.p[1], (int)v.i[2], v.p[3], v.f[4], (float*)v.p[5], v.p[6], v.i[7],
+                                 v.i[8], v.i[9], v.i[10], (int)v.i[11], v.p[12], (size_t)v.i[13], v.p[14]))
+CALL(router_balance_loss_backward, 8, "ppppfpiiiiip",
+     ((balance_bwd_fn)g_training[8])(v.p[0], v.p[1], (float*)v.p[2], v.p[3], v.f[4], v.p[5], v.i[6], v.i[7], v.i[8],
+                                     v.i[9], (int)v.i[10], v.p[11]))
+
+#define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, "rowops_" #name}
+
 static PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "bind(softmax, layernorm_gelu, layernorm_gelu_erf)"},
     {"softmax", (PyCFunction)(void (*)(void))softmax, METH_FASTCALL, "rowops_softmax"},
     {"layernorm_gelu", (PyCFunction)(void (*)(void))layernorm_gelu, METH_FASTCALL, "rowops_layernorm_gelu"},
     {"layernorm_gelu_erf", (PyCFunction)(void (*)(void))layernorm_gelu_erf, METH_FASTCALL,
      "rowops_layernorm_gelu_erf"},
+    {"bind_training", (PyCFunction)(void (*)(void))bind_training, METH_FASTCALL, "addresses of the functions below"},
+    METHOD(groupnorm_act_workspace_bytes),
+    METHOD(groupnorm_act),
+    METHOD(groupnorm_act_backward_workspace_bytes),
+    METHOD(groupnorm_act_backward),
+    METHOD(bias_dropout_residual),
+    METHOD(bias_dropout_residual_backward_workspace_bytes),
+    METHOD(bias_dropout_residual_backward),
+    METHOD(router_balance_loss),
+    METHOD(router_balance_loss_backward),
     {NULL, NULL, 0, NULL},
 };
 

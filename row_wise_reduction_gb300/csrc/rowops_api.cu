@@ -8,6 +8,8 @@
 #include <mutex>
 #include <vector>
 
+#include <cuda.h>
+
 #include "rowops.h"
 #include "rowops_launch.h"
 
@@ -40,6 +42,7 @@ struct Tuning {
     long long stall_row = -1; // test hook (see include/rowops.h)
     int sched = 0;            // full-row pipelines: 0 automatic, 1 static, 2 dynamic (cluster launch control)
     int unit_rows = 0;        // dynamic schedule: rows per group in a work unit (0: automatic)
+    int groupnorm = 0;        // group norm: 0 automatic, 1 one kernel where it can, 2 two passes
     int bwd = 0;              // LayerNorm+GELU backward partials: 0 automatic, 1 registers, 2 tensor memory
 };
 
@@ -81,6 +84,7 @@ Tuning read_tuning() {
         else if (is("UNIT_ROWS")) t.unit_rows = int(parse_int(v, 0));
         else if (is("SCHED")) t.sched = !std::strcmp(v, "static") ? 1 : (!std::strcmp(v, "dynamic") ? 2 : 0);
         else if (is("BWD_PARTIALS")) t.bwd = !std::strcmp(v, "registers") ? 1 : (!std::strcmp(v, "tmem") ? 2 : 0);
+        else if (is("GROUPNORM")) t.groupnorm = !std::strcmp(v, "fused") ? 1 : (!std::strcmp(v, "two_pass") ? 2 : 0);
         else if (is("ONLINE"))
             t.online = !std::strcmp(v, "two_pass") ? 1
                      : !std::strcmp(v, "single_read") ? 2
@@ -519,6 +523,36 @@ unsigned long long current_context_id() {
     unsigned long long id = 0;
     if (g_ctx_get_current(&ctx) != 0 || ctx == nullptr || g_ctx_get_id(ctx, &id) != 0) return 0;
     return id;
+}
+
+namespace {
+using TensorMapFn = decltype(&cuTensorMapEncodeTiled);
+std::once_flag g_map_fn_once;
+TensorMapFn g_map_fn = nullptr;
+}  // namespace
+
+cudaError_t rows_map(RowsMap* m, const void* base, int64_t row_bytes, int64_t rows, int64_t ld_bytes, int box_bytes,
+                     int box_rows) {
+    static_assert(sizeof(RowsMap) == sizeof(CUtensorMap), "a tensor map's size");
+    std::call_once(g_map_fn_once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_map_fn = reinterpret_cast<TensorMapFn>(f);
+        cudaGetLastError();
+    });
+    if (!g_map_fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {cuuint64_t(row_bytes / 8), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld_bytes)};
+    const cuuint32_t box[2] = {cuuint32_t(box_bytes / 8), cuuint32_t(box_rows)};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = g_map_fn(reinterpret_cast<CUtensorMap*>(m), CU_TENSOR_MAP_DATA_TYPE_INT64, 2,
+                                const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 int grid_for(const void* func, int block, size_t smem, int64_t items, const LaunchCfg& cfg) {
@@ -1061,6 +1095,46 @@ rowops_status_t check_groups(int64_t B, int64_t S, int64_t C, int64_t G, rowops_
     return ROWOPS_OK;
 }
 
+// One kernel or two passes: what the model of the time says (vec: channels of an
+// access). The last shapes' answers are kept per thread: the model tries some
+// thirty splits, a microsecond of a call that takes a few.
+struct GnChoice {
+    int64_t B = -1, S, C, G;
+    int es, tensors, vec, knob;
+    bool one;
+    GnFused f;
+};
+const GnChoice& gn_choose(int64_t B, int64_t S, int64_t C, int64_t G, int es, int tensors, int vec, int knob) {
+    static thread_local GnChoice kept[8];
+    static thread_local unsigned next = 0;
+    for (const GnChoice& k : kept)
+        if (k.B == B && k.S == S && k.C == C && k.G == G && k.es == es && k.tensors == tensors && k.vec == vec &&
+            k.knob == knob)
+            return k;
+    GnChoice& k = kept[next++ % 8];
+    k = GnChoice{};
+    k.B = B, k.S = S, k.C = C, k.G = G, k.es = es, k.tensors = tensors, k.vec = vec, k.knob = knob;
+    const GnArgs a = gn_plan(B, S, C, G, C, es, tensors, 0.f);
+    const double one = knob == 2 ? -1.0 : gn_fused_plan(a, es, tensors, vec, &k.f);
+    k.one = one >= 0 && (knob == 1 || one <= gn_two_pass_time(a, es, tensors));
+    return k;
+}
+
+// A workspace for whichever width of access the call's alignment allows. One
+// kernel: none forward, backward two sums for the channels of every CTA of a
+// cluster. Two passes: a mean and a sum of squares for every chunk's groups;
+// backward two sums for its groups and channels.
+size_t gn_bytes(int64_t B, int64_t S, int64_t C, int64_t G, int es, int tensors, int knob) {
+    size_t most = 0;
+    for (const int vec : {1, 16 / es}) {
+        if (C % vec) continue;
+        const GnChoice& k = gn_choose(B, S, C, G, es, tensors, vec, knob);
+        const size_t rows = size_t(B) * (k.one ? k.f.cluster : gn_plan(B, S, C, G, C, es, tensors, 0.f).chunks);
+        most = std::max(most, rows * ((k.one ? 0 : size_t(G)) + (tensors > 1 ? size_t(C) : 0)) * 8);
+    }
+    return most;
+}
+
 bool valid_act(rowops_act_t act) { return act >= ROWOPS_ACT_NONE && act <= ROWOPS_ACT_GELU_TANH; }
 
 rowops_status_t make_mask(float p, uint64_t seed, uint64_t offset, const uint64_t* device_offset, DropoutMask* m) {
@@ -1081,8 +1155,7 @@ bool vector_rows(const Tuning& tn, int64_t N, int64_t ld, int es, std::initializ
 size_t rowops_groupnorm_act_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G, rowops_dtype_t dtype) {
     int64_t M = 0;
     if (check_groups(B, S, C, G, dtype, &M) != ROWOPS_OK || M == 0) return 0;
-    const GnArgs a = gn_plan(B, S, C, G, C, elem_bytes(dtype), 0.f);
-    return size_t(B) * a.chunks * size_t(G) * 8;  // a mean and a sum of squares for every chunk's groups
+    return gn_bytes(B, S, C, G, elem_bytes(dtype), 1, tuning().groupnorm);
 }
 
 rowops_status_t rowops_groupnorm_act(const void* x, void* y, const void* w, const void* b, float eps, int64_t B,
@@ -1101,25 +1174,25 @@ rowops_status_t rowops_groupnorm_act(const void* x, void* y, const void* w, cons
     if (!apart_from({y, rows}, {{w, row}, {b, row}}) ||
         !apart_from({stats, sb}, {{x, rows}, {y, rows}, {w, row}, {b, row}}))
         return ROWOPS_ERR_INVALID_VALUE;
-    if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < rowops_groupnorm_act_workspace_bytes(B, S, C, G, dtype))
-        return ROWOPS_ERR_WORKSPACE;
-    if (!apart_from({workspace, workspace_bytes}, {{x, rows}, {y, rows}, {w, row}, {b, row}, {stats, sb}}))
+    const size_t need = rowops_groupnorm_act_workspace_bytes(B, S, C, G, dtype);
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ROWOPS_ERR_WORKSPACE;
+    if (need && !apart_from({workspace, workspace_bytes}, {{x, rows}, {y, rows}, {w, row}, {b, row}, {stats, sb}}))
         return ROWOPS_ERR_INVALID_VALUE;
     const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
     const bool vec = vector_rows(tn, C, ld, es, {x, y});
     const GnForwardLaunch fn = dtype == ROWOPS_F32 ? gn_forward_f32(vec, act) : gn_forward_bf16(vec, act);
-    return finish(fn(x, y, w, b, stats, workspace, gn_plan(B, S, C, G, ld, es, eps), cfg));
+    const GnArgs a = gn_plan(B, S, C, G, ld, es, 1, eps);
+    const GnChoice& k = gn_choose(B, S, C, G, es, 1, vec ? 16 / es : 1, tn.groupnorm);
+    return finish(fn(x, y, w, b, stats, workspace, a, k.one ? &k.f : nullptr, cfg));
 }
 
 size_t rowops_groupnorm_act_backward_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t G,
                                                      rowops_dtype_t dtype) {
     int64_t M = 0;
     if (check_groups(B, S, C, G, dtype, &M) != ROWOPS_OK || M == 0) return 0;
-    const GnArgs a = gn_plan(B, S, C, G, C, elem_bytes(dtype), 0.f);
-    return size_t(B) * a.chunks * (size_t(C) + size_t(G)) * 8;  // two sums for every chunk's channels and groups
+    return gn_bytes(B, S, C, G, elem_bytes(dtype), 2, tuning().groupnorm);
 }
 
 rowops_status_t rowops_groupnorm_act_backward(const void* x, const void* dy, const void* w, const void* b,
@@ -1146,19 +1219,20 @@ rowops_status_t rowops_groupnorm_act_backward(const void* x, const void* dy, con
         st = zero(dw, C, stream);
         return st == ROWOPS_OK ? zero(db, C, stream) : st;
     }
-    if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < rowops_groupnorm_act_backward_workspace_bytes(B, S, C, G, dtype))
-        return ROWOPS_ERR_WORKSPACE;
+    const size_t need = rowops_groupnorm_act_backward_workspace_bytes(B, S, C, G, dtype);
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ROWOPS_ERR_WORKSPACE;
     for (const Range& r : in)
-        if (!apart(workspace, workspace_bytes, r.p, r.n)) return ROWOPS_ERR_INVALID_VALUE;
-    if (!apart_from({workspace, workspace_bytes}, {{dx, rows}, {dw, sums}, {db, sums}}))
+        if (need && !apart(workspace, workspace_bytes, r.p, r.n)) return ROWOPS_ERR_INVALID_VALUE;
+    if (need && !apart_from({workspace, workspace_bytes}, {{dx, rows}, {dw, sums}, {db, sums}}))
         return ROWOPS_ERR_INVALID_VALUE;
     const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
     const bool vec = vector_rows(tn, C, ld, es, {x, dy, dx});
     const GnBackwardLaunch fn = dtype == ROWOPS_F32 ? gn_backward_f32(vec, act) : gn_backward_bf16(vec, act);
-    return finish(fn(x, dy, w, b, stats, dx, dw, db, workspace, gn_plan(B, S, C, G, ld, es, 0.f), cfg));
+    const GnArgs a = gn_plan(B, S, C, G, ld, es, 2, 0.f);
+    const GnChoice& k = gn_choose(B, S, C, G, es, 2, vec ? 16 / es : 1, tn.groupnorm);
+    return finish(fn(x, dy, w, b, stats, dx, dw, db, workspace, a, k.one ? &k.f : nullptr, cfg));
 }
 
 rowops_status_t rowops_bias_dropout_residual(const void* x, const void* residual, const void* bias, void* y, float p,

@@ -2,6 +2,8 @@
 // instantiation units. Not part of the public interface.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -254,43 +256,145 @@ using BalanceBackwardLaunch = cudaError_t (*)(const void* logits, const int64_t*
 BalanceBackwardLaunch balance_backward_f32();
 BalanceBackwardLaunch balance_backward_bf16();
 
-// Group norm + activation on channels-last data and its backward; GnArgs'
-// chunks, chunk_rows and rows as gn_plan sets them (the workspace's layout
-// follows from them).
+// Group norm + activation on channels-last data and its backward.
 constexpr int kGnMaxChannels = 8192;
+constexpr int kGnBlock = 256;                      // threads of a CTA: the fused form and pass 2
+constexpr int kGnWide = 1024, kGnWideBwd = 512;    // pass 1, forward and backward
+constexpr int kGnSms = 152;
+constexpr size_t kGnSmem = 227 * 1024;
 struct GnArgs {
     int64_t S, ld;
-    int B, C, G, L;      // L = C / G channels of a group
+    int B, C, G, L;  // L = C / G channels of a group
+    float eps, m;    // m = S L elements of a group
+    float inv_L, inv_S, inv_m;
+    // the two-pass form
     int tx, tiles;       // channel vectors side by side, and how many times
-    int chunks;          // of a sample, in the pass that leaves sums
-    int64_t chunk_rows;  // positions of such a chunk
-    int64_t rows;        // positions of a CTA of the pass that writes
-    float eps;
+    int64_t batch, b0;   // samples of a batch; its first
+    int chunks;          // CTAs of pass 1 a sample
+    int64_t chunk_rows;  // their positions
+    int64_t rows;        // positions of a CTA of pass 2
 };
-// Chunks of a sample: four CTAs for each of 152 SMs over all samples, of at
-// least 16 KiB, and at most 65536 group sums a sample (a CTA of the second pass
-// reads all of its sample's).
-inline GnArgs gn_plan(int64_t B, int64_t S, int64_t C, int64_t G, int64_t ld, int es, float eps) {
+
+// The two-pass form takes batches of samples that stay in L2 between the passes
+// (64 MB of 129). In each, every SM gets as many CTAs as it holds at once (a
+// grid of 1.3 waves took the time of two): one of pass 1, three (backward two) of
+// pass 2, of at least 16 KiB. Pass 1 leaves at most 16384 group sums a sample: a
+// CTA of pass 2 reads all of its sample's.
+constexpr int64_t kGnBatchBytes = int64_t(64) << 20;
+inline GnArgs gn_plan(int64_t B, int64_t S, int64_t C, int64_t G, int64_t ld, int es, int tensors, float eps) {
     GnArgs a{};
     a.S = S, a.ld = ld, a.B = int(B), a.C = int(C), a.G = int(G), a.L = int(C / G), a.eps = eps;
-    const int64_t least = (16384 + C * es - 1) / (C * es);
-    auto split = [&](int64_t ctas, int64_t most) {
-        int64_t n = (ctas + B - 1) / B;
-        const int64_t fit = (S + least - 1) / least;
-        n = n < fit ? n : fit;
-        n = n < most ? n : most;
-        return (S + n - 1) / n;  // positions of a chunk
-    };
-    a.chunk_rows = split(608, 65536 / G);
+    a.m = float(S) * float(a.L), a.inv_L = 1.f / a.L, a.inv_S = float(1.0 / S), a.inv_m = float(1.0 / (double(S) * a.L));
+    a.batch = std::min(B, std::max(int64_t(1), kGnBatchBytes / (S * C * es * tensors)));
+    const int64_t least = (16384 + C * es * tensors - 1) / (C * es * tensors);
+    auto chunks = [&](int64_t ctas) { return std::min(std::max(int64_t(1), ctas / a.batch), (S + least - 1) / least); };
+    int64_t n = std::min(chunks(kGnSms), std::max(int64_t(1), 16384 / G));
+    a.chunk_rows = (S + n - 1) / n;
     a.chunks = int((S + a.chunk_rows - 1) / a.chunk_rows);
-    a.rows = split(1216, 65535);
+    n = chunks((tensors > 1 ? 2 : 3) * kGnSms);
+    a.rows = (S + n - 1) / n;
     return a;
 }
+
+// A tensor map for boxes of a matrix's rows (128 bytes, a CUtensorMap).
+struct alignas(64) RowsMap {
+    unsigned char bytes[128];
+};
+// Rows of row_bytes (a multiple of 8), ld_bytes apart (a multiple of 16) from a
+// 16-byte aligned base; boxes of box_bytes (a multiple of 16, at most 2048) by
+// box_rows (at most 256).
+cudaError_t rows_map(RowsMap* m, const void* base, int64_t row_bytes, int64_t rows, int64_t ld_bytes, int box_bytes,
+                     int box_rows);
+
+// The form that holds a slab (a sample's positions of a block of whole groups)
+// in the shared memory of a cluster of CTAs and reads every tensor once.
+struct GnFused {
+    int blocks, cluster, cluster_log2;  // blocks of groups of a sample; CTAs of a cluster
+    int W, tx, ty, inv_tx;   // channels of a block; its vectors; positions of a CTA at a time; 2^16 / tx
+    int rows;                // positions of a CTA
+    int box, boxes, pitch;   // positions of a copy; copies; vectors from one to the next
+    int parts_log2, team_log2;  // lanes that add up a channel, a group
+    size_t tile, smem;       // bytes: the slab's share; in all
+};
+constexpr int kGnMaxBoxes = 32;
+
+// The fastest split into groups' blocks and clusters by a model of the time, in
+// microseconds; `tensors`: 1 forward, 2 backward (read and held). Returns the
+// modelled time, or a negative number where no split holds the slab. The model:
+// the traffic at the card's copy rate, or the waves of CTAs at the rate of an
+// SM's share if that is longer; a launch, and an exchange where a cluster
+// has several CTAs.
+inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFused* best) {
+    double least = -1.0;
+    const double all = double(a.B) * a.S * a.C * es * (tensors + 1);
+    if (double(a.B) * a.S > 2147483647.0) return least;  // a copy's coordinates
+    auto log2_floor = [](int v) {
+        int l = 0;
+        while (v > 1) v >>= 1, ++l;
+        return l;
+    };
+    for (int blocks = 1; blocks <= a.G; ++blocks) {
+        if (a.G % blocks) continue;
+        const int W = a.C / blocks, tx = (W + vec - 1) / vec;
+        if (W % vec || tx > kGnBlock || (vec > 1 && W * es > 2048)) continue;
+        if (blocks > 1 && W * es < 64) break;
+        for (int cl = 0; cl <= 4; ++cl) {
+            const int cluster = 1 << cl;
+            if (cluster > 1 && cluster > a.S) break;
+            const double ctas = double(a.B) * blocks * cluster;
+            if (ctas > 2147483647.0) break;
+            const int64_t rows = (a.S + cluster - 1) / cluster;
+            if (rows * tx > int64_t(kGnSmem)) continue;
+            GnFused f{};
+            f.blocks = blocks, f.cluster = cluster, f.cluster_log2 = cl, f.W = W, f.tx = tx;
+            f.ty = int(std::min<int64_t>(kGnBlock / tx, rows));
+            f.inv_tx = (65536 + tx - 1) / tx;
+            f.rows = int(rows);
+            // four copies where they are worth it, of at most 256 rows; slots of 128 bytes
+            f.boxes = vec == 1 ? 1 : int(std::max<int64_t>(rows * W * es >= 16384 ? 4 : 1, (rows + 255) / 256));
+            f.box = int((rows + f.boxes - 1) / f.boxes);
+            f.boxes = int((rows + f.box - 1) / f.box);
+            if (f.boxes > kGnMaxBoxes) continue;
+            const int unit = 128 / (vec * es);
+            f.pitch = vec == 1 ? f.box * tx : (f.box * tx + unit - 1) / unit * unit;
+            f.tile = (size_t(tensors) * f.boxes * f.pitch * vec * es + 127) / 128 * 128;
+            const size_t groups = size_t(W / a.L);
+            f.smem = f.tile + size_t(f.ty) * W * 8 + size_t(W) * 8 + groups * 8 * (1 + cluster) + f.boxes * 8 +
+                     size_t(f.ty) * 4;
+            if (f.smem > kGnSmem) continue;
+            f.parts_log2 = W >= kGnBlock ? 0 : std::min(5, log2_floor(std::min(kGnBlock / W, f.ty)));
+            f.team_log2 = std::min(std::min(5, log2_floor(kGnBlock / std::min<int>(kGnBlock, int(groups)))),
+                                   log2_floor(2 * a.L - 1));
+            const int per_sm = f.smem <= kGnSmem / 3 - 1024 && tensors == 1 ? 3 : f.smem <= kGnSmem / 2 - 512 ? 2 : 1;
+            double wide = 1.0;
+            if (tx * f.ty < kGnBlock * 3 / 4) wide *= 1.15;
+            const double io = double(rows) * W * es * (tensors + 1) * wide;
+            // SMs that clusters of this size can fill (the GPCs have no multiple of it)
+            const double sms = kGnSms * (cluster == 16 ? 0.74 : cluster == 8 ? 0.9 : cluster == 4 ? 0.96 : 1.0);
+            const double sm = ctas <= sms ? io : std::ceil(ctas / (sms * per_sm)) * per_sm * io;
+            double t = 3.0 + (cluster > 1 ? 1.0 : 0.0) + std::max(all * wide / 6.8e6, sm / 5.5e4);
+            if (per_sm == 1 && ctas > kGnSms) t *= 1.4;  // nothing covers a CTA's exchange
+            if (least < 0 || t < least) {
+                least = t;
+                *best = f;
+            }
+        }
+    }
+    return least;
+}
+
+// The two-pass form's modelled time: its launches, the first read, and the second
+// at twice the copy rate next to the writes.
+inline double gn_two_pass_time(const GnArgs& a, int es, int tensors) {
+    const double in = double(a.B) * a.S * a.C * es * tensors;
+    return std::ceil(double(a.B) / a.batch) * 5.0 + (1.5 * in + in / tensors) / 6.8e6;
+}
+
 using GnForwardLaunch = cudaError_t (*)(const void* x, void* y, const void* w, const void* b, float* stats, void* ws,
-                                        GnArgs a, const LaunchCfg& cfg);
+                                        GnArgs a, const GnFused* f, const LaunchCfg& cfg);
 using GnBackwardLaunch = cudaError_t (*)(const void* x, const void* dy, const void* w, const void* b,
                                          const float* stats, void* dx, float* dw, float* db, void* ws, GnArgs a,
-                                         const LaunchCfg& cfg);
+                                         const GnFused* f, const LaunchCfg& cfg);
 GnForwardLaunch gn_forward_f32(bool vec, int act);
 GnForwardLaunch gn_forward_bf16(bool vec, int act);
 GnBackwardLaunch gn_backward_f32(bool vec, int act);

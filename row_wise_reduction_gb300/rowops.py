@@ -159,12 +159,25 @@ def library() -> ctypes.CDLL:
     return _lib
 
 
+_TRAINING = (
+    "groupnorm_act_workspace_bytes",
+    "groupnorm_act",
+    "groupnorm_act_backward_workspace_bytes",
+    "groupnorm_act_backward",
+    "bias_dropout_residual",
+    "bias_dropout_residual_backward_workspace_bytes",
+    "bias_dropout_residual_backward",
+    "router_balance_loss",
+    "router_balance_loss_backward",
+)
+
+
 class _Calls:
     """The entry points whose small calls are bound by host time: through the
     CPython call module ``_rowops_call`` where it was built (about 0.1 us of
     marshalling per call), else through ctypes (about 2 us)."""
 
-    __slots__ = ("softmax", "layernorm_gelu", "layernorm_gelu_erf", "module")
+    __slots__ = ("softmax", "layernorm_gelu", "layernorm_gelu_erf", "module") + _TRAINING
 
 
 _calls: Optional[_Calls] = None
@@ -186,6 +199,10 @@ def _bind_calls(L: ctypes.CDLL) -> None:
     else:
         c.softmax, c.layernorm_gelu, c.layernorm_gelu_erf = (L.rowops_softmax, L.rowops_layernorm_gelu,
                                                               L.rowops_layernorm_gelu_erf)
+    if fast is not None:
+        fast.bind_training(*(addr(getattr(L, "rowops_" + n)) for n in _TRAINING))
+    for n in _TRAINING:
+        setattr(c, n, getattr(L, "rowops_" + n) if fast is None else getattr(fast, n))
     c.module = fast
     _calls = c
 
@@ -598,6 +615,8 @@ def rowops_gelu(x: torch.Tensor, y: Optional[torch.Tensor] = None, approximate: 
 # ---------------------------------------------------------------------------
 def _elsewhere(fn, stream, dev, *args, **kwargs):
     """``fn`` with the tensors' device and ``stream`` current."""
+    if dev < 0:
+        raise ValueError("the call's tensors must be CUDA tensors")
     with torch.cuda.device(dev):
         if stream is None:
             return fn(*args, **kwargs)
@@ -631,11 +650,10 @@ def _act(act: str) -> int:
 def _positions(x: torch.Tensor, name: str):
     """(B, S, C, ld) of a channels-last (B, S, C) CUDA tensor whose B * S
     positions are one stride apart."""
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dim() != 3:
+    sh = x.shape
+    if len(sh) != 3:
         raise ValueError(f"{name} must be 3-D (samples, positions, channels)")
-    B, S, C = x.shape
+    B, S, C = sh
     sb, ss, sc = x.stride()
     if C > 1 and sc != 1:
         raise ValueError(f"{name} must have unit channel stride")
@@ -650,7 +668,7 @@ def _like_positions(x: torch.Tensor, ld: int, t: Optional[torch.Tensor], name: s
         return torch.empty_strided(x.shape, (x.shape[1] * ld, ld, 1), dtype=x.dtype, device=x.device)
     if t.dtype is not x.dtype or t.get_device() != x.get_device() or t.shape != x.shape:
         raise ValueError(f"{name} must match x in shape, dtype and device")
-    if x.shape[0] * x.shape[1] > 1 and _positions(t, name)[3] != ld:
+    if t.stride() != x.stride() and x.shape[0] * x.shape[1] > 1 and _positions(t, name)[3] != ld:
         raise ValueError(f"x and {name} must share the stride of their positions")
     return t
 
@@ -695,18 +713,19 @@ def rowops_groupnorm_act(
     least ``rowops_groupnorm_act_workspace_bytes(...)`` bytes, allocated per call
     when omitted."""
     dev = x.get_device()
-    if stream is not None or (dev >= 0 and dev != _current_device()):
+    if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_groupnorm_act, stream, dev, x, groups, w, b, eps, act, y, stats, workspace=workspace)
     B, S, C, ld = _positions(x, "x")
     code = _dtype_code(x)
     y = _like_positions(x, ld, y, "y")
-    L = _lib or library()
-    ws, wp, wn = _scratch(workspace, L.rowops_groupnorm_act_workspace_bytes(B, S, C, groups, code), dev)
-    st = L.rowops_groupnorm_act(
+    L = _calls or _hot_calls()
+    ws, wp, wn = _scratch(workspace, L.groupnorm_act_workspace_bytes(B, S, C, groups, code), dev)
+    st = L.groupnorm_act(
         x.data_ptr(), y.data_ptr(), _affine(w, x, C, dev, "w"), _affine(b, x, C, dev, "b"), eps, B, S, C, groups, ld,
         _act(act), None if stats is None else _group_stats(stats, B, groups, dev), code, wp, wn,
         _current_raw_stream(dev))
-    _check("rowops_groupnorm_act", st)
+    if st:
+        raise RowopsError("rowops_groupnorm_act", st)
     return y
 
 
@@ -733,7 +752,7 @@ def rowops_groupnorm_act_backward(
     ``stats`` that the forward call wrote: ``(dx, dw, db)``, dx as x, dw and db
     float32 (C,)."""
     dev = x.get_device()
-    if stream is not None or (dev >= 0 and dev != _current_device()):
+    if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_groupnorm_act_backward, stream, dev, x, dy, stats, groups, w, b, act, dx, dw, db,
                           workspace=workspace)
     B, S, C, ld = _positions(x, "x")
@@ -742,17 +761,15 @@ def rowops_groupnorm_act_backward(
     dx = _like_positions(x, ld, dx, "dx")
     dw = _floats(dw, C, dev, "dw")
     db = _floats(db, C, dev, "db")
-    L = _lib or library()
-    ws, wp, wn = _scratch(workspace, L.rowops_groupnorm_act_backward_workspace_bytes(B, S, C, groups, code), dev)
-    st = L.rowops_groupnorm_act_backward(
+    L = _calls or _hot_calls()
+    ws, wp, wn = _scratch(workspace, L.groupnorm_act_backward_workspace_bytes(B, S, C, groups, code), dev)
+    st = L.groupnorm_act_backward(
         x.data_ptr(), dy.data_ptr(), _affine(w, x, C, dev, "w"), _affine(b, x, C, dev, "b"),
         _group_stats(stats, B, groups, dev), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), B, S, C, groups, ld,
         _act(act), code, wp, wn, _current_raw_stream(dev))
-    _check("rowops_groupnorm_act_backward", st)
+    if st:
+        raise RowopsError("rowops_groupnorm_act_backward", st)
     return dx, dw, db
-
-
-_U64 = (1 << 64) - 1
 
 
 def _device_offset(t: Optional[torch.Tensor], dev: int):
@@ -782,17 +799,18 @@ def rowops_bias_dropout_residual(
     an int64 tensor of one entry that is added to ``offset`` when the kernel
     runs, so that a captured graph replays with new masks."""
     dev = x.get_device()
-    if stream is not None or (dev >= 0 and dev != _current_device()):
+    if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_bias_dropout_residual, stream, dev, x, residual, bias, p, seed, offset, y,
                           device_offset=device_offset)
     M, N, ld, y, code, dev = _xy(x, y)
-    if residual is not None:
-        _out_like(x, residual)  # same shape, dtype, device and row stride
-    st = (_lib or library()).rowops_bias_dropout_residual(
+    if residual is not None and (residual.dtype is not x.dtype or residual.get_device() != dev
+                                 or residual.shape != x.shape or (M > 1 and residual.stride() != x.stride())):
+        raise ValueError("residual must match x in shape, dtype, device and row stride")
+    st = (_calls or _hot_calls()).bias_dropout_residual(
         x.data_ptr(), None if residual is None else residual.data_ptr(), _affine(bias, x, N, dev, "bias"),
-        y.data_ptr(), p, seed & _U64, offset & _U64, _device_offset(device_offset, dev), M, N, ld, code,
-        _current_raw_stream(dev))
-    _check("rowops_bias_dropout_residual", st)
+        y.data_ptr(), p, seed, offset, _device_offset(device_offset, dev), M, N, ld, code, _current_raw_stream(dev))
+    if st:
+        raise RowopsError("rowops_bias_dropout_residual", st)
     return y
 
 
@@ -818,22 +836,23 @@ def rowops_bias_dropout_residual_backward(
     may be ``dy``), dbias float32 (N,), or None without ``bias_grad``. The
     residual's gradient is dy itself."""
     dev = dy.get_device()
-    if stream is not None or (dev >= 0 and dev != _current_device()):
+    if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_bias_dropout_residual_backward, stream, dev, dy, p, seed, offset, dx, dbias,
                           bias_grad, device_offset=device_offset, workspace=workspace)
     M, N, ld, dx, code, dev = _xy(dy, dx)
-    L = _lib or library()
+    L = _calls or _hot_calls()
     ws, wp, wn = None, None, 0
     if bias_grad:
         dbias = _floats(dbias, N, dev, "dbias")
-        need = L.rowops_bias_dropout_residual_backward_workspace_bytes(M, N, code)
+        need = L.bias_dropout_residual_backward_workspace_bytes(M, N, code)
         ws, wp, wn = _scratch(workspace, need, dev)
     elif dbias is not None:
         raise ValueError("dbias is given but bias_grad is false")
-    st = L.rowops_bias_dropout_residual_backward(
-        dy.data_ptr(), dx.data_ptr(), None if dbias is None else dbias.data_ptr(), p, seed & _U64, offset & _U64,
+    st = L.bias_dropout_residual_backward(
+        dy.data_ptr(), dx.data_ptr(), None if dbias is None else dbias.data_ptr(), p, seed, offset,
         _device_offset(device_offset, dev), M, N, ld, code, wp, wn, _current_raw_stream(dev))
-    _check("rowops_bias_dropout_residual_backward", st)
+    if st:
+        raise RowopsError("rowops_bias_dropout_residual_backward", st)
     return dx, dbias
 
 
@@ -875,7 +894,7 @@ def rowops_router_balance_loss(
     counts int64 (E + 1,): the experts' counts and, last, the rows that took
     part. ``mask``: bool or uint8 (T,), rows with 0 take no part."""
     dev = logits.get_device()
-    if stream is not None or (dev >= 0 and dev != _current_device()):
+    if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_router_balance_loss, stream, dev, logits, experts, coef, mask, loss, counts,
                           workspace=workspace)
     T, E, ld = _rows(logits, "logits")
@@ -887,12 +906,13 @@ def rowops_router_balance_loss(
         raise TypeError(f"experts must be int32 or int64, not {experts.dtype}")
     loss = _floats(loss, 1, dev, "loss")
     counts = _counts(counts, E, dev)
-    L = _lib or library()
-    ws, wp, wn = _scratch(workspace, L.rowops_router_balance_loss_workspace_bytes(T, E, code), dev)
-    st = L.rowops_router_balance_loss(
+    L = _calls or _hot_calls()
+    ws, wp, wn = _scratch(workspace, library().rowops_router_balance_loss_workspace_bytes(T, E, code), dev)
+    st = L.router_balance_loss(
         logits.data_ptr(), experts.data_ptr(), width, _row_mask(mask, T, dev), coef, loss.data_ptr(),
         counts.data_ptr(), T, E, experts.shape[1], ld, code, wp, wn, _current_raw_stream(dev))
-    _check("rowops_router_balance_loss", st)
+    if st:
+        raise RowopsError("rowops_router_balance_loss", st)
     return loss, counts
 
 
@@ -912,14 +932,15 @@ def rowops_router_balance_loss_backward(
     the loss's own gradient ``dloss`` (float32, one entry, on the GPU).
     ``dlogits`` may be ``logits``."""
     dev = logits.get_device()
-    if stream is not None or (dev >= 0 and dev != _current_device()):
+    if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_router_balance_loss_backward, stream, dev, logits, counts, top_k, dloss, coef, mask,
                           dlogits)
     T, E, ld, dlogits, code, dev = _xy(logits, dlogits)
     if dloss.dtype is not torch.float32 or dloss.numel() != 1 or dloss.get_device() != dev:
         raise ValueError("dloss must be a float32 CUDA tensor of one entry")
-    st = (_lib or library()).rowops_router_balance_loss_backward(
+    st = (_calls or _hot_calls()).router_balance_loss_backward(
         logits.data_ptr(), _counts(counts, E, dev).data_ptr(), dloss.data_ptr(), _row_mask(mask, T, dev), coef,
         dlogits.data_ptr(), T, E, top_k, ld, code, _current_raw_stream(dev))
-    _check("rowops_router_balance_loss_backward", st)
+    if st:
+        raise RowopsError("rowops_router_balance_loss_backward", st)
     return dlogits

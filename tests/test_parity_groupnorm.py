@@ -233,3 +233,90 @@ def test_refusals_of_the_binding():
         ro.rowops_groupnorm_act(x.half(), 4)
     with pytest.raises(ro.RowopsError):
         ro.rowops_groupnorm_act(x, 5)
+
+
+FORMS = ["fused", "two_pass"]
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize(
+    "B,S,C,G,pad,offset",
+    [(2, 64, 1280, 32, 0, 0), (3, 1155, 330, 30, 5, 0), (1, 4096, 320, 32, 0, 0), (9, 1024, 64, 4, 0, 0),
+     (2, 5, 96, 12, 0, 0), (1, 3000, 8, 8, 0, 0), (20, 2048, 32, 2, 8, 8), (4, 333, 40, 5, 0, 1), (1, 20000, 16, 1, 0, 0),
+     (300, 1, 640, 32, 0, 0), (2, 16, 8192, 8192, 0, 0), (1, 40, 4100, 41, 0, 0)])
+def test_both_forms(form, dtype, B, S, C, G, pad, offset, monkeypatch):
+    monkeypatch.setenv("ROWOPS_GROUPNORM", form)
+    if S == 1 and C == G or (C == G and S < 20):
+        # nearly empty groups: the 64-bit variance's own rounding would show
+        check(B, S, C, G, dtype, pad=pad, offset=offset, eps=1e-2)
+    else:
+        check(B, S, C, G, dtype, pad=pad, offset=offset)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("act", ACTS)
+def test_activations_of_both_forms(form, act, monkeypatch):
+    monkeypatch.setenv("ROWOPS_GROUPNORM", form)
+    for dtype in TYPES:
+        check(2, 300, 64, 8, dtype, act)
+        check(2, 77, 30, 5, dtype, act)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_batches_of_samples_in_two_passes(dtype, monkeypatch):
+    """Three samples of more than 32 MB: one or a few at a time. Checked against
+    the same calls on each sample alone, which the other tests hold to the
+    64-bit form, and one sample against that form in sums."""
+    monkeypatch.setenv("ROWOPS_GROUPNORM", "two_pass")
+    B, S, C, G = 3, 66000, 256, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(B, S, C, generator=g, device="cuda").to(TYPES[dtype])
+    dy = torch.randn(B, S, C, generator=g, device="cuda").to(TYPES[dtype])
+    stats = torch.empty(B, G, 2, device="cuda")
+    y = ro.rowops_groupnorm_act(x, G, stats=stats)
+    dx, dw, db = ro.rowops_groupnorm_act_backward(x, dy, stats, G)
+    v = x.double().reshape(B, S, G, C // G)
+    mean = v.mean(dim=(1, 3), keepdim=True)
+    xh = (v - mean) / (v.var(dim=(1, 3), keepdim=True, correction=0) + 1e-5).sqrt()
+    q = torch.sigmoid(xh)
+    u = 2.0**-8 if dtype == "bf16" else 0
+    ref = (xh * q).reshape(B, S, C)
+    assert torch.all((y - ref).abs() <= 1e-5 * ref.abs().clamp(min=1) + u * ref.abs())
+    dz = (dy.double().reshape(v.shape) * (q + xh * q * (1 - q)))
+    # a thread adds up to 66000 / 8 positions in turn, but their signs are random: sqrt(8250) 2^-24 of the terms' rms
+    # over the square root of their number, far below 2e-5 of the sum of magnitudes
+    size = dy.double().abs().reshape(v.shape)
+    assert torch.all((db - dz.sum(dim=(0, 1)).reshape(-1)).abs() <= 2e-5 * size.sum(dim=(0, 1)).reshape(-1))
+    assert torch.all((dw - (dz * xh).sum(dim=(0, 1)).reshape(-1)).abs()
+                     <= 2e-5 * (size * xh.abs()).sum(dim=(0, 1)).reshape(-1))
+    rstd = 1 / (v.var(dim=(1, 3), keepdim=True, correction=0) + 1e-5).sqrt()
+    rdx = rstd * (dz - dz.mean(dim=(1, 3), keepdim=True) - xh * (dz * xh).mean(dim=(1, 3), keepdim=True))
+    rsize = rstd * (size + size.mean(dim=(1, 3), keepdim=True)
+                    + xh.abs() * (size * xh.abs()).mean(dim=(1, 3), keepdim=True))
+    assert torch.all((dx.reshape(v.shape) - rdx).abs() <= 2e-5 * rsize + u * rdx.abs())
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_a_wait_that_runs_out_is_reported(backward, monkeypatch):
+    """The one-kernel form's copies in: a box that never completes ends its wait
+    in a recorded timeout, and the next call is clean."""
+    assert ro.rowops_device_status() == 0
+    x, dy, w, b = make(2, 512, 64, 4, "bf16")
+    stats = torch.empty(2, 4, 2, device="cuda")
+    monkeypatch.setenv("ROWOPS_GROUPNORM", "fused")
+    clean = ro.rowops_groupnorm_act(x, 4, w, b, stats=stats)
+    cleans = ro.rowops_groupnorm_act_backward(x, dy, stats, 4, w, b)
+    assert ro.rowops_device_status() == 0
+    monkeypatch.setenv("ROWOPS_WAIT_LIMIT_NS", "20000000")
+    monkeypatch.setenv("ROWOPS_TEST_STALL_ROW", "700")
+    if backward:
+        ro.rowops_groupnorm_act_backward(x, dy, stats, 4, w, b)
+    else:
+        ro.rowops_groupnorm_act(x, 4, w, b)
+    assert ro.rowops_device_status() == 5
+    monkeypatch.delenv("ROWOPS_TEST_STALL_ROW")
+    assert torch.equal(ro.rowops_groupnorm_act(x, 4, w, b), clean)
+    for u, v in zip(ro.rowops_groupnorm_act_backward(x, dy, stats, 4, w, b), cleans):
+        assert torch.equal(u, v)
+    assert ro.rowops_device_status() == 0
