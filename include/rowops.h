@@ -74,9 +74,10 @@
  *                                 two row groups of 256 threads, or four of 128, covers a row
  *                                 with at most 32 columns a thread) or in registers (one row
  *                                 group of up to 1024 threads per CTA)
- *   ROWOPS_GROUPNORM=fused|two_pass  group norm and its backward: one kernel that holds a sample's
- *                                 groups in the shared memory of a cluster wherever they fit, or
- *                                 two passes (default: whichever a model of the time prefers)
+ *   ROWOPS_GROUPNORM=fused|stream  group norm and its backward: a sample's groups held in the
+ *                                 shared memory of a cluster wherever they fit, or streamed, the
+ *                                 second read from L2 (default: whichever a model of the time
+ *                                 prefers)
  *   ROWOPS_WAIT_LIMIT_NS=<ns>     limit of every device-side wait (default 2 s)
  *   ROWOPS_TEST_STALL_ROW=<row>   test hook for the timeout path: the wait that concerns this
  *                                 row is made to run out (the row pipeline's bulk copy of it is
@@ -435,7 +436,8 @@ rowops_status_t rowops_fused_residual_rmsnorm(const void* x, const void* residua
  *           rowops_groupnorm_act_workspace_bytes(B, S, C, G, dtype) bytes
  *           (overwritten; 0 where one kernel does it: NULL will do), apart from the
  *           other tensors; calls sharing it must be ordered on one stream.
- * C is at most 8192 (ROWOPS_ERR_UNSUPPORTED beyond) and a multiple of G. B == 0
+ * C is at most 8192 and B at most 2^30 (ROWOPS_ERR_UNSUPPORTED beyond), C a
+ * multiple of G. B == 0
  * or S == 0 is a no-op. A NaN or an infinity in a group makes that group of that
  * sample NaN. The variance is merged from centred partial sums, so a mean far
  * from zero costs it no precision.
@@ -543,7 +545,7 @@ rowops_status_t rowops_bias_dropout_residual_backward(const void* dy, void* dx, 
  *             or 8) bytes each. One outside [0, E) counts for no expert (a
  *             dropped choice); one that occurs twice in a row counts twice.
  *   mask      NULL, or T bytes: a row whose byte is 0 takes no part (padding):
- *             its logits and choices are not read.
+ *             what its logits and choices hold does not matter.
  *   loss      device pointer to one float.
  *   counts    device pointer to E + 1 int64: the experts' counts, then n. For
  *             the backward pass, and for the dispatch of the tokens.

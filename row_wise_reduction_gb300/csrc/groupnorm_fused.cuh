@@ -103,25 +103,6 @@ __device__ __forceinline__ bool gn_arrived(uint64_t* bars, int q, unsigned long 
     else return true;
 }
 
-// Sums over `lanes` consecutive lanes (a power of two).
-__device__ __forceinline__ float2 lanes_sum(float2 s, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) {
-        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-    }
-    return s;
-}
-
-// f(item, lane of its team) for items shared out to teams of `team` lanes, the whole
-// CTA in step (f holds shuffles); items at or past n: live is false.
-template <typename F>
-__device__ __forceinline__ void by_teams(int n, int team_log2, F f) {
-    for (int i0 = 0; i0 < n << team_log2; i0 += kGnBlock) {
-        const int i = i0 + int(threadIdx.x), item = i >> team_log2;
-        f(item < n ? item : 0, i & ((1 << team_log2) - 1), item < n);
-    }
-}
-
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kGnBlock, 3)
     gn_fused_kernel(const __grid_constant__ RowsMap mx, const __grid_constant__ RowsMap my, const T* x, T* y,
@@ -189,8 +170,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             s.y += fmaf(m * d, d, pq[r * f.W + ch]);
         }
         s = lanes_sum(s, 1 << f.parts_log2);
-        const float off = s.x * inv_rows, q = fmaf(-s.x, off, s.y);
-        if (live && lane == 0) col[ch] = make_float2(ref + off, q < 0.f ? 0.f : q);
+        if (live && lane == 0) col[ch] = joined(ref, s, 1.f, inv_rows);
     });
     __syncthreads();
     if (f.cluster > 1) cl.barrier_wait();
@@ -204,8 +184,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             s.y += fmaf(m * d, d, cg_[i].y);
         }
         s = lanes_sum(s, 1 << f.team_log2);
-        const float off = s.x * a.inv_L, q = fmaf(-m * s.x, off, s.y);
-        const float2 mine = k.rows ? make_float2(ref + off, q < 0.f ? 0.f : q) : f2(0.f);
+        const float2 mine = k.rows ? joined(ref, s, m, a.inv_L) : f2(0.f);
         if (live)
             for (int r = lane; r < f.cluster; r += 1 << f.team_log2)
                 *in_cta(cl, &got[k.rank * Gb + g], r, f.cluster) = mine;
@@ -219,9 +198,9 @@ __global__ void __launch_bounds__(kGnBlock, 3)
         const float2 v = got[r * Gb + g];
         const float d = v.x - ref;
         const float2 s = lanes_sum(make_float2(m * d, fmaf(m * float(a.L) * d, d, v.y)), f.cluster);
-        const float off = s.x * a.inv_S, q = fmaf(-float(a.L) * s.x, off, s.y);
         if (live && r == 0) {
-            gs[g] = make_float2(ref + off, rsqrtf((q < 0.f ? 0.f : q) * a.inv_m + a.eps));
+            const float2 v = joined(ref, s, float(a.L), a.inv_S);
+            gs[g] = make_float2(v.x, rsqrtf(v.y * a.inv_m + a.eps));
             if (stats_out && k.rank == 0) stats_out[k.sample * a.G + k.block * Gb + g] = gs[g];
         }
     });
@@ -332,10 +311,10 @@ __global__ void __launch_bounds__(kGnBlock, 2)
     else __syncthreads();
     by_teams(Gb, f.cluster_log2, [&](int g, int r, bool live) {
         const float2 s = lanes_sum(got[r * Gb + g], f.cluster);
-        if (live && r == 0) gs[g] = make_float2(-s.x / a.m, -s.y / a.m);
+        if (live && r == 0) gs[g] = make_float2(-s.x * a.inv_m, -s.y * a.inv_m);
     });
     __syncthreads();
-    if (k.active) slope.means(gs, c, a);
+    if (k.active) slope.means([&](int g) { return gs[g]; }, c, a);
     T* po = dx + k.at;
     for (int q = 0; q * f.box < k.rows; ++q) {
         const bool whole = VEC > 1 && (q + 1) * f.box <= k.rows;

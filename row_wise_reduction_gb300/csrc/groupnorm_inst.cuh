@@ -2,6 +2,7 @@
 #pragma once
 
 #include "groupnorm_fused.cuh"
+#include "groupnorm_stream.cuh"
 
 namespace rowops {
 
@@ -9,7 +10,7 @@ template <typename T, int VEC, int ACT>
 cudaError_t gn_forward_launch(const void* x, void* y, const void* w, const void* b, float* stats, void* ws, GnArgs a,
                               const GnFused* f, const LaunchCfg& cfg) {
     return f ? gn_forward_fused<T, VEC, ACT>(x, y, w, b, stats, a, *f, cfg)
-             : gn_forward_two_pass<T, VEC, ACT>(x, y, w, b, stats, ws, a, cfg);
+             : gn_forward_stream<T, VEC, ACT>(x, y, w, b, stats, ws, a, cfg);
 }
 
 template <typename T, int VEC, int ACT>
@@ -17,7 +18,7 @@ cudaError_t gn_backward_launch(const void* x, const void* dy, const void* w, con
                                void* dx, float* dw, float* db, void* ws, GnArgs a, const GnFused* f,
                                const LaunchCfg& cfg) {
     return f ? gn_backward_fused<T, VEC, ACT>(x, dy, w, b, stats, dx, dw, db, ws, a, *f, cfg)
-             : gn_backward_two_pass<T, VEC, ACT>(x, dy, w, b, stats, dx, dw, db, ws, a, cfg);
+             : gn_backward_stream<T, VEC, ACT>(x, dy, w, b, stats, dx, dw, db, ws, a, cfg);
 }
 
 template <typename T>

@@ -1,0 +1,506 @@
+// Group norm + activation and its backward for samples too large to hold: one
+// persistent kernel that reads the tensors twice, the second time from L2.
+//
+// The work is a sequence of items, each a chunk of a sample's positions: one that
+// adds up ("sums") and one that writes ("apply"). CTAs take them off the sequence
+// with a counter. An apply item stands behind all sums of its sample, by as much as
+// the CTAs have in hand, so its sample's results are there when it is taken and its
+// chunk is still in L2; sums of later samples and writes of earlier ones share
+// the memory system meanwhile. Whoever finishes a sample's last sums adds up its
+// chunks, in order. An apply item that comes too early waits (with a limit); it
+// waits for items before it in the sequence alone, and sums never wait, so the
+// waits end whatever CTAs run at the same time.
+#pragma once
+
+#include "async_ring.cuh"
+#include "groupnorm_kernels.cuh"
+#include "row_pipeline.cuh"
+
+namespace rowops {
+
+// f(words) for a thread's n positions, `step` elements apart, of N tensors: vectors
+// through a ring of copies, D positions on their way; single elements U at a time.
+template <typename T, int VEC, int D, int N, typename F>
+__device__ __forceinline__ void walk(const T* const (&from)[N], int64_t step, int n, uint4* slots, F f) {
+    using V = Vec<T, VEC>;
+    const T* p[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) p[k] = from[k];
+    if constexpr (VEC > 1) {
+        Ring<D, N, kGnBlock> ring(slots);
+        int asked = 0;
+        auto ask = [&] {
+            if (asked < n)
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    ring.ask(k, p[k]);
+                    p[k] += step;
+                }
+            ring.asked();
+            ++asked;
+        };
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d) ask();
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            ask();
+            ring.wait();
+            typename V::Word w[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) w[k] = ring.get(k);
+            f(w);
+            ring.done();
+        }
+    } else {
+        constexpr int U = 4;
+        auto batch = [&](int live) {
+            typename V::Word w[U][N];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < live)
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        w[u][k] = V::load(p[k]);
+                        p[k] += step;
+                    }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < live) f(w[u]);
+        };
+        for (; n >= U; n -= U) batch(U);
+        if (n > 0) batch(n);
+    }
+}
+template <int VEC, int D, int N>
+constexpr size_t walk_smem() {
+    return VEC > 1 ? size_t(D) * N * kGnBlock * 16 : 0;
+}
+
+// The workspace: the item counter and a counter for each sample (zeroed before
+// the kernel), results for each sample's groups, sums of each chunk's.
+struct GnStreamWs {
+    unsigned* next;
+    unsigned* done;  // [B] chunks added up; chunks + 1: the results are there
+    float2* result;  // [B][G] mean, rstd; backward -c1, -c2
+    float2* part;    // [B chunks][G]
+    float* chans;    // backward: [B chunks][2 C] sums of dz xh, dz
+    float *dw, *db;  // backward: [B] samples' channel sums, `pitch` apart
+    int64_t pitch;
+};
+
+static __global__ void gn_zero_kernel(unsigned* p, int n) {
+    grid_wait();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0u;
+}
+
+constexpr int kGnStreamDepth = 6, kGnStreamDepthBwd = 4;
+
+// Items of the sequence: `lag` sums, then apply and sums in turn, then apply.
+struct GnItem {
+    bool apply;
+    int sample, chunk;
+    __device__ __forceinline__ GnItem(unsigned i, const GnArgs& a) {
+        const unsigned N = unsigned(a.B) * a.chunks, lag = unsigned(a.lag);
+        unsigned k = i;
+        apply = false;
+        if (i >= lag) {
+            const unsigned j = i - lag;
+            if (j < 2 * (N - lag)) {
+                apply = !(j & 1);
+                k = apply ? j >> 1 : lag + (j >> 1);
+            } else {
+                apply = true;
+                k = j - (N - lag);
+            }
+        }
+        sample = int(k / unsigned(a.chunks));
+        chunk = int(k - unsigned(sample) * a.chunks);
+        if (apply) chunk = a.chunks - 1 - chunk;  // what was read last first
+    }
+};
+
+// The thread's share of an item.
+struct GnShare {
+    int tx, ty, n, rows;   // n: its positions; rows: the chunk's
+    int64_t first, step;   // element offsets of its first position (channel 0), between them
+    __device__ __forceinline__ GnShare(const GnArgs& a, const GnItem& it) {
+        ty = int(threadIdx.x) * a.inv_tx >> 16;
+        tx = int(threadIdx.x) - ty * a.tx;
+        const int64_t r0 = int64_t(it.chunk) * a.chunk_rows, left = a.S - r0;
+        rows = int(left < a.chunk_rows ? left : a.chunk_rows);
+        n = ty < a.ty && rows > ty ? (rows - ty + a.ty - 1) / a.ty : 0;
+        first = (int64_t(it.sample) * a.S + r0 + ty) * a.ld;
+        step = int64_t(a.ty) * a.ld;
+    }
+};
+
+// Thread 0 has counted the CTA's sums in; true in every thread where they were the
+// sample's last.
+__device__ __forceinline__ bool gn_last(unsigned* done, int chunks, unsigned* word) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        *word = atomicAdd(done, 1u);
+    }
+    __syncthreads();
+    if (*word != unsigned(chunks - 1)) return false;
+    __threadfence();
+    return true;
+}
+
+// Every thread of the CTA: the sample's results are there; false where the wait ran out.
+__device__ __forceinline__ bool gn_ready(const unsigned* done, unsigned want, unsigned long long wait_ns) {
+    int ok = 1;
+    if (threadIdx.x == 0) {
+        auto there = [&] {
+            unsigned v;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+            return v == want;
+        };
+        if (!there()) {
+            const unsigned long long t0 = global_ns();
+            ok = 0;
+            for (uint32_t i = 0; i < (1u << 26) && !ok; ++i) {
+                __nanosleep(100);
+                ok = there();
+                if (!ok && global_ns() - t0 > wait_ns) break;
+            }
+        }
+    }
+    return __syncthreads_and(ok);
+}
+
+// The sequence's items, one after the other: sums(item, share), which leaves a chunk's
+// sums, last(sample), which joins a sample's, and apply(item, share).
+template <typename Sums, typename Last, typename Apply>
+__device__ __forceinline__ void gn_sequence(const GnArgs& a, const GnStreamWs& ws, unsigned* err,
+                                            unsigned long long wait_ns, int stall, Sums sums, Last last,
+                                            Apply apply) {
+    __shared__ unsigned word[2];
+    const int t = threadIdx.x;
+    grid_wait();
+    if (t == 0) word[0] = atomicAdd(ws.next, 1u);
+    __syncthreads();
+    const unsigned items = 2u * unsigned(a.B) * unsigned(a.chunks);
+    for (unsigned i = word[0]; i < items;) {
+        // the next one while this one is worked on, but where a CTA has only a few:
+        // it would keep a second one from a CTA that has none
+        unsigned after = 0;
+        if (t == 0 && a.early) after = atomicAdd(ws.next, 1u);
+        const GnItem it(i, a);
+        const GnShare k(a, it);
+        if (it.apply) {
+            if (gn_ready(&ws.done[it.sample], unsigned(a.chunks) + 1u, wait_ns)) apply(it, k);
+            else if (t == 0) atomicExch(err, kDeviceErrTimeout);
+        } else {
+            sums(it, k);
+            if (gn_last(&ws.done[it.sample], a.chunks, &word[1])) {
+                last(it.sample);
+                __syncthreads();
+                if (t == 0 && it.sample != stall) {
+                    __threadfence();
+                    atomicExch(&ws.done[it.sample], unsigned(a.chunks) + 1u);
+                }
+            }
+        }
+        if (t == 0 && !a.early) after = atomicAdd(ws.next, 1u);
+        __syncthreads();
+        if (t == 0) word[0] = after;
+        __syncthreads();
+        i = word[0];
+    }
+}
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnBlock, 3)
+    gn_stream_kernel(const T* x, T* y, const T* w, const T* b, float2* stats_out, const __grid_constant__ GnStreamWs ws,
+                     const __grid_constant__ GnArgs a, unsigned* err, unsigned long long wait_ns, int stall) {
+    using V = Vec<T, VEC>;
+    constexpr int P = V::P, D = kGnStreamDepth;
+    extern __shared__ __align__(16) uint4 slots[];  // the positions on their way, then:
+    const int W = a.tx * VEC;
+    float* pm = reinterpret_cast<float*>(slots) + walk_smem<VEC, D, 1>() / 4;  // [ty][W] the threads' means
+    float* pq = pm + a.ty * W;                               // [ty][W] and squares
+    float2* col = reinterpret_cast<float2*>(pq + a.ty * W);  // [C] the channels'
+    auto sums = [&](const GnItem& it, const GnShare& k) {
+        const float inv_rows = 1.f / float(k.rows);
+        for (int tile = 0; tile < a.tiles; ++tile) {
+            const int c0 = tile * W, c = c0 + k.tx * VEC;
+            Shifted<P> s;
+            s.clear();
+            if (k.n > 0 && c < a.C) {
+                const T* const from[1] = {x + k.first + c};
+                bool first = true;
+                walk<T, VEC, D>(from, k.step, k.n, slots, [&](const typename V::Word (&wd)[1]) {
+                    float2 v[P];
+                    V::get(wd[0], v);
+                    if (first) s.start(v);
+                    first = false;
+                    s.add(v);
+                });
+            }
+            if (k.ty < a.ty)
+                s.template leave<VEC>(c < a.C ? k.n : 0, pm + k.ty * W + k.tx * VEC, pq + k.ty * W + k.tx * VEC);
+            __syncthreads();
+            const int each = k.rows / a.ty, more = k.rows - each * a.ty;  // positions of row r: each + (r < more)
+            by_teams(min(W, a.C - c0), a.parts_log2, [&](int ch, int lane, bool live) {
+                const float ref = pm[ch];
+                float2 s2 = f2(0.f);
+                for (int r = lane; r < a.ty; r += 1 << a.parts_log2) {
+                    const float m = float(each + (r < more)), d = pm[r * W + ch] - ref;
+                    s2.x = fmaf(m, d, s2.x);
+                    s2.y += fmaf(m * d, d, pq[r * W + ch]);
+                }
+                s2 = lanes_sum(s2, 1 << a.parts_log2);
+                if (live && lane == 0) col[c0 + ch] = joined(ref, s2, 1.f, inv_rows);
+            });
+            __syncthreads();
+        }
+        float2* out = ws.part + (int64_t(it.sample) * a.chunks + it.chunk) * a.G;
+        by_teams(a.G, a.team_log2, [&](int g, int lane, bool live) {
+            const float2* cg_ = col + g * a.L;
+            const float ref = cg_[0].x, m = float(k.rows);
+            float2 s = f2(0.f);
+            for (int i = lane; i < a.L; i += 1 << a.team_log2) {
+                const float d = cg_[i].x - ref;
+                s.x += d;
+                s.y += fmaf(m * d, d, cg_[i].y);
+            }
+            s = lanes_sum(s, 1 << a.team_log2);
+            if (live && lane == 0) out[g] = joined(ref, s, m, a.inv_L);
+        });
+    };
+    auto last = [&](int sample) {
+        by_teams(a.G, a.last_log2, [&](int g, int lane, bool live) {
+            const float2* p = ws.part + int64_t(sample) * a.chunks * a.G + g;
+            const float ref = __ldcg(p).x;
+            float2 s = f2(0.f);
+#pragma unroll 8
+            for (int i = lane; i < a.chunks; i += 1 << a.last_log2) {
+                const float2 v = __ldcg(p + int64_t(i) * a.G);
+                const int64_t left = a.S - i * a.chunk_rows;
+                const float m = float(left < a.chunk_rows ? left : a.chunk_rows), d = v.x - ref;
+                s.x = fmaf(m, d, s.x);
+                s.y += fmaf(m * float(a.L) * d, d, v.y);
+            }
+            s = lanes_sum(s, 1 << a.last_log2);
+            if (live && lane == 0) {
+                const float2 v = joined(ref, s, float(a.L), a.inv_S);
+                const float2 r = make_float2(v.x, rsqrtf(v.y * a.inv_m + a.eps));
+                ws.result[int64_t(sample) * a.G + g] = r;
+                if (stats_out) stats_out[int64_t(sample) * a.G + g] = r;
+            }
+        });
+    };
+    auto apply = [&](const GnItem& it, const GnShare& k) {
+        if (k.n == 0) return;
+        for (int tile = 0; tile < a.tiles; ++tile) {
+            const int c = (tile * a.tx + k.tx) * VEC;
+            if (c >= a.C) continue;
+            const Groups<VEC> g(c, a);
+            const float2* res = ws.result + int64_t(it.sample) * a.G;
+            float2 mean[P], mul[P], add[P], rstd[P];
+            load_affine<T, VEC>(w, c, 1.f, mul);
+            load_affine<T, VEC>(b, c, 0.f, add);
+            each_channel<VEC>(mean, [&](int e) { return -__ldcg(&res[g.g[e]]).x; });
+            each_channel<VEC>(rstd, [&](int e) { return __ldcg(&res[g.g[e]]).y; });
+#pragma unroll
+            for (int j = 0; j < P; ++j) mul[j] = f2_mul(mul[j], rstd[j]);
+            const T* const from[1] = {x + k.first + c};
+            T* py = y + k.first + c;
+            walk<T, VEC, D>(from, k.step, k.n, slots, [&](const typename V::Word (&wd)[1]) {
+                float2 v[P];
+                V::get(wd[0], v);
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[j] = act_of2<ACT>(f2_fma(f2_add(v[j], mean[j]), mul[j], add[j]));
+                V::put(py, v);
+                py += k.step;
+            });
+        }
+    };
+    gn_sequence(a, ws, err, wait_ns, stall, sums, last, apply);
+}
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kGnBlock, 2)
+    gn_bwd_stream_kernel(const T* x, const T* dy, T* dx, const T* w, const T* b, const float2* stats,
+                         const __grid_constant__ GnStreamWs ws, const __grid_constant__ GnArgs a, unsigned* err,
+                         unsigned long long wait_ns, int stall) {
+    using E = Elem<T>;
+    using V = Vec<T, VEC>;
+    constexpr int P = V::P, D = kGnStreamDepthBwd;
+    extern __shared__ __align__(16) uint4 slots[];  // the positions on their way, then:
+    const int t = threadIdx.x, W = a.tx * VEC;
+    float2* red = reinterpret_cast<float2*>(slots) + walk_smem<VEC, D, 2>() / 8;  // [ty][W] the threads' A, Q
+    float2* col = red + a.ty * W;  // [C] the channels', times w
+    auto sums = [&](const GnItem& it, const GnShare& k) {
+        const int64_t slot = int64_t(it.sample) * a.chunks + it.chunk;
+        float* cw = ws.chans + slot * 2 * a.C;
+        for (int tile = 0; tile < a.tiles; ++tile) {
+            const int c0 = tile * W, c = c0 + k.tx * VEC;
+            GnSlope<T, VEC, ACT> slope;
+            float2 sa[P], sq[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) sa[j] = sq[j] = slope.rstd[j] = f2(0.f);
+            if (k.n > 0 && c < a.C) {
+                slope.load(w, b, stats + int64_t(it.sample) * a.G, c, c, a);
+                const T* const from[2] = {x + k.first + c, dy + k.first + c};
+                walk<T, VEC, D>(from, k.step, k.n, slots,
+                                [&](const typename V::Word (&wd)[2]) { slope.add(wd[0], wd[1], sa, sq); });
+            }
+            if (k.ty < a.ty) slope.leave(sa, sq, red + k.ty * W + k.tx * VEC);
+            __syncthreads();
+            by_teams(min(W, a.C - c0), a.parts_log2, [&](int ch, int lane, bool live) {
+                float2 s = f2(0.f);
+                for (int r = lane; r < a.ty; r += 1 << a.parts_log2) s = f2_add(s, red[r * W + ch]);
+                s = lanes_sum(s, 1 << a.parts_log2);
+                if (live && lane == 0) {
+                    cw[c0 + ch] = s.y;
+                    cw[a.C + c0 + ch] = s.x;
+                    const float wv = w ? E::load(w + c0 + ch) : 1.f;
+                    col[c0 + ch] = make_float2(wv * s.x, wv * s.y);
+                }
+            });
+            __syncthreads();
+        }
+        by_teams(a.G, a.team_log2, [&](int g, int lane, bool live) {
+            float2 s = f2(0.f);
+            for (int i = lane; i < a.L; i += 1 << a.team_log2) s = f2_add(s, col[g * a.L + i]);
+            s = lanes_sum(s, 1 << a.team_log2);
+            if (live && lane == 0) ws.part[slot * a.G + g] = s;
+        });
+    };
+    auto last = [&](int sample) {
+        by_teams(a.G, a.last_log2, [&](int g, int lane, bool live) {
+            const float2* p = ws.part + int64_t(sample) * a.chunks * a.G + g;
+            float2 s = f2(0.f);
+#pragma unroll 8
+            for (int i = lane; i < a.chunks; i += 1 << a.last_log2) s = f2_add(s, __ldcg(p + int64_t(i) * a.G));
+            s = lanes_sum(s, 1 << a.last_log2);
+            if (live && lane == 0) ws.result[int64_t(sample) * a.G + g] = make_float2(-s.x * a.inv_m, -s.y * a.inv_m);
+        });
+        for (int c = t; c < 2 * a.C; c += kGnBlock) {
+            const float* p = ws.chans + int64_t(sample) * a.chunks * 2 * a.C + c;
+            float s = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < a.chunks; ++i) s += __ldcg(p + int64_t(i) * 2 * a.C);
+            (c < a.C ? ws.dw[sample * ws.pitch + c] : ws.db[sample * ws.pitch + c - a.C]) = s;
+        }
+    };
+    auto apply = [&](const GnItem& it, const GnShare& k) {
+        if (k.n == 0) return;
+        for (int tile = 0; tile < a.tiles; ++tile) {
+            const int c = (tile * a.tx + k.tx) * VEC;
+            if (c >= a.C) continue;
+            GnSlope<T, VEC, ACT> slope;
+            slope.load(w, b, stats + int64_t(it.sample) * a.G, c, c, a);
+            // past L1: another SM wrote them during this kernel
+            const float2* res = ws.result + int64_t(it.sample) * a.G;
+            slope.means([&](int g) { return __ldcg(&res[g]); }, c, a);
+            const T* const from[2] = {x + k.first + c, dy + k.first + c};
+            T* po = dx + k.first + c;
+            walk<T, VEC, D>(from, k.step, k.n, slots, [&](const typename V::Word (&wd)[2]) {
+                float2 v[P];
+                slope.of(wd[0], wd[1], v);
+                V::put(po, v);
+                po += k.step;
+            });
+        }
+    };
+    gn_sequence(a, ws, err, wait_ns, stall, sums, last, apply);
+}
+
+// ---- launchers -------------------------------------------------------------
+// A launch that may start while the one before it drains: every kernel here waits
+// for that one before it touches memory.
+inline cudaError_t gn_launch(const void* kern, int grid, int block, size_t smem, const LaunchCfg& cfg, void** args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(grid));
+    lc.blockDim = dim3(unsigned(block));
+    lc.dynamicSmemBytes = smem;
+    lc.stream = cfg.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelExC(&lc, kern, args);
+}
+
+// Channel vectors side by side: all of them where they fit the CTA, else equal tiles.
+inline void gn_tiles(GnArgs& a, int vec) {
+    auto log2_floor = [](int v) {
+        int l = 0;
+        while (v > 1) v >>= 1, ++l;
+        return l;
+    };
+    const int nv = (a.C + vec - 1) / vec;
+    a.tiles = (nv + kGnBlock - 1) / kGnBlock;
+    a.tx = (nv + a.tiles - 1) / a.tiles;
+    a.ty = kGnBlock / a.tx;
+    a.inv_tx = (65536 + a.tx - 1) / a.tx;
+    a.parts_log2 = std::min(5, log2_floor(std::max(1, std::min(kGnBlock / (a.tx * vec), a.ty))));
+    a.last_log2 = std::min(5, log2_floor(kGnBlock / std::min(kGnBlock, a.G)));
+    a.team_log2 = std::min(a.last_log2, log2_floor(2 * a.L - 1));
+}
+
+// Lays out the workspace, zeroes its counters and launches the kernel.
+inline cudaError_t gn_stream_launch(const void* kern, GnArgs& a, GnStreamWs& ws, void* workspace, int vec, size_t smem,
+                                    bool backward, void** args, const LaunchCfg& cfg) {
+    cudaError_t e = allow_smem(kern, smem, cfg);
+    if (e != cudaSuccess) return e;
+    const int64_t N = int64_t(a.B) * a.chunks;
+    const int grid = grid_for(kern, kGnBlock, smem, 2 * N, cfg);
+    a.lag = int(std::min<int64_t>(N, int64_t(a.chunks) + grid));
+    a.early = 2 * N >= 8 * int64_t(grid);
+    char* p = static_cast<char*>(workspace);
+    ws.next = reinterpret_cast<unsigned*>(p);
+    ws.done = ws.next + 1;
+    p += gn_counter_bytes(a.B);
+    ws.result = reinterpret_cast<float2*>(p);
+    ws.part = ws.result + int64_t(a.B) * a.G;
+    if (backward) ws.chans = reinterpret_cast<float*>(ws.part + N * a.G);
+    unsigned* counters = ws.next;
+    int n = a.B + 1;
+    void* zero_args[] = {&counters, &n};
+    e = gn_launch(reinterpret_cast<const void*>(gn_zero_kernel), 1, 1024, 0, cfg, zero_args);
+    return e == cudaSuccess ? gn_launch(kern, grid, kGnBlock, smem, cfg, args) : e;
+}
+
+template <typename T, int VEC, int ACT>
+cudaError_t gn_forward_stream(const void* x, void* y, const void* w, const void* b, float* stats, void* workspace,
+                              GnArgs a, const LaunchCfg& cfg) {
+    gn_tiles(a, VEC);
+    GnStreamWs ws{};
+    unsigned* err = cfg.dev_error;
+    unsigned long long wait_ns = cfg.wait_ns;
+    int stall = cfg.stall_row < 0 ? -1 : int(cfg.stall_row / a.S);
+    void* args[] = {&x, &y, &w, &b, &stats, &ws, &a, &err, &wait_ns, &stall};
+    return gn_stream_launch(reinterpret_cast<const void*>(gn_stream_kernel<T, VEC, ACT>), a, ws, workspace, VEC,
+                            walk_smem<VEC, kGnStreamDepth, 1>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C), false, args,
+                            cfg);
+}
+
+template <typename T, int VEC, int ACT>
+cudaError_t gn_backward_stream(const void* x, const void* dy, const void* w, const void* b, const float* stats,
+                               void* dx, float* dw, float* db, void* workspace, GnArgs a, const LaunchCfg& cfg) {
+    gn_tiles(a, VEC);
+    GnStreamWs ws{};
+    // one sample's channel sums are the result
+    float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + gn_counter_bytes(a.B)) +
+                  2 * (int64_t(a.B) * a.G + int64_t(a.B) * a.chunks * a.G) + int64_t(a.B) * a.chunks * 2 * a.C;
+    ws.dw = a.B == 1 ? dw : sums;
+    ws.db = a.B == 1 ? db : sums + a.C;
+    ws.pitch = 2 * int64_t(a.C);
+    unsigned* err = cfg.dev_error;
+    unsigned long long wait_ns = cfg.wait_ns;
+    int stall = cfg.stall_row < 0 ? -1 : int(cfg.stall_row / a.S);
+    void* args[] = {&x, &dy, &dx, &w, &b, &stats, &ws, &a, &err, &wait_ns, &stall};
+    const cudaError_t e =
+        gn_stream_launch(reinterpret_cast<const void*>(gn_bwd_stream_kernel<T, VEC, ACT>), a, ws, workspace, VEC,
+                         walk_smem<VEC, kGnStreamDepthBwd, 2>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C), true, args,
+                         cfg);
+    return e == cudaSuccess && a.B > 1 ? gn_reduce_channels(sums, a.B, a.C, dw, db, cfg) : e;
+}
+
+}  // namespace rowops

@@ -10,13 +10,24 @@
 
 namespace rowops {
 
-__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint2 k) {
+// The rounds' keys: key + round (golden ratio, sqrt(3) - 1), computed once on the host
+// and read from the kernel's arguments, so a round is four instructions.
+struct PhiloxKeys {
+    uint2 k[10];
+    __host__ explicit PhiloxKeys(uint64_t key) {
+        for (unsigned r = 0; r < 10; ++r) {
+            k[r].x = uint32_t(key) + r * 0x9E3779B9u;
+            k[r].y = uint32_t(key >> 32) + r * 0xBB67AE85u;
+        }
+    }
+};
+
+__device__ __forceinline__ uint4 philox4x32_10(uint4 c, const PhiloxKeys& keys) {
 #pragma unroll
     for (int round = 0; round < 10; ++round) {
         const uint64_t a = uint64_t(0xD2511F53u) * c.x, b = uint64_t(0xCD9E8D57u) * c.z;
-        c = make_uint4(uint32_t(b >> 32) ^ c.y ^ k.x, uint32_t(b), uint32_t(a >> 32) ^ c.w ^ k.y, uint32_t(a));
-        k.x += 0x9E3779B9u;
-        k.y += 0xBB67AE85u;
+        c = make_uint4(uint32_t(b >> 32) ^ c.y ^ keys.k[round].x, uint32_t(b),
+                       uint32_t(a >> 32) ^ c.w ^ keys.k[round].y, uint32_t(a));
     }
     return c;
 }

@@ -42,7 +42,7 @@ struct Tuning {
     long long stall_row = -1; // test hook (see include/rowops.h)
     int sched = 0;            // full-row pipelines: 0 automatic, 1 static, 2 dynamic (cluster launch control)
     int unit_rows = 0;        // dynamic schedule: rows per group in a work unit (0: automatic)
-    int groupnorm = 0;        // group norm: 0 automatic, 1 one kernel where it can, 2 two passes
+    int groupnorm = 0;        // group norm: 0 automatic, 1 slabs held where they fit, 2 streamed
     int bwd = 0;              // LayerNorm+GELU backward partials: 0 automatic, 1 registers, 2 tensor memory
 };
 
@@ -84,7 +84,7 @@ Tuning read_tuning() {
         else if (is("UNIT_ROWS")) t.unit_rows = int(parse_int(v, 0));
         else if (is("SCHED")) t.sched = !std::strcmp(v, "static") ? 1 : (!std::strcmp(v, "dynamic") ? 2 : 0);
         else if (is("BWD_PARTIALS")) t.bwd = !std::strcmp(v, "registers") ? 1 : (!std::strcmp(v, "tmem") ? 2 : 0);
-        else if (is("GROUPNORM")) t.groupnorm = !std::strcmp(v, "fused") ? 1 : (!std::strcmp(v, "two_pass") ? 2 : 0);
+        else if (is("GROUPNORM")) t.groupnorm = !std::strcmp(v, "fused") ? 1 : (!std::strcmp(v, "stream") ? 2 : 0);
         else if (is("ONLINE"))
             t.online = !std::strcmp(v, "two_pass") ? 1
                      : !std::strcmp(v, "single_read") ? 2
@@ -494,6 +494,31 @@ int ctas_per_sm(const void* func, int block, size_t smem, const LaunchCfg& cfg) 
         n = 0;
     }
     g_occ.push_back(OccEntry{func, cfg.ctx, block, smem, n});
+    return n;
+}
+
+int clusters_on_device(const void* func, int block, size_t smem, int cluster, const LaunchCfg& cfg) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    const int key = -cluster * 4096 - block;  // apart from the entries of single CTAs
+    for (auto& o : g_occ)
+        if (o.func == func && o.ctx == cfg.ctx && o.block == key && o.smem == smem) return o.blocks_per_sm;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(cluster));
+    lc.blockDim = dim3(unsigned(block));
+    lc.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, func, &lc) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    if (n < 1) n = 1;
+    g_occ.push_back(OccEntry{func, cfg.ctx, key, smem, n});
     return n;
 }
 
@@ -1089,13 +1114,13 @@ rowops_status_t zero(float* p, int64_t n, cudaStream_t stream) {
 // Group norm: the shape's checks; M = B S rows.
 rowops_status_t check_groups(int64_t B, int64_t S, int64_t C, int64_t G, rowops_dtype_t dtype, int64_t* M) {
     if (!valid_dtype(dtype) || B < 0 || S < 0 || C < 1 || G < 1 || C % G != 0) return ROWOPS_ERR_INVALID_VALUE;
-    if (C > kGnMaxChannels || B > INT32_MAX || (S > 0 && B > INT64_MAX / 16 / kGnMaxChannels / S))
+    if (C > kGnMaxChannels || B > (int64_t(1) << 30) || (S > 0 && B > INT64_MAX / 16 / kGnMaxChannels / S))
         return ROWOPS_ERR_UNSUPPORTED;
     *M = B * S;
     return ROWOPS_OK;
 }
 
-// One kernel or two passes: what the model of the time says (vec: channels of an
+// Slabs held in shared memory or streamed: what the model of the time says (vec: channels of an
 // access). The last shapes' answers are kept per thread: the model tries some
 // thirty splits, a microsecond of a call that takes a few.
 struct GnChoice {
@@ -1116,21 +1141,20 @@ const GnChoice& gn_choose(int64_t B, int64_t S, int64_t C, int64_t G, int es, in
     k.B = B, k.S = S, k.C = C, k.G = G, k.es = es, k.tensors = tensors, k.vec = vec, k.knob = knob;
     const GnArgs a = gn_plan(B, S, C, G, C, es, tensors, 0.f);
     const double one = knob == 2 ? -1.0 : gn_fused_plan(a, es, tensors, vec, &k.f);
-    k.one = one >= 0 && (knob == 1 || one <= gn_two_pass_time(a, es, tensors));
+    k.one = one >= 0 && (knob == 1 || one <= gn_stream_time(a, es, tensors));
     return k;
 }
 
 // A workspace for whichever width of access the call's alignment allows. One
-// kernel: none forward, backward two sums for the channels of every CTA of a
-// cluster. Two passes: a mean and a sum of squares for every chunk's groups;
-// backward two sums for its groups and channels.
+// kernel that holds its slabs: none forward, backward two sums for the channels of
+// every CTA of a cluster.
 size_t gn_bytes(int64_t B, int64_t S, int64_t C, int64_t G, int es, int tensors, int knob) {
     size_t most = 0;
     for (const int vec : {1, 16 / es}) {
         if (C % vec) continue;
         const GnChoice& k = gn_choose(B, S, C, G, es, tensors, vec, knob);
-        const size_t rows = size_t(B) * (k.one ? k.f.cluster : gn_plan(B, S, C, G, C, es, tensors, 0.f).chunks);
-        most = std::max(most, rows * ((k.one ? 0 : size_t(G)) + (tensors > 1 ? size_t(C) : 0)) * 8);
+        most = std::max(most, !k.one ? gn_stream_bytes(gn_plan(B, S, C, G, C, es, tensors, 0.f), tensors)
+                              : tensors > 1 ? size_t(B) * k.f.cluster * C * 8 : 0);
     }
     return most;
 }
@@ -1255,7 +1279,7 @@ rowops_status_t rowops_bias_dropout_residual(const void* x, const void* residual
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
     const bool vec = vector_rows(tn, N, ld, es, {x, y, residual});
     const DropoutLaunch fn = dtype == ROWOPS_F32 ? dropout_f32() : dropout_bf16();
-    return finish(fn(x, residual, bias, y, nullptr, 0, nullptr, M, N, ld, mask, vec, cfg));
+    return finish(fn(x, residual, bias, y, nullptr, 0, nullptr, M, N, ld, mask, vec, tn.family == Family::Looped, cfg));
 }
 
 size_t rowops_bias_dropout_residual_backward_workspace_bytes(int64_t M, int64_t N, rowops_dtype_t dtype) {
@@ -1293,7 +1317,8 @@ rowops_status_t rowops_bias_dropout_residual_backward(const void* dy, void* dx, 
     const bool vec = vector_rows(tn, N, ld, es, {dy, dx});
     const int most = int(std::min<int64_t>(M, bwd_max_partials(N)));
     const DropoutLaunch fn = dtype == ROWOPS_F32 ? dropout_f32() : dropout_bf16();
-    return finish(fn(dy, nullptr, nullptr, dx, static_cast<float*>(workspace), most, dbias, M, N, ld, mask, vec, cfg));
+    return finish(fn(dy, nullptr, nullptr, dx, static_cast<float*>(workspace), most, dbias, M, N, ld, mask, vec,
+                     tn.family == Family::Looped, cfg));
 }
 
 size_t rowops_router_balance_loss_workspace_bytes(int64_t T, int64_t E, rowops_dtype_t dtype) {

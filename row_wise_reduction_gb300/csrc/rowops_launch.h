@@ -61,6 +61,10 @@ inline int cap_ctas(int grid, int cap, const LaunchCfg& cfg) {
 // CTAs of `func` one SM can hold at once (occupancy API, cached per device).
 int ctas_per_sm(const void* func, int block, size_t smem, const LaunchCfg& cfg);
 
+// Clusters of `cluster` CTAs of `func` the device can hold at once (cached): fewer than
+// its SMs' places allow, as a cluster stays within one GPC.
+int clusters_on_device(const void* func, int block, size_t smem, int cluster, const LaunchCfg& cfg);
+
 // Allow `func` to use `smem` bytes of dynamic shared memory (once per device).
 // max_carveout: also ask for the largest shared-memory carveout (for kernels
 // with a small ring per CTA, where the driver's own choice held fewer CTAs per
@@ -227,7 +231,8 @@ ReduceLaunch reduce_looped_bf16(int op);
 
 // Bias + dropout + residual (r, b may be NULL), and with db (N floats) the
 // column sums of the dropped-out rows, by way of at most max_partials rows of N
-// floats in `part`. drop: round(65536 p).
+// floats in `part`. drop: round(65536 p). vec: 16-byte vectors throughout; else,
+// with elements, single elements alone.
 struct DropoutMask {
     unsigned drop;
     uint64_t seed, offset;
@@ -235,7 +240,7 @@ struct DropoutMask {
 };
 using DropoutLaunch = cudaError_t (*)(const void* x, const void* r, const void* b, void* y, float* part,
                                       int max_partials, float* db, int64_t M, int64_t N, int64_t ld,
-                                      const DropoutMask& mask, bool vec, const LaunchCfg& cfg);
+                                      const DropoutMask& mask, bool vec, bool elements, const LaunchCfg& cfg);
 DropoutLaunch dropout_f32();
 DropoutLaunch dropout_bf16();
 
@@ -258,42 +263,45 @@ BalanceBackwardLaunch balance_backward_bf16();
 
 // Group norm + activation on channels-last data and its backward.
 constexpr int kGnMaxChannels = 8192;
-constexpr int kGnBlock = 256;                      // threads of a CTA: the fused form and pass 2
-constexpr int kGnWide = 1024, kGnWideBwd = 512;    // pass 1, forward and backward
+constexpr int kGnBlock = 256;
 constexpr int kGnSms = 152;
 constexpr size_t kGnSmem = 227 * 1024;
 struct GnArgs {
     int64_t S, ld;
     int B, C, G, L;  // L = C / G channels of a group
-    float eps, m;    // m = S L elements of a group
-    float inv_L, inv_S, inv_m;
-    // the two-pass form
-    int tx, tiles;       // channel vectors side by side, and how many times
-    int64_t batch, b0;   // samples of a batch; its first
-    int chunks;          // CTAs of pass 1 a sample
-    int64_t chunk_rows;  // their positions
-    int64_t rows;        // positions of a CTA of pass 2
+    float eps;
+    float inv_L, inv_S, inv_m;  // m = S L elements of a group
+    // the streaming form
+    int tx, ty, tiles, inv_tx;  // channel vectors side by side, positions at a time, tiles; 2^16 / tx
+    int parts_log2, team_log2, last_log2;  // lanes that add up a channel, a group, a group's chunks
+    int chunks, lag;            // of a sample; sums before the first apply
+    bool early;                 // CTAs take their next item ahead
+    int64_t chunk_rows;         // positions of a chunk
 };
 
-// The two-pass form takes batches of samples that stay in L2 between the passes
-// (64 MB of 129). In each, every SM gets as many CTAs as it holds at once (a
-// grid of 1.3 waves took the time of two): one of pass 1, three (backward two) of
-// pass 2, of at least 16 KiB. Pass 1 leaves at most 16384 group sums a sample: a
-// CTA of pass 2 reads all of its sample's.
-constexpr int64_t kGnBatchBytes = int64_t(64) << 20;
+// The streaming form's chunks: of about 128 KiB, whole waves of CTAs where there are
+// few (two CTAs for each SM backward, three forward), at least 16 KiB.
 inline GnArgs gn_plan(int64_t B, int64_t S, int64_t C, int64_t G, int64_t ld, int es, int tensors, float eps) {
     GnArgs a{};
     a.S = S, a.ld = ld, a.B = int(B), a.C = int(C), a.G = int(G), a.L = int(C / G), a.eps = eps;
-    a.m = float(S) * float(a.L), a.inv_L = 1.f / a.L, a.inv_S = float(1.0 / S), a.inv_m = float(1.0 / (double(S) * a.L));
-    a.batch = std::min(B, std::max(int64_t(1), kGnBatchBytes / (S * C * es * tensors)));
-    const int64_t least = (16384 + C * es * tensors - 1) / (C * es * tensors);
-    auto chunks = [&](int64_t ctas) { return std::min(std::max(int64_t(1), ctas / a.batch), (S + least - 1) / least); };
-    int64_t n = std::min(chunks(kGnSms), std::max(int64_t(1), 16384 / G));
+    a.inv_L = 1.f / a.L, a.inv_S = float(1.0 / S), a.inv_m = float(1.0 / (double(S) * a.L));
+    const double sample = double(S) * C * es * tensors;
+    const int64_t ctas = (tensors > 1 ? 2 : 3) * kGnSms;
+    int64_t n = int64_t(std::ceil(sample / (128.0 * 1024)));
+    if (B * n < 4 * ctas) n = std::max(int64_t(1), std::max(int64_t(1), B * n / ctas) * ctas / B);
+    n = std::min(n, std::max(int64_t(1), int64_t(sample / 16384)));
+    n = std::min(n, S);
+    n = std::min(n, std::max(int64_t(1), (int64_t(1) << 30) / B));  // items are counted in 32 bits
     a.chunk_rows = (S + n - 1) / n;
     a.chunks = int((S + a.chunk_rows - 1) / a.chunk_rows);
-    n = chunks((tensors > 1 ? 2 : 3) * kGnSms);
-    a.rows = (S + n - 1) / n;
     return a;
+}
+inline size_t gn_counter_bytes(int64_t B) { return size_t((B + 1) * 4 + 255) / 256 * 256; }
+// Workspace: counters; results of the samples' groups, sums of the chunks'; backward
+// the chunks' and samples' channel sums.
+inline size_t gn_stream_bytes(const GnArgs& a, int tensors) {
+    const size_t B = a.B, N = B * a.chunks;
+    return gn_counter_bytes(a.B) + (B + N) * a.G * 8 + (tensors > 1 ? (B + N) * a.C * 8 : 0);
 }
 
 // A tensor map for boxes of a matrix's rows (128 bytes, a CUtensorMap).
@@ -383,11 +391,11 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
     return least;
 }
 
-// The two-pass form's modelled time: its launches, the first read, and the second
-// at twice the copy rate next to the writes.
-inline double gn_two_pass_time(const GnArgs& a, int es, int tensors) {
+// The streaming form's modelled time: a launch, the zeroing and the end of the sums,
+// and the traffic, the second read at twice the copy rate.
+inline double gn_stream_time(const GnArgs& a, int es, int tensors) {
     const double in = double(a.B) * a.S * a.C * es * tensors;
-    return std::ceil(double(a.B) / a.batch) * 5.0 + (1.5 * in + in / tensors) / 6.8e6;
+    return 7.0 + (1.5 * in + in / tensors) / 6.8e6;
 }
 
 using GnForwardLaunch = cudaError_t (*)(const void* x, void* y, const void* w, const void* b, float* stats, void* ws,

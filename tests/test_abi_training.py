@@ -20,7 +20,7 @@ def lib():
 def test_groupnorm_refusals(lib, monkeypatch):
     q = lib.rowops_groupnorm_act_workspace_bytes
     assert q(2, 16, 64, 8, F32) == 0  # one kernel: no workspace
-    monkeypatch.setenv("ROWOPS_GROUPNORM", "two_pass")
+    monkeypatch.setenv("ROWOPS_GROUPNORM", "stream")
     f, q = lib.rowops_groupnorm_act, lib.rowops_groupnorm_act_workspace_bytes
     need = q(2, 16, 64, 8, F32)
     assert need > 0 and q(0, 16, 64, 8, F32) == 0 and q(2, 16, 64, 7, F32) == 0 and q(2, 16, 64, 8, 5) == 0
@@ -47,7 +47,7 @@ def test_groupnorm_refusals(lib, monkeypatch):
 def test_groupnorm_backward_refusals(lib, monkeypatch):
     q = lib.rowops_groupnorm_act_backward_workspace_bytes
     assert q(3, 16, 64, 8, F32) >= 3 * 64 * 8  # one kernel: the samples' channel sums
-    monkeypatch.setenv("ROWOPS_GROUPNORM", "two_pass")
+    monkeypatch.setenv("ROWOPS_GROUPNORM", "stream")
     f, q = lib.rowops_groupnorm_act_backward, lib.rowops_groupnorm_act_backward_workspace_bytes
     need = q(2, 16, 64, 8, BF16)
     assert need > 0 and q(2, -1, 64, 8, BF16) == 0

@@ -235,7 +235,7 @@ def test_refusals_of_the_binding():
         ro.rowops_groupnorm_act(x, 5)
 
 
-FORMS = ["fused", "two_pass"]
+FORMS = ["fused", "stream"]
 
 
 @pytest.mark.parametrize("form", FORMS)
@@ -264,11 +264,11 @@ def test_activations_of_both_forms(form, act, monkeypatch):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_batches_of_samples_in_two_passes(dtype, monkeypatch):
+def test_large_samples_streamed(dtype, monkeypatch):
     """Three samples of more than 32 MB: one or a few at a time. Checked against
     the same calls on each sample alone, which the other tests hold to the
     64-bit form, and one sample against that form in sums."""
-    monkeypatch.setenv("ROWOPS_GROUPNORM", "two_pass")
+    monkeypatch.setenv("ROWOPS_GROUPNORM", "stream")
     B, S, C, G = 3, 66000, 256, 8
     g = torch.Generator(device="cuda").manual_seed(3)
     x = torch.randn(B, S, C, generator=g, device="cuda").to(TYPES[dtype])
@@ -297,14 +297,15 @@ def test_batches_of_samples_in_two_passes(dtype, monkeypatch):
     assert torch.all((dx.reshape(v.shape) - rdx).abs() <= 2e-5 * rsize + u * rdx.abs())
 
 
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("backward", [False, True])
-def test_a_wait_that_runs_out_is_reported(backward, monkeypatch):
-    """The one-kernel form's copies in: a box that never completes ends its wait
-    in a recorded timeout, and the next call is clean."""
+def test_a_wait_that_runs_out_is_reported(backward, form, monkeypatch):
+    """A copy in that never completes, or a sample whose results are never
+    announced, ends its wait in a recorded timeout, and the next call is clean."""
     assert ro.rowops_device_status() == 0
     x, dy, w, b = make(2, 512, 64, 4, "bf16")
     stats = torch.empty(2, 4, 2, device="cuda")
-    monkeypatch.setenv("ROWOPS_GROUPNORM", "fused")
+    monkeypatch.setenv("ROWOPS_GROUPNORM", form)
     clean = ro.rowops_groupnorm_act(x, 4, w, b, stats=stats)
     cleans = ro.rowops_groupnorm_act_backward(x, dy, stats, 4, w, b)
     assert ro.rowops_device_status() == 0

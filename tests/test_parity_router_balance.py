@@ -111,6 +111,15 @@ def test_masked_experts_and_dead_rows():
     assert torch.all(d[:, 5] == 0) and torch.all(d[17] == 0)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_at_the_types_ends(dtype):
+    """All logits at the lowest (or highest) value: an even row."""
+    logits, experts = make(60, 24, 2, dtype)
+    logits[19] = torch.finfo(logits.dtype).min
+    logits[20] = torch.finfo(logits.dtype).max
+    check(60, 24, 2, dtype, logits=logits, experts=experts)
+
+
 @pytest.mark.parametrize("T", [100, 9000])
 def test_nan_logits(T):
     logits, experts = make(T, 64, 2, "f32")
