@@ -21,7 +21,7 @@ static __global__ void __launch_bounds__(1024) column_partials_kernel(const floa
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.f;
     if (c < N) {
-#pragma unroll 8
+#pragma unroll 16
         for (int p = threadIdx.y; p < P; p += 32) s += part[p * pitch + c];
     }
     acc[threadIdx.y][threadIdx.x] = s;

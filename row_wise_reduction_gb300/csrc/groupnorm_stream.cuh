@@ -27,29 +27,32 @@ __device__ __forceinline__ void walk(const T* const (&from)[N], int64_t step, in
 #pragma unroll
     for (int k = 0; k < N; ++k) p[k] = from[k];
     if constexpr (VEC > 1) {
-        Ring<D, N, kGnBlock> ring(slots);
-        int asked = 0;
-        auto ask = [&] {
-            if (asked < n)
+        // unrolled over the ring, so that a slot's place is a constant
+        uint4* at = slots + threadIdx.x;
+        auto ask = [&](int d, int i) {
+            if (i < n)
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    ring.ask(k, p[k]);
+                    copy_async<16>(at + (d * N + k) * kGnBlock, p[k]);
                     p[k] += step;
                 }
-            ring.asked();
-            ++asked;
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
 #pragma unroll
-        for (int d = 0; d < D - 1; ++d) ask();
+        for (int d = 0; d < D - 1; ++d) ask(d, d);
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            ask();
-            ring.wait();
-            typename V::Word w[N];
+        for (int i = 0; i < n; i += D) {
 #pragma unroll
-            for (int k = 0; k < N; ++k) w[k] = ring.get(k);
-            f(w);
-            ring.done();
+            for (int d = 0; d < D; ++d) {
+                ask((d + D - 1) % D, i + d + D - 1);
+                asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+                if (i + d < n) {
+                    typename V::Word w[N];
+#pragma unroll
+                    for (int k = 0; k < N; ++k) w[k] = at[(d * N + k) * kGnBlock];
+                    f(w);
+                }
+            }
         }
     } else {
         constexpr int U = 4;
@@ -84,8 +87,6 @@ struct GnStreamWs {
     float2* result;  // [B][G] mean, rstd; backward -c1, -c2
     float2* part;    // [B chunks][G]
     float* chans;    // backward: [B chunks][2 C] sums of dz xh, dz
-    float *dw, *db;  // backward: [B] samples' channel sums, `pitch` apart
-    int64_t pitch;
 };
 
 static __global__ void gn_zero_kernel(unsigned* p, int n) {
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             const float2* p = ws.part + int64_t(sample) * a.chunks * a.G + g;
             const float ref = __ldcg(p).x;
             float2 s = f2(0.f);
-#pragma unroll 8
+#pragma unroll 16
             for (int i = lane; i < a.chunks; i += 1 << a.last_log2) {
                 const float2 v = __ldcg(p + int64_t(i) * a.G);
                 const int64_t left = a.S - i * a.chunk_rows;
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
     using V = Vec<T, VEC>;
     constexpr int P = V::P, D = kGnStreamDepthBwd;
     extern __shared__ __align__(16) uint4 slots[];  // the positions on their way, then:
-    const int t = threadIdx.x, W = a.tx * VEC;
+    const int W = a.tx * VEC;
     float2* red = reinterpret_cast<float2*>(slots) + walk_smem<VEC, D, 2>() / 8;  // [ty][W] the threads' A, Q
     float2* col = red + a.ty * W;  // [C] the channels', times w
     auto sums = [&](const GnItem& it, const GnShare& k) {
@@ -374,18 +375,11 @@ __global__ void __launch_bounds__(kGnBlock, 2)
         by_teams(a.G, a.last_log2, [&](int g, int lane, bool live) {
             const float2* p = ws.part + int64_t(sample) * a.chunks * a.G + g;
             float2 s = f2(0.f);
-#pragma unroll 8
+#pragma unroll 16
             for (int i = lane; i < a.chunks; i += 1 << a.last_log2) s = f2_add(s, __ldcg(p + int64_t(i) * a.G));
             s = lanes_sum(s, 1 << a.last_log2);
             if (live && lane == 0) ws.result[int64_t(sample) * a.G + g] = make_float2(-s.x * a.inv_m, -s.y * a.inv_m);
         });
-        for (int c = t; c < 2 * a.C; c += kGnBlock) {
-            const float* p = ws.chans + int64_t(sample) * a.chunks * 2 * a.C + c;
-            float s = 0.f;
-#pragma unroll 8
-            for (int i = 0; i < a.chunks; ++i) s += __ldcg(p + int64_t(i) * 2 * a.C);
-            (c < a.C ? ws.dw[sample * ws.pitch + c] : ws.db[sample * ws.pitch + c - a.C]) = s;
-        }
     };
     auto apply = [&](const GnItem& it, const GnShare& k) {
         if (k.n == 0) return;
@@ -486,12 +480,6 @@ cudaError_t gn_backward_stream(const void* x, const void* dy, const void* w, con
                                void* dx, float* dw, float* db, void* workspace, GnArgs a, const LaunchCfg& cfg) {
     gn_tiles(a, VEC);
     GnStreamWs ws{};
-    // one sample's channel sums are the result
-    float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + gn_counter_bytes(a.B)) +
-                  2 * (int64_t(a.B) * a.G + int64_t(a.B) * a.chunks * a.G) + int64_t(a.B) * a.chunks * 2 * a.C;
-    ws.dw = a.B == 1 ? dw : sums;
-    ws.db = a.B == 1 ? db : sums + a.C;
-    ws.pitch = 2 * int64_t(a.C);
     unsigned* err = cfg.dev_error;
     unsigned long long wait_ns = cfg.wait_ns;
     int stall = cfg.stall_row < 0 ? -1 : int(cfg.stall_row / a.S);
@@ -500,7 +488,7 @@ cudaError_t gn_backward_stream(const void* x, const void* dy, const void* w, con
         gn_stream_launch(reinterpret_cast<const void*>(gn_bwd_stream_kernel<T, VEC, ACT>), a, ws, workspace, VEC,
                          walk_smem<VEC, kGnStreamDepthBwd, 2>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C), true, args,
                          cfg);
-    return e == cudaSuccess && a.B > 1 ? gn_reduce_channels(sums, a.B, a.C, dw, db, cfg) : e;
+    return e == cudaSuccess ? gn_reduce_channels(ws.chans, int64_t(a.B) * a.chunks, a.C, dw, db, cfg) : e;
 }
 
 }  // namespace rowops

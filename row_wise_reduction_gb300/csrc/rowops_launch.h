@@ -298,10 +298,10 @@ inline GnArgs gn_plan(int64_t B, int64_t S, int64_t C, int64_t G, int64_t ld, in
 }
 inline size_t gn_counter_bytes(int64_t B) { return size_t((B + 1) * 4 + 255) / 256 * 256; }
 // Workspace: counters; results of the samples' groups, sums of the chunks'; backward
-// the chunks' and samples' channel sums.
+// the chunks' channel sums.
 inline size_t gn_stream_bytes(const GnArgs& a, int tensors) {
     const size_t B = a.B, N = B * a.chunks;
-    return gn_counter_bytes(a.B) + (B + N) * a.G * 8 + (tensors > 1 ? (B + N) * a.C * 8 : 0);
+    return gn_counter_bytes(a.B) + (B + N) * a.G * 8 + (tensors > 1 ? N * a.C * 8 : 0);
 }
 
 // A tensor map for boxes of a matrix's rows (128 bytes, a CUtensorMap).
@@ -326,12 +326,19 @@ struct GnFused {
 };
 constexpr int kGnMaxBoxes = 32;
 
+// Clusters of 1, 2, 4, 8, 16 CTAs that one, two CTAs for each SM leave room for (as the
+// occupancy query gives them on GB300: its GPCs hold no whole number of large ones).
+constexpr int kGnClusters[2][5] = {{152, 76, 36, 15, 7}, {304, 152, 74, 36, 14}};
+
 // The fastest split into groups' blocks and clusters by a model of the time, in
 // microseconds; `tensors`: 1 forward, 2 backward (read and held). Returns the
 // modelled time, or a negative number where no split holds the slab. The model:
-// the traffic at the card's copy rate, or the waves of CTAs at the rate of an
-// SM's share if that is longer; a launch, and an exchange where a cluster
-// has several CTAs.
+// the traffic at the card's copy rate, or the turns of the clusters, each with the
+// arithmetic of an SM's CTAs (0.26 us for a vector of every thread forward, 0.52
+// backward, two thirds of it in fp32, less for single elements) and an exchange; and
+// a launch. Modelled and measured in us: B8 S4096 C320 bf16 SiLU 17 and 16, its
+// backward pass 30 and 32, with B32 53 and 58, 105 and 105; B3 S1155 C330 fp32
+// backward 15 and 14.
 inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFused* best) {
     double least = -1.0;
     const double all = double(a.B) * a.S * a.C * es * (tensors + 1);
@@ -361,27 +368,26 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
             // four copies where they are worth it, of at most 256 rows; slots of 128 bytes
             f.boxes = vec == 1 ? 1 : int(std::max<int64_t>(rows * W * es >= 16384 ? 4 : 1, (rows + 255) / 256));
             f.box = int((rows + f.boxes - 1) / f.boxes);
+            if (f.boxes > 1) f.box = std::min((f.box + 7) / 8 * 8, 256);  // whole slots, one after the other
             f.boxes = int((rows + f.box - 1) / f.box);
             if (f.boxes > kGnMaxBoxes) continue;
             const int unit = 128 / (vec * es);
             f.pitch = vec == 1 ? f.box * tx : (f.box * tx + unit - 1) / unit * unit;
             f.tile = (size_t(tensors) * f.boxes * f.pitch * vec * es + 127) / 128 * 128;
             const size_t groups = size_t(W / a.L);
-            f.smem = f.tile + size_t(f.ty) * W * 8 + size_t(W) * 8 + groups * 8 * (1 + cluster) + f.boxes * 8 +
+            f.smem = f.tile + size_t(f.ty) * W * 8 + size_t(W) * 8 + groups * 8 * (1 + 2 * cluster) + f.boxes * 8 +
                      size_t(f.ty) * 4;
             if (f.smem > kGnSmem) continue;
             f.parts_log2 = W >= kGnBlock ? 0 : std::min(5, log2_floor(std::min(kGnBlock / W, f.ty)));
             f.team_log2 = std::min(std::min(5, log2_floor(kGnBlock / std::min<int>(kGnBlock, int(groups)))),
                                    log2_floor(2 * a.L - 1));
-            const int per_sm = f.smem <= kGnSmem / 3 - 1024 && tensors == 1 ? 3 : f.smem <= kGnSmem / 2 - 512 ? 2 : 1;
-            double wide = 1.0;
-            if (tx * f.ty < kGnBlock * 3 / 4) wide *= 1.15;
-            const double io = double(rows) * W * es * (tensors + 1) * wide;
-            // SMs that clusters of this size can fill (the GPCs have no multiple of it)
-            const double sms = kGnSms * (cluster == 16 ? 0.74 : cluster == 8 ? 0.9 : cluster == 4 ? 0.96 : 1.0);
-            const double sm = ctas <= sms ? io : std::ceil(ctas / (sms * per_sm)) * per_sm * io;
-            double t = 3.0 + (cluster > 1 ? 1.0 : 0.0) + std::max(all * wide / 6.8e6, sm / 5.5e4);
-            if (per_sm == 1 && ctas > kGnSms) t *= 1.4;  // nothing covers a CTA's exchange
+            const int per_sm = f.smem <= kGnSmem / 2 - 512 ? 2 : 1;
+            const double slabs = double(a.B) * blocks, held = std::min(slabs, double(kGnClusters[per_sm - 1][cl]));
+            const double turns = std::ceil(slabs / held), slots = std::ceil(double(rows) / f.ty);
+            const double ctas_sm = std::ceil(held * cluster / kGnSms);
+            const double slot = (tensors == 1 ? 0.26 : ctas_sm > 1 ? 0.52 : 0.7) * (vec == 1 ? 0.4 : es == 4 ? 0.67 : 1.0);
+            const double exchange = cluster > 1 ? 2.0 : 1.0;
+            double t = std::max(all / 6.8e6, turns * (ctas_sm * slots * slot + exchange / ctas_sm)) + 4.5 + exchange / 2;
             if (least < 0 || t < least) {
                 least = t;
                 *best = f;
@@ -391,11 +397,12 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
     return least;
 }
 
-// The streaming form's modelled time: a launch, the zeroing and the end of the sums,
-// and the traffic, the second read at twice the copy rate.
+// The streaming form's modelled time: launches and the ends of the sums, and its
+// traffic at what it measured. Modelled and measured in us, the same sizes: 25 and 25,
+// 38 and 34, with B32 49 and 49, 101 and 100; odd C (21 and 22).
 inline double gn_stream_time(const GnArgs& a, int es, int tensors) {
     const double in = double(a.B) * a.S * a.C * es * tensors;
-    return 7.0 + (1.5 * in + in / tensors) / 6.8e6;
+    return 17.0 + (in + in / tensors) / (tensors == 1 ? 5.2e6 : 3.0e6);
 }
 
 using GnForwardLaunch = cudaError_t (*)(const void* x, void* y, const void* w, const void* b, float* stats, void* ws,
