@@ -138,7 +138,7 @@ static int take(const char* name, const char* form, PyObject* const* a, Py_ssize
 }
 
 /* the addresses, in the order of bind_training's arguments */
-static void* g_training[9];
+static void* g_training[10];
 
 typedef size_t (*gn_bytes_fn)(int64_t, int64_t, int64_t, int64_t, int);
 typedef size_t (*rows_bytes_fn)(int64_t, int64_t, int);
@@ -158,8 +158,8 @@ typedef int (*balance_bwd_fn)(const void*, const void*, const float*, const void
 static PyObject* bind_training(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     int k;
     (void)self;
-    if (!nargs_ok(n, 9, "bind_training")) return NULL;
-    for (k = 0; k < 9; ++k)
+    if (!nargs_ok(n, 10, "bind_training")) return NULL;
+    for (k = 0; k < 10; ++k)
         if (as_ptr(a[k], &g_training[k])) return NULL;
     Py_RETURN_NONE;
 }
@@ -210,6 +210,8 @@ CALL(router_balance_loss, 7, "ppipfppiiiiipip",
 CALL(router_balance_loss_backward, 8, "ppppfpiiiiip",
      ((balance_bwd_fn)g_training[8])(v.p[0], v.p[1], (float*)v.p[2], v.p[3], v.f[4], v.p[5], v.i[6], v.i[7], v.i[8],
                                      v.i[9], (int)v.i[10], v.p[11]))
+BYTES(router_balance_loss_workspace_bytes, 9, "iii",
+      ((rows_bytes_fn)g_training[9])(v.i[0], v.i[1], (int)v.i[2]))
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, "rowops_" #name}
 
@@ -229,6 +231,7 @@ static PyMethodDef methods[] = {
     METHOD(bias_dropout_residual_backward),
     METHOD(router_balance_loss),
     METHOD(router_balance_loss_backward),
+    METHOD(router_balance_loss_workspace_bytes),
     {NULL, NULL, 0, NULL},
 };
 

@@ -169,6 +169,7 @@ _TRAINING = (
     "bias_dropout_residual_backward",
     "router_balance_loss",
     "router_balance_loss_backward",
+    "router_balance_loss_workspace_bytes",
 )
 
 
@@ -665,6 +666,8 @@ def _positions(x: torch.Tensor, name: str):
 
 def _like_positions(x: torch.Tensor, ld: int, t: Optional[torch.Tensor], name: str) -> torch.Tensor:
     if t is None:
+        if x.is_contiguous():
+            return torch.empty_like(x)
         return torch.empty_strided(x.shape, (x.shape[1] * ld, ld, 1), dtype=x.dtype, device=x.device)
     if t.dtype is not x.dtype or t.get_device() != x.get_device() or t.shape != x.shape:
         raise ValueError(f"{name} must match x in shape, dtype and device")
@@ -907,7 +910,7 @@ def rowops_router_balance_loss(
     loss = _floats(loss, 1, dev, "loss")
     counts = _counts(counts, E, dev)
     L = _calls or _hot_calls()
-    ws, wp, wn = _scratch(workspace, library().rowops_router_balance_loss_workspace_bytes(T, E, code), dev)
+    ws, wp, wn = _scratch(workspace, L.router_balance_loss_workspace_bytes(T, E, code), dev)
     st = L.router_balance_loss(
         logits.data_ptr(), experts.data_ptr(), width, _row_mask(mask, T, dev), coef, loss.data_ptr(),
         counts.data_ptr(), T, E, experts.shape[1], ld, code, wp, wn, _current_raw_stream(dev))
