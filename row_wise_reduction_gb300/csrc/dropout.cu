@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kWarps * 32, Elem<T>::kBytes == 2 ? 4 : 3)
     using E = Elem<T>;
     constexpr int PE = E::kVec, NP = 8 / PE, N = NP * (RES ? 2 : 1), D = N == 1 ? 6 : (N == 2 ? 4 : 3);
     extern __shared__ uint4 slots[];
+    if constexpr (SUM) let_next_start();
     const Columns<PE> c(a);
     const Generator gen(a, RNG);
     Ring<D, N, kWarps * 32> ring(slots);
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     dropout_elements_kernel(const T* x, const T* r, const T* b, T* y, float* part,
                    const __grid_constant__ DropArgs a) {
     using E = Elem<T>;
+    if constexpr (SUM) let_next_start();
     const Columns<1> c(a);
     const Generator gen(a, RNG);
     float bias[8], acc[8][1] = {};
@@ -288,6 +290,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     constexpr int V = E::kVec, SPAN = kSegVecs * V;  // columns from one segment to the next
     constexpr int N = RES ? 2 : 1, D = RES ? 4 : 6;
     extern __shared__ uint4 slots[];
+    if constexpr (SUM) let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r0 = int64_t(blockIdx.y) * a.chunk_rows + warp;
     const int64_t r1 = int64_t(blockIdx.y + 1) * a.chunk_rows < a.M ? int64_t(blockIdx.y + 1) * a.chunk_rows : a.M;
@@ -435,15 +438,23 @@ struct DropCall {
     float* db;
 };
 
-// Rows of a chunk: one wave of CTAs with column sums, four without; whole steps
-// of the CTA unless that leaves CTAs idle.
+// Rows of a chunk: without column sums four waves of CTAs. With them every chunk
+// leaves partial rows, and fewer are better: of the vector form two CTAs an SM, whose
+// rings keep the memory busy (bf16 16384 x 8192 88 us, with four 99, in two waves of
+// those 92; 4096 x 1024 8 us, 9.6 and 11); of the others, which have more to compute, as
+// many as fit, and twice as many where a chunk still has 32 rows (bf16 4001 x 4097 28
+// us, one wave 30; 1000 x 1025 10 us and 9). Whole steps of the CTA unless that leaves
+// CTAs idle.
 template <typename T>
 cudaError_t launch(DropKernel<T> kern, size_t smem, int64_t gx, int64_t step, int64_t unit, int partials,
-                   const DropCall& c, DropArgs a, const LaunchCfg& cfg) {
+                   bool rings, const DropCall& c, DropArgs a, const LaunchCfg& cfg) {
     const void* f = reinterpret_cast<const void*>(kern);
     cudaError_t e = allow_smem(f, smem, cfg);
     if (e != cudaSuccess) return e;
-    const int64_t want = int64_t(grid_for(f, kWarps * 32, smem, INT64_MAX, cfg)) * (c.db ? 1 : 4);
+    int64_t want = grid_for(f, kWarps * 32, smem, INT64_MAX, cfg);
+    if (!c.db) want *= 4;
+    else if (rings) want = std::min(want, int64_t(2) * cfg.num_sms);
+    else if (a.M * gx / 32 >= 2 * want) want *= 2;
     int64_t chunks = std::max(int64_t(1), want / gx);
     if (c.db) chunks = std::min(chunks, int64_t(c.max_partials / partials));
     chunks = std::min(chunks, int64_t(65535));
@@ -463,7 +474,7 @@ cudaError_t dropout_form(const DropCall& c, DropArgs a, int form, const LaunchCf
     constexpr int V = Elem<T>::kVec;
     if (form == 1)  // shifted: a tail lane behind the last whole vector of a row that starts on a boundary
         return launch<T>(dropout_shifted_kernel<T, RNG, SUM, RES>, size_t(RES ? 8 : 6) * kWarps * 512,
-                         (a.N / V + 1 + kSegVecs - 1) / kSegVecs, kWarps * 4, kWarps, 2, c, a, cfg);
+                         (a.N / V + 1 + kSegVecs - 1) / kSegVecs, kWarps * 4, kWarps, 2, false, c, a, cfg);
     a.tl_log2 = pick_log2(a.N, 8, 5);
     const int64_t segs = (a.N + (int64_t(8) << a.tl_log2) - 1) / (int64_t(8) << a.tl_log2);
     a.wx_log2 = pick_log2(segs, 1, 3);
@@ -471,9 +482,10 @@ cudaError_t dropout_form(const DropCall& c, DropArgs a, int form, const LaunchCf
     const int64_t rows = int64_t(kWarps >> a.wx_log2) * (32 >> a.tl_log2);  // of a CTA at a time
     if (form == 0) {
         constexpr int N = 8 / V * (RES ? 2 : 1), D = N == 1 ? 6 : (N == 2 ? 4 : 3);
-        return launch<T>(dropout_kernel<T, RNG, SUM, RES>, size_t(N) * D * kWarps * 512, gx, rows * 4, 1, 1, c, a, cfg);
+        return launch<T>(dropout_kernel<T, RNG, SUM, RES>, size_t(N) * D * kWarps * 512, gx, rows * 4, 1, 1, true, c, a,
+                         cfg);
     }
-    return launch<T>(dropout_elements_kernel<T, RNG, SUM, 2>, 0, gx, rows * 2, 1, 1, c, a, cfg);
+    return launch<T>(dropout_elements_kernel<T, RNG, SUM, 2>, 0, gx, rows * 2, 1, 1, false, c, a, cfg);
 }
 
 template <typename T>

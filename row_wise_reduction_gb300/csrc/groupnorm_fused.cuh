@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
     const typename V::Word* const tiles[2] = {tx, td};
     const int c = k.tx * VEC;
     int fail = 0;
+    let_next_start();
     for (; k.slab < k.slabs; k.next()) {
         gn_fetch<T, VEC, 2>(k, maps, from, tx, bars, stall_row);
         float2* got = gots + (k.turn & 1) * f.cluster * Gb;

@@ -170,7 +170,6 @@ __device__ __forceinline__ float2 joined(float ref, float2 s, float n, float per
 }
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // a value where CTA `rank` of the cluster keeps it
 template <typename V>

@@ -90,6 +90,7 @@ struct GnStreamWs {
 };
 
 static __global__ void gn_zero_kernel(unsigned* p, int n) {
+    let_next_start();
     grid_wait();
     for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0u;
 }
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
     const int W = a.tx * VEC;
     float2* red = reinterpret_cast<float2*>(slots) + walk_smem<VEC, D, 2>() / 8;  // [ty][W] the threads' A, Q
     float2* col = red + a.ty * W;  // [C] the channels', times w
+    let_next_start();
     auto sums = [&](const GnItem& it, const GnShare& k) {
         const int64_t slot = int64_t(it.sample) * a.chunks + it.chunk;
         float* cw = ws.chans + slot * 2 * a.C;

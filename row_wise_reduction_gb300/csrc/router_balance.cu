@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kBlock, NV * VEC <= 16 ? 3 : 1)
     int* cs = reinterpret_cast<int*>(Ps + E);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int TL = 1 << tl_log2, tl = lane & (TL - 1), sub = lane >> tl_log2, SR = 32 >> tl_log2;
+    let_next_start();
     for (int i = threadIdx.x; i <= E; i += kBlock) cnt[i] = 0;
     __syncthreads();
 
@@ -309,7 +310,13 @@ __global__ void __launch_bounds__(1024)
     int* c = reinterpret_cast<int*>(P + E);  // [E + 1]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.f;
-    int k = 0;
+    int k = 0, took[kBalanceMaxClusters / 32];  // the rows that take part
+    if (t < 32)
+#pragma unroll
+        for (int u = 0; u < kBalanceMaxClusters / 32; ++u) {
+            const int g = t + 32 * u;
+            took[u] = g < G ? part_c[int64_t(g) * (E + 1) + E] : 0;
+        }
     if (e < E) {
         constexpr int U = 16;  // partial rows on their way
         for (int g0 = y; g0 < G; g0 += U * Y) {
@@ -330,9 +337,10 @@ __global__ void __launch_bounds__(1024)
     }
     tp[t] = s;
     tc[t] = k;
-    if (t < 32) {  // the rows that take part
+    if (t < 32) {
         int n = 0;
-        for (int g = t; g < G; g += 32) n += part_c[int64_t(g) * (E + 1) + E];
+#pragma unroll
+        for (int u = 0; u < kBalanceMaxClusters / 32; ++u) n += took[u];
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
         if (t == 0) c[E] = n;
     }

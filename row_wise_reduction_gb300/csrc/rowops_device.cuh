@@ -295,4 +295,8 @@ __device__ __forceinline__ MD group_merge(MD s, float* red_m, float* red_d) {
     return s;
 }
 
+// In a kernel before one that waits for its end (griddepcontrol.wait): that one may
+// be launched once every CTA has got here, into what room they leave.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 }  // namespace rowops
