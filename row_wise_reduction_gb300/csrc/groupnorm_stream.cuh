@@ -79,22 +79,25 @@ constexpr size_t walk_smem() {
     return VEC > 1 ? size_t(D) * N * kGnBlock * 16 : 0;
 }
 
-// The workspace: the item counter and a counter for each sample (zeroed before
-// the kernel), results for each sample's groups, sums of each chunk's.
+// The workspace: the item counter and counters for each sample (zeroed before the
+// kernel), results for each sample's groups, sums of each chunk's and bunch's.
 struct GnStreamWs {
     unsigned* next;
-    unsigned* done;  // [B] chunks added up; chunks + 1: the results are there
-    float2* result;  // [B][G] mean, rstd; backward -c1, -c2
-    float2* part;    // [B chunks][G]
+    unsigned* done;        // [B] sets of sums added up; kGnThere: the results are there
+    unsigned* bunch_done;  // [B bunches] chunks added up
+    float2* result;        // [B][G] mean, rstd; backward -c1, -c2
+    float2* part;          // [B chunks][G]
+    float2* bunch;         // [B bunches][G]
     float* chans;    // backward: [B chunks][2 C] sums of dz xh, dz
 };
 
-static __global__ void gn_zero_kernel(unsigned* p, int n) {
+static __global__ void gn_zero_kernel(unsigned* p, int64_t n) {
     let_next_start();
     grid_wait();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0u;
+    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0u;
 }
 
+constexpr unsigned kGnThere = 0x80000000u;
 constexpr int kGnStreamDepth = 6, kGnStreamDepthBwd = 4;
 
 // Items of the sequence: `lag` sums, then apply and sums in turn, then apply.
@@ -136,28 +139,98 @@ struct GnShare {
     }
 };
 
-// Thread 0 has counted the CTA's sums in; true in every thread where they were the
-// sample's last.
-__device__ __forceinline__ bool gn_last(unsigned* done, int chunks, unsigned* word) {
+// Counts the CTA's sums in; true in every thread where they were the last of `sets`.
+__device__ __forceinline__ bool gn_last(unsigned* done, int sets, unsigned* word) {
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
         *word = atomicAdd(done, 1u);
     }
     __syncthreads();
-    if (*word != unsigned(chunks - 1)) return false;
+    if (*word != unsigned(sets - 1)) return false;
     __threadfence();
     return true;
 }
 
+// The CTA adds up n sets of sums of G groups, in order; set i is of `rows` positions,
+// S in all. Forward (MEANS: a group's mean and squares about it) the means enter less
+// the first set's; to[g] is the same of all sets or, `last`, mean and rstd. Backward the
+// plain sums, times -inv_m at the last. A function of its own, and a short one: it runs
+// once or twice in a CTA, and its time is that of fetching its code and waiting for
+// its loads.
+template <bool MEANS>
+__device__ __noinline__ void gn_join(const float2* sets, int n, int64_t S, int64_t rows, bool last, float2* to,
+                                     float2* also, const GnArgs& a) {
+    by_teams(a.G, a.last_log2, [&](int g, int lane, bool live) {
+        const float2* p = sets + g;
+        const float ref = MEANS ? __ldcg(p).x : 0.f;
+        const int step = 1 << a.last_log2;
+        float2 s = f2(0.f);
+#pragma unroll 1
+        for (int i = lane; i < n; i += 4 * step) {
+            float2 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u * step < n) v[u] = __ldcg(p + int64_t(i + u * step) * a.G);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i + u * step < n) {
+                    if constexpr (MEANS) {
+                        const int64_t left = S - (i + u * step) * rows;
+                        const float m = float(left < rows ? left : rows), d = v[u].x - ref;
+                        s.x = fmaf(m, d, s.x);
+                        s.y += fmaf(m * float(a.L) * d, d, v[u].y);
+                    } else {
+                        s = f2_add(s, v[u]);
+                    }
+                }
+        }
+        s = lanes_sum(s, step);
+        if (!live || lane != 0) return;
+        if constexpr (MEANS) {
+            s = joined(ref, s, float(a.L), 1.f / float(S));
+            if (last) s.y = rsqrtf(s.y * a.inv_m + a.eps);
+        } else if (last) {
+            s = make_float2(-s.x * a.inv_m, -s.y * a.inv_m);
+        }
+        to[g] = s;
+        if (also) also[g] = s;
+    });
+}
+
+// A sample's chunks' sums (or a bunch's, where chunks go in bunches) are in: joins them.
+template <bool MEANS>
+__device__ __forceinline__ bool gn_joined(const GnItem& it, const GnArgs& a, const GnStreamWs& ws, float2* stats,
+                                          unsigned* word) {
+    const float2* part = ws.part + int64_t(it.sample) * a.chunks * a.G;
+    int n = a.chunks;
+    int64_t rows = a.chunk_rows;
+    if (a.bunches > 1) {
+        const int k = it.chunk / a.bunch, first = k * a.bunch, size = min(a.bunch, a.chunks - first);
+        if (!gn_last(&ws.bunch_done[int64_t(it.sample) * a.bunches + k], size, word)) return false;
+        float2* to = ws.bunch + int64_t(it.sample) * a.bunches * a.G;
+        const int64_t at = first * rows, left = a.S - at;
+        gn_join<MEANS>(part + int64_t(first) * a.G, size, left < a.bunch * rows ? left : a.bunch * rows, rows, false,
+                       to + k * a.G, nullptr, a);
+        part = to;
+        n = a.bunches;
+        rows *= a.bunch;
+    }
+    if (!gn_last(&ws.done[it.sample], n, word)) return false;
+    gn_join<MEANS>(part, n, a.S, rows, true, ws.result + int64_t(it.sample) * a.G,
+                   stats ? stats + int64_t(it.sample) * a.G : nullptr, a);
+    __syncthreads();
+    return true;
+}
+
 // Every thread of the CTA: the sample's results are there; false where the wait ran out.
-__device__ __forceinline__ bool gn_ready(const unsigned* done, unsigned want, unsigned long long wait_ns) {
+__device__ __forceinline__ bool gn_ready(const unsigned* done, unsigned long long wait_ns) {
     int ok = 1;
     if (threadIdx.x == 0) {
         auto there = [&] {
             unsigned v;
             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
-            return v == want;
+            return v == kGnThere;
         };
         if (!there()) {
             const unsigned long long t0 = global_ns();
@@ -173,10 +246,10 @@ __device__ __forceinline__ bool gn_ready(const unsigned* done, unsigned want, un
 }
 
 // The sequence's items, one after the other: sums(item, share), which leaves a chunk's
-// sums, last(sample), which joins a sample's, and apply(item, share).
-template <typename Sums, typename Last, typename Apply>
+// sums, join(item), true where that made a sample's results, and apply(item, share).
+template <typename Sums, typename Join, typename Apply>
 __device__ __forceinline__ void gn_sequence(const GnArgs& a, const GnStreamWs& ws, unsigned* err,
-                                            unsigned long long wait_ns, int stall, Sums sums, Last last,
+                                            unsigned long long wait_ns, int stall, Sums sums, Join join,
                                             Apply apply) {
     __shared__ unsigned word[2];
     const int t = threadIdx.x;
@@ -192,17 +265,13 @@ __device__ __forceinline__ void gn_sequence(const GnArgs& a, const GnStreamWs& w
         const GnItem it(i, a);
         const GnShare k(a, it);
         if (it.apply) {
-            if (gn_ready(&ws.done[it.sample], unsigned(a.chunks) + 1u, wait_ns)) apply(it, k);
+            if (gn_ready(&ws.done[it.sample], wait_ns)) apply(it, k);
             else if (t == 0) atomicExch(err, kDeviceErrTimeout);
         } else {
             sums(it, k);
-            if (gn_last(&ws.done[it.sample], a.chunks, &word[1])) {
-                last(it.sample);
-                __syncthreads();
-                if (t == 0 && it.sample != stall) {
-                    __threadfence();
-                    atomicExch(&ws.done[it.sample], unsigned(a.chunks) + 1u);
-                }
+            if (join(it, &word[1]) && t == 0 && it.sample != stall) {
+                __threadfence();
+                atomicExch(&ws.done[it.sample], kGnThere);
             }
         }
         if (t == 0 && !a.early) after = atomicAdd(ws.next, 1u);
@@ -272,28 +341,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             if (live && lane == 0) out[g] = joined(ref, s, m, a.inv_L);
         });
     };
-    auto last = [&](int sample) {
-        by_teams(a.G, a.last_log2, [&](int g, int lane, bool live) {
-            const float2* p = ws.part + int64_t(sample) * a.chunks * a.G + g;
-            const float ref = __ldcg(p).x;
-            float2 s = f2(0.f);
-#pragma unroll 16
-            for (int i = lane; i < a.chunks; i += 1 << a.last_log2) {
-                const float2 v = __ldcg(p + int64_t(i) * a.G);
-                const int64_t left = a.S - i * a.chunk_rows;
-                const float m = float(left < a.chunk_rows ? left : a.chunk_rows), d = v.x - ref;
-                s.x = fmaf(m, d, s.x);
-                s.y += fmaf(m * float(a.L) * d, d, v.y);
-            }
-            s = lanes_sum(s, 1 << a.last_log2);
-            if (live && lane == 0) {
-                const float2 v = joined(ref, s, float(a.L), a.inv_S);
-                const float2 r = make_float2(v.x, rsqrtf(v.y * a.inv_m + a.eps));
-                ws.result[int64_t(sample) * a.G + g] = r;
-                if (stats_out) stats_out[int64_t(sample) * a.G + g] = r;
-            }
-        });
-    };
+    auto join = [&](const GnItem& it, unsigned* word) { return gn_joined<true>(it, a, ws, stats_out, word); };
     auto apply = [&](const GnItem& it, const GnShare& k) {
         if (k.n == 0) return;
         for (int tile = 0; tile < a.tiles; ++tile) {
@@ -320,7 +368,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             });
         }
     };
-    gn_sequence(a, ws, err, wait_ns, stall, sums, last, apply);
+    gn_sequence(a, ws, err, wait_ns, stall, sums, join, apply);
 }
 
 template <typename T, int VEC, int ACT>
@@ -373,16 +421,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
             if (live && lane == 0) ws.part[slot * a.G + g] = s;
         });
     };
-    auto last = [&](int sample) {
-        by_teams(a.G, a.last_log2, [&](int g, int lane, bool live) {
-            const float2* p = ws.part + int64_t(sample) * a.chunks * a.G + g;
-            float2 s = f2(0.f);
-#pragma unroll 16
-            for (int i = lane; i < a.chunks; i += 1 << a.last_log2) s = f2_add(s, __ldcg(p + int64_t(i) * a.G));
-            s = lanes_sum(s, 1 << a.last_log2);
-            if (live && lane == 0) ws.result[int64_t(sample) * a.G + g] = make_float2(-s.x * a.inv_m, -s.y * a.inv_m);
-        });
-    };
+    auto join = [&](const GnItem& it, unsigned* word) { return gn_joined<false>(it, a, ws, nullptr, word); };
     auto apply = [&](const GnItem& it, const GnShare& k) {
         if (k.n == 0) return;
         for (int tile = 0; tile < a.tiles; ++tile) {
@@ -403,7 +442,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
             });
         }
     };
-    gn_sequence(a, ws, err, wait_ns, stall, sums, last, apply);
+    gn_sequence(a, ws, err, wait_ns, stall, sums, join, apply);
 }
 
 // ---- launchers -------------------------------------------------------------
@@ -452,12 +491,14 @@ inline cudaError_t gn_stream_launch(const void* kern, GnArgs& a, GnStreamWs& ws,
     char* p = static_cast<char*>(workspace);
     ws.next = reinterpret_cast<unsigned*>(p);
     ws.done = ws.next + 1;
-    p += gn_counter_bytes(a.B);
+    ws.bunch_done = ws.done + a.B;
+    p += gn_counter_bytes(a);
     ws.result = reinterpret_cast<float2*>(p);
     ws.part = ws.result + int64_t(a.B) * a.G;
-    if (backward) ws.chans = reinterpret_cast<float*>(ws.part + N * a.G);
+    ws.bunch = ws.part + N * a.G;
+    if (backward) ws.chans = reinterpret_cast<float*>(ws.bunch + gn_bunches(a) * a.G);
     unsigned* counters = ws.next;
-    int n = a.B + 1;
+    int64_t n = 1 + a.B + gn_bunches(a);
     void* zero_args[] = {&counters, &n};
     e = gn_launch(reinterpret_cast<const void*>(gn_zero_kernel), 1, 1024, 0, cfg, zero_args);
     return e == cudaSuccess ? gn_launch(kern, grid, kGnBlock, smem, cfg, args) : e;

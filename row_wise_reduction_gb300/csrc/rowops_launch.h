@@ -275,6 +275,7 @@ struct GnArgs {
     int tx, ty, tiles, inv_tx;  // channel vectors side by side, positions at a time, tiles; 2^16 / tx
     int parts_log2, team_log2, last_log2;  // lanes that add up a channel, a group, a group's chunks
     int chunks, lag;            // of a sample; sums before the first apply
+    int bunch, bunches;         // chunks whose sums are joined first, and how many such (1: none)
     bool early;                 // CTAs take their next item ahead
     int64_t chunk_rows;         // positions of a chunk
 };
@@ -294,14 +295,20 @@ inline GnArgs gn_plan(int64_t B, int64_t S, int64_t C, int64_t G, int64_t ld, in
     n = std::min(n, std::max(int64_t(1), (int64_t(1) << 30) / B));  // items are counted in 32 bits
     a.chunk_rows = (S + n - 1) / n;
     a.chunks = int((S + a.chunk_rows - 1) / a.chunk_rows);
+    // In two steps where a sample has many chunks: joining 456 took the last CTA 8 us
+    // (B1 S262144 C128 bf16 56 us, in two steps 52). Of 40 and of 152 chunks one step is
+    // better, as the samples are more (B32 S4096 C320 backward 99 us and 106).
+    a.bunch = a.chunks <= 256 ? a.chunks : int(std::ceil(std::sqrt(double(a.chunks))));
+    a.bunches = (a.chunks + a.bunch - 1) / a.bunch;
     return a;
 }
-inline size_t gn_counter_bytes(int64_t B) { return size_t((B + 1) * 4 + 255) / 256 * 256; }
-// Workspace: counters; results of the samples' groups, sums of the chunks'; backward
+inline int64_t gn_bunches(const GnArgs& a) { return a.bunches > 1 ? int64_t(a.B) * a.bunches : 0; }
+inline size_t gn_counter_bytes(const GnArgs& a) { return size_t((1 + a.B + gn_bunches(a)) * 4 + 255) / 256 * 256; }
+// Workspace: counters; results of the samples' groups, sums of the chunks' and bunches'; backward
 // the chunks' channel sums.
 inline size_t gn_stream_bytes(const GnArgs& a, int tensors) {
     const size_t B = a.B, N = B * a.chunks;
-    return gn_counter_bytes(a.B) + (B + N) * a.G * 8 + (tensors > 1 ? N * a.C * 8 : 0);
+    return gn_counter_bytes(a) + (B + N + gn_bunches(a)) * a.G * 8 + (tensors > 1 ? N * a.C * 8 : 0);
 }
 
 // A tensor map for boxes of a matrix's rows (128 bytes, a CUtensorMap).
