@@ -18,62 +18,77 @@
 
 namespace rowops {
 
-// f(words) for a thread's n positions, `step` elements apart, of N tensors: vectors
-// through a ring of copies, D positions on their way; single elements U at a time.
-template <typename T, int VEC, int D, int N, typename F>
-__device__ __forceinline__ void walk(const T* const (&from)[N], int64_t step, int n, uint4* slots, F f) {
+// A thread's n positions, `step` elements apart, of N tensors: run(f) calls f(words)
+// for each in order. Vectors come through a ring of copies, D positions on their
+// way, the first of them asked for by the constructor: what else a pass needs first
+// (its parameters, a wait) goes between. Single elements: U at a time.
+template <typename T, int VEC, int D, int N>
+struct Walk {
     using V = Vec<T, VEC>;
     const T* p[N];
+    int64_t step;
+    int n;
+    uint4* at;
+    __device__ __forceinline__ Walk(const T* const (&from)[N], int64_t step_, int n_, uint4* slots)
+        : step(step_), n(n_), at(slots + threadIdx.x) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) p[k] = from[k];
-    if constexpr (VEC > 1) {
-        // unrolled over the ring, so that a slot's place is a constant
-        uint4* at = slots + threadIdx.x;
-        auto ask = [&](int d, int i) {
-            if (i < n)
+        for (int k = 0; k < N; ++k) p[k] = from[k];
+        if constexpr (VEC > 1)
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    copy_async<16>(at + (d * N + k) * kGnBlock, p[k]);
-                    p[k] += step;
-                }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
+            for (int d = 0; d < D - 1; ++d) ask(d, d);
+    }
+    __device__ __forceinline__ void ask(int d, int i) {
+        if (i < n)
 #pragma unroll
-        for (int d = 0; d < D - 1; ++d) ask(d, d);
+            for (int k = 0; k < N; ++k) {
+                copy_async<16>(at + (d * N + k) * kGnBlock, p[k]);
+                p[k] += step;
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // for a walk that does not run
+    __device__ __forceinline__ void drop() const {
+        if constexpr (VEC > 1) asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    template <typename F>
+    __device__ __forceinline__ void run(F f) {
+        if constexpr (VEC > 1) {
+            // unrolled over the ring, so that a slot's place is a constant
 #pragma unroll 1
-        for (int i = 0; i < n; i += D) {
+            for (int i = 0; i < n; i += D) {
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                ask((d + D - 1) % D, i + d + D - 1);
-                asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-                if (i + d < n) {
-                    typename V::Word w[N];
+                for (int d = 0; d < D; ++d) {
+                    ask((d + D - 1) % D, i + d + D - 1);
+                    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+                    if (i + d < n) {
+                        typename V::Word w[N];
 #pragma unroll
-                    for (int k = 0; k < N; ++k) w[k] = at[(d * N + k) * kGnBlock];
-                    f(w);
+                        for (int k = 0; k < N; ++k) w[k] = at[(d * N + k) * kGnBlock];
+                        f(w);
+                    }
                 }
             }
+        } else {
+            constexpr int U = 4;
+            auto batch = [&](int live) {
+                typename V::Word w[U][N];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < live)
+#pragma unroll
+                        for (int k = 0; k < N; ++k) {
+                            w[u][k] = V::load(p[k]);
+                            p[k] += step;
+                        }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < live) f(w[u]);
+            };
+            for (; n >= U; n -= U) batch(U);
+            if (n > 0) batch(n);
         }
-    } else {
-        constexpr int U = 4;
-        auto batch = [&](int live) {
-            typename V::Word w[U][N];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (u < live)
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        w[u][k] = V::load(p[k]);
-                        p[k] += step;
-                    }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (u < live) f(w[u]);
-        };
-        for (; n >= U; n -= U) batch(U);
-        if (n > 0) batch(n);
     }
-}
+};
 template <int VEC, int D, int N>
 constexpr size_t walk_smem() {
     return VEC > 1 ? size_t(D) * N * kGnBlock * 16 : 0;
@@ -245,8 +260,12 @@ __device__ __forceinline__ bool gn_ready(const unsigned* done, unsigned long lon
     return __syncthreads_and(ok);
 }
 
-// The sequence's items, one after the other: sums(item, share), which leaves a chunk's
-// sums, join(item), true where that made a sample's results, and apply(item, share).
+// The sequence's items, one after the other: sums(item, share, walked), which leaves a
+// chunk's sums and calls walked() once it has read the chunk, join(item), true where
+// that made a sample's results, and apply(item, share, ready), which calls ready()
+// before it uses them and ends where that is false. (Chunks applied in two parts, for
+// a more even end, cost B1 S262144 C128 bf16 59 us instead of 52: an item's start and
+// end are the dearer.)
 template <typename Sums, typename Join, typename Apply>
 __device__ __forceinline__ void gn_sequence(const GnArgs& a, const GnStreamWs& ws, unsigned* err,
                                             unsigned long long wait_ns, int stall, Sums sums, Join join,
@@ -258,23 +277,28 @@ __device__ __forceinline__ void gn_sequence(const GnArgs& a, const GnStreamWs& w
     __syncthreads();
     const unsigned items = 2u * unsigned(a.B) * unsigned(a.chunks);
     for (unsigned i = word[0]; i < items;) {
-        // the next one while this one is worked on, but where a CTA has only a few:
-        // it would keep a second one from a CTA that has none
+        // the next one while this one is worked on; where a CTA has only a few, which
+        // would keep a second one from a CTA that has none, while its sums are joined
         unsigned after = 0;
         if (t == 0 && a.early) after = atomicAdd(ws.next, 1u);
         const GnItem it(i, a);
         const GnShare k(a, it);
         if (it.apply) {
-            if (gn_ready(&ws.done[it.sample], wait_ns)) apply(it, k);
-            else if (t == 0) atomicExch(err, kDeviceErrTimeout);
+            apply(it, k, [&] {
+                const bool there = gn_ready(&ws.done[it.sample], wait_ns);
+                if (!there && t == 0) atomicExch(err, kDeviceErrTimeout);
+                return there;
+            });
         } else {
-            sums(it, k);
+            sums(it, k, [&] {
+                if (t == 0 && !a.early) after = atomicAdd(ws.next, 1u);
+            });
             if (join(it, &word[1]) && t == 0 && it.sample != stall) {
                 __threadfence();
                 atomicExch(&ws.done[it.sample], kGnThere);
             }
         }
-        if (t == 0 && !a.early) after = atomicAdd(ws.next, 1u);
+        if (t == 0 && !a.early && it.apply) after = atomicAdd(ws.next, 1u);
         __syncthreads();
         if (t == 0) word[0] = after;
         __syncthreads();
@@ -293,7 +317,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
     float* pm = reinterpret_cast<float*>(slots) + walk_smem<VEC, D, 1>() / 4;  // [ty][W] the threads' means
     float* pq = pm + a.ty * W;                               // [ty][W] and squares
     float2* col = reinterpret_cast<float2*>(pq + a.ty * W);  // [C] the channels'
-    auto sums = [&](const GnItem& it, const GnShare& k) {
+    auto sums = [&](const GnItem& it, const GnShare& k, auto walked) {
         const float inv_rows = 1.f / float(k.rows);
         for (int tile = 0; tile < a.tiles; ++tile) {
             const int c0 = tile * W, c = c0 + k.tx * VEC;
@@ -302,7 +326,8 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             if (k.n > 0 && c < a.C) {
                 const T* const from[1] = {x + k.first + c};
                 bool first = true;
-                walk<T, VEC, D>(from, k.step, k.n, slots, [&](const typename V::Word (&wd)[1]) {
+                Walk<T, VEC, D, 1> walk(from, k.step, k.n, slots);
+                walk.run([&](const typename V::Word (&wd)[1]) {
                     float2 v[P];
                     V::get(wd[0], v);
                     if (first) s.start(v);
@@ -310,6 +335,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
                     s.add(v);
                 });
             }
+            if (tile == a.tiles - 1) walked();
             if (k.ty < a.ty)
                 s.template leave<VEC>(c < a.C ? k.n : 0, pm + k.ty * W + k.tx * VEC, pq + k.ty * W + k.tx * VEC);
             __syncthreads();
@@ -342,23 +368,27 @@ __global__ void __launch_bounds__(kGnBlock, 3)
         });
     };
     auto join = [&](const GnItem& it, unsigned* word) { return gn_joined<true>(it, a, ws, stats_out, word); };
-    auto apply = [&](const GnItem& it, const GnShare& k) {
-        if (k.n == 0) return;
+    auto apply = [&](const GnItem& it, const GnShare& k, auto ready) {
         for (int tile = 0; tile < a.tiles; ++tile) {
             const int c = (tile * a.tx + k.tx) * VEC;
-            if (c >= a.C) continue;
-            const Groups<VEC> g(c, a);
-            const float2* res = ws.result + int64_t(it.sample) * a.G;
+            const bool mine = k.n > 0 && c < a.C;
+            const int64_t at = mine ? k.first + c : 0;
+            const T* const from[1] = {x + at};
+            Walk<T, VEC, D, 1> walk(from, k.step, mine ? k.n : 0, slots);
             float2 mean[P], mul[P], add[P], rstd[P];
-            load_affine<T, VEC>(w, c, 1.f, mul);
-            load_affine<T, VEC>(b, c, 0.f, add);
+            load_affine<T, VEC>(w, mine ? c : 0, 1.f, mul);
+            load_affine<T, VEC>(b, mine ? c : 0, 0.f, add);
+            if (tile == 0 && !ready()) return walk.drop();
+            if (!mine) continue;
+            const Groups<VEC> g(c, a);
+            // past L1: another SM wrote them during this kernel
+            const float2* res = ws.result + int64_t(it.sample) * a.G;
             each_channel<VEC>(mean, [&](int e) { return -__ldcg(&res[g.g[e]]).x; });
             each_channel<VEC>(rstd, [&](int e) { return __ldcg(&res[g.g[e]]).y; });
 #pragma unroll
             for (int j = 0; j < P; ++j) mul[j] = f2_mul(mul[j], rstd[j]);
-            const T* const from[1] = {x + k.first + c};
-            T* py = y + k.first + c;
-            walk<T, VEC, D>(from, k.step, k.n, slots, [&](const typename V::Word (&wd)[1]) {
+            T* py = y + at;
+            walk.run([&](const typename V::Word (&wd)[1]) {
                 float2 v[P];
                 V::get(wd[0], v);
 #pragma unroll
@@ -384,7 +414,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
     float2* red = reinterpret_cast<float2*>(slots) + walk_smem<VEC, D, 2>() / 8;  // [ty][W] the threads' A, Q
     float2* col = red + a.ty * W;  // [C] the channels', times w
     let_next_start();
-    auto sums = [&](const GnItem& it, const GnShare& k) {
+    auto sums = [&](const GnItem& it, const GnShare& k, auto walked) {
         const int64_t slot = int64_t(it.sample) * a.chunks + it.chunk;
         float* cw = ws.chans + slot * 2 * a.C;
         for (int tile = 0; tile < a.tiles; ++tile) {
@@ -394,11 +424,12 @@ __global__ void __launch_bounds__(kGnBlock, 2)
 #pragma unroll
             for (int j = 0; j < P; ++j) sa[j] = sq[j] = slope.rstd[j] = f2(0.f);
             if (k.n > 0 && c < a.C) {
-                slope.load(w, b, stats + int64_t(it.sample) * a.G, c, c, a);
                 const T* const from[2] = {x + k.first + c, dy + k.first + c};
-                walk<T, VEC, D>(from, k.step, k.n, slots,
-                                [&](const typename V::Word (&wd)[2]) { slope.add(wd[0], wd[1], sa, sq); });
+                Walk<T, VEC, D, 2> walk(from, k.step, k.n, slots);
+                slope.load(w, b, stats + int64_t(it.sample) * a.G, c, c, a);
+                walk.run([&](const typename V::Word (&wd)[2]) { slope.add(wd[0], wd[1], sa, sq); });
             }
+            if (tile == a.tiles - 1) walked();
             if (k.ty < a.ty) slope.leave(sa, sq, red + k.ty * W + k.tx * VEC);
             __syncthreads();
             by_teams(min(W, a.C - c0), a.parts_log2, [&](int ch, int lane, bool live) {
@@ -422,19 +453,22 @@ __global__ void __launch_bounds__(kGnBlock, 2)
         });
     };
     auto join = [&](const GnItem& it, unsigned* word) { return gn_joined<false>(it, a, ws, nullptr, word); };
-    auto apply = [&](const GnItem& it, const GnShare& k) {
-        if (k.n == 0) return;
+    auto apply = [&](const GnItem& it, const GnShare& k, auto ready) {
         for (int tile = 0; tile < a.tiles; ++tile) {
             const int c = (tile * a.tx + k.tx) * VEC;
-            if (c >= a.C) continue;
+            const bool mine = k.n > 0 && c < a.C;
+            const int64_t at = mine ? k.first + c : 0;
+            const T* const from[2] = {x + at, dy + at};
+            Walk<T, VEC, D, 2> walk(from, k.step, mine ? k.n : 0, slots);
             GnSlope<T, VEC, ACT> slope;
-            slope.load(w, b, stats + int64_t(it.sample) * a.G, c, c, a);
+            slope.load(w, b, stats + int64_t(it.sample) * a.G, mine ? c : 0, mine ? c : 0, a);
+            if (tile == 0 && !ready()) return walk.drop();
+            if (!mine) continue;
             // past L1: another SM wrote them during this kernel
             const float2* res = ws.result + int64_t(it.sample) * a.G;
             slope.means([&](int g) { return __ldcg(&res[g]); }, c, a);
-            const T* const from[2] = {x + k.first + c, dy + k.first + c};
-            T* po = dx + k.first + c;
-            walk<T, VEC, D>(from, k.step, k.n, slots, [&](const typename V::Word (&wd)[2]) {
+            T* po = dx + at;
+            walk.run([&](const typename V::Word (&wd)[2]) {
                 float2 v[P];
                 slope.of(wd[0], wd[1], v);
                 V::put(po, v);
