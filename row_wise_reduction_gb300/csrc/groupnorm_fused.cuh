@@ -8,7 +8,7 @@
 // copies and stores several times the instructions and shared-memory wavefronts
 // that it moves data with), is worked on box by box as it arrives, and the
 // results go out the same way from the same boxes. Rows that are no whole vectors
-// come and go by single elements.
+// come and go by two elements or one.
 //
 // As many clusters as the device holds at once take the slabs in turn: as soon as a
 // box of one slab has gone out the same box of the next comes in, so the memory
@@ -133,12 +133,12 @@ __device__ __forceinline__ void gn_ask(const GnTile<T, VEC>& k, unsigned slab, c
     for (int i = 0; i < N; ++i) tensor_load(tile + (i * f.boxes + q) * f.pitch, maps[i], x, y, &bars[q]);
 }
 
-// The first slab's copies in (single elements: every slab's).
+// The first slab's copies in (one or two elements: every slab's).
 template <typename T, int VEC, int N>
 __device__ __forceinline__ void gn_fetch(const GnTile<T, VEC>& k, const RowsMap* const (&maps)[N],
                                          const T* const (&from)[N], typename Vec<T, VEC>::Word* tile, uint64_t* bars,
                                          int64_t stall_row) {
-    if constexpr (VEC > 1) {
+    if constexpr (Vec<T, VEC>::kWhole) {
         if (k.t == 0 && k.turn == 0) {
             for (int q = 0; q < k.f.boxes; ++q) mbar_init(&bars[q], 1);
             mbar_init_fence();
@@ -152,7 +152,7 @@ __device__ __forceinline__ void gn_fetch(const GnTile<T, VEC>& k, const RowsMap*
             for (int i = 0; i < N; ++i)
 #pragma unroll 8
                 for (int r = k.ty; r < k.rows; r += k.f.ty)
-                    tile[i * k.f.pitch + r * k.f.tx + k.tx] = from[i][k.at + r * k.a.ld];
+                    tile[i * k.f.pitch + r * k.f.tx + k.tx] = Vec<T, VEC>::load(from[i] + k.at + r * k.a.ld);
         }
     }
 }
@@ -166,7 +166,7 @@ __device__ __forceinline__ int gn_read(const GnTile<T, VEC>& k, const typename V
     k.template each<U, N>(
         tiles,
         [&](int end) {
-            if constexpr (VEC > 1)
+            if constexpr (Vec<T, VEC>::kWhole)
                 for (; q * k.f.box < end; ++q)
                     if (!fail) late |= !mbar_wait(&bars[q], k.turn & 1, wait_ns);
         },
@@ -182,13 +182,14 @@ __device__ __forceinline__ void gn_write(const GnTile<T, VEC>& k, const RowsMap*
                                          const typename Vec<T, VEC>::Word* const (&tiles)[N], uint64_t* bars,
                                          int fail, F g) {
     const GnFused& f = k.f;
-    const bool more = VEC > 1 && !fail && k.more();
-    const int whole = VEC > 1 ? k.rows / f.box * f.box : 0;  // positions that go out as boxes
+    constexpr bool kWhole = Vec<T, VEC>::kWhole;
+    const bool more = kWhole && !fail && k.more();
+    const int whole = kWhole ? k.rows / f.box * f.box : 0;  // positions that go out as boxes
     int q = 0;
     k.template each<U, N>(
         tiles, [](int) {}, [&](const typename Vec<T, VEC>::Word (&w)[N], int at, int r) { g(w, at, r, r < whole); },
         [&](int end) {
-            if constexpr (VEC > 1) {
+            if constexpr (Vec<T, VEC>::kWhole) {
                 for (; min((q + 1) * f.box, k.rows) <= end && q * f.box < k.rows; ++q) {
                     fence_proxy_async_smem();
                     __syncthreads();
@@ -206,7 +207,7 @@ __device__ __forceinline__ void gn_write(const GnTile<T, VEC>& k, const RowsMap*
                 }
             }
         });
-    if (VEC > 1 && k.t == 0 && !fail && k.rows > 0) {
+    if (kWhole && k.t == 0 && !fail && k.rows > 0) {
         tensor_stores_read<0>();
         if (more) gn_ask<T, VEC, N>(k, k.slab + k.stride, maps, tile, bars, (k.rows - 1) / f.box, 0u);
     }
@@ -214,9 +215,9 @@ __device__ __forceinline__ void gn_write(const GnTile<T, VEC>& k, const RowsMap*
 
 // After a wait that ran out: nothing more is asked for or written; the copies still
 // in flight get one more wait, and the error word is set.
-template <int VEC, typename K>
-__device__ __forceinline__ void break_waits(const K& k, uint64_t* bars, unsigned* err, unsigned long long wait_ns) {
-    if (VEC == 1 || k.t != 0) return;
+template <typename T, int VEC>
+__device__ __forceinline__ void break_waits(const GnTile<T, VEC>& k, uint64_t* bars, unsigned* err, unsigned long long wait_ns) {
+    if (!Vec<T, VEC>::kWhole || k.t != 0) return;
     for (int q = 0; q * k.f.box < k.rows; ++q) mbar_wait(&bars[q], k.turn & 1, wait_ns);
     atomicExch(err, kDeviceErrTimeout);
 }
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
                         if (whole) V::keep(&tile[at], v);
                         else if (!fail) V::put(py + r * a.ld, v);
                     });
-        if (fail && !before) break_waits<VEC>(k, bars, err, wait_ns);
+        if (fail && !before) break_waits(k, bars, err, wait_ns);
     }
 }
 
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
                         if (whole) V::keep(&tx[at], v);
                         else if (!fail) V::put(po + r * a.ld, v);
                     });
-        if (fail && !before) break_waits<VEC>(k, bars, err, wait_ns);
+        if (fail && !before) break_waits(k, bars, err, wait_ns);
     }
 }
 
@@ -457,7 +458,7 @@ inline cudaError_t gn_cluster_launch(const void* kern, const GnFused& f, int64_t
 
 template <typename T, int VEC>
 cudaError_t gn_map(RowsMap* m, const void* p, const GnArgs& a, const GnFused& f) {
-    if (VEC == 1) return cudaSuccess;
+    if (!Vec<T, VEC>::kWhole) return cudaSuccess;
     return rows_map(m, p, a.C * int64_t(sizeof(T)), int64_t(a.B) * a.S, a.ld * int64_t(sizeof(T)),
                     f.W * int(sizeof(T)), f.box);
 }

@@ -22,22 +22,25 @@ cudaError_t gn_backward_launch(const void* x, const void* dy, const void* w, con
 }
 
 template <typename T>
-GnForwardLaunch gn_forward_table(bool vec, int act) {
+GnForwardLaunch gn_forward_table(int vec, int act) {
     constexpr int V = Elem<T>::kVec;
-    static const GnForwardLaunch t[2][4] = {
+    static const GnForwardLaunch t[3][4] = {
         {gn_forward_launch<T, 1, 0>, gn_forward_launch<T, 1, 1>, gn_forward_launch<T, 1, 2>, gn_forward_launch<T, 1, 3>},
+        {gn_forward_launch<T, 2, 0>, gn_forward_launch<T, 2, 1>, gn_forward_launch<T, 2, 2>, gn_forward_launch<T, 2, 3>},
         {gn_forward_launch<T, V, 0>, gn_forward_launch<T, V, 1>, gn_forward_launch<T, V, 2>, gn_forward_launch<T, V, 3>}};
-    return t[vec][act];
+    return t[vec < 2 ? 0 : (vec == 2 ? 1 : 2)][act];
 }
 
 template <typename T>
-GnBackwardLaunch gn_backward_table(bool vec, int act) {
+GnBackwardLaunch gn_backward_table(int vec, int act) {
     constexpr int V = Elem<T>::kVec;
-    static const GnBackwardLaunch t[2][4] = {{gn_backward_launch<T, 1, 0>, gn_backward_launch<T, 1, 1>,
+    static const GnBackwardLaunch t[3][4] = {{gn_backward_launch<T, 1, 0>, gn_backward_launch<T, 1, 1>,
                                               gn_backward_launch<T, 1, 2>, gn_backward_launch<T, 1, 3>},
+                                             {gn_backward_launch<T, 2, 0>, gn_backward_launch<T, 2, 1>,
+                                              gn_backward_launch<T, 2, 2>, gn_backward_launch<T, 2, 3>},
                                              {gn_backward_launch<T, V, 0>, gn_backward_launch<T, V, 1>,
                                               gn_backward_launch<T, V, 2>, gn_backward_launch<T, V, 3>}};
-    return t[vec][act];
+    return t[vec < 2 ? 0 : (vec == 2 ? 1 : 2)][act];
 }
 
 }  // namespace rowops

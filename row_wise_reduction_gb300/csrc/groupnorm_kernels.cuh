@@ -32,41 +32,50 @@ namespace rowops {
 
 namespace cg = cooperative_groups;
 
-// A vector of VEC channels as P pairs (one element: the second half is 0).
+// A vector of VEC channels as P pairs: 16 bytes, or two elements, or one (whose
+// pair's second half is 0).
 template <typename T, int VEC>
 struct Vec {
     using E = Elem<T>;
-    using Word = std::conditional_t<VEC == 1, T, uint4>;
+    static constexpr bool kWhole = VEC * sizeof(T) == 16;
+    static_assert(kWhole || VEC <= 2, "16 bytes, or one or two elements");
+    using Two = std::conditional_t<sizeof(T) == 4, uint2, uint32_t>;
+    using Word = std::conditional_t<kWhole, uint4, std::conditional_t<VEC == 1, T, Two>>;
     static constexpr int P = VEC == 1 ? 1 : VEC / 2;
-    __device__ __forceinline__ static Word load(const T* p) {
-        if constexpr (VEC == 1) return *p;
-        else return *reinterpret_cast<const uint4*>(p);
-    }
+    __device__ __forceinline__ static Word load(const T* p) { return *reinterpret_cast<const Word*>(p); }
     __device__ __forceinline__ static void get(const Word& w, float2 (&v)[P]) {
-        if constexpr (VEC == 1) {
-            v[0] = make_float2(E::load(&w), 0.f);
-        } else {
+        if constexpr (kWhole) {
             float f[VEC];
             E::unpack(w, f);
 #pragma unroll
             for (int k = 0; k < P; ++k) v[k] = make_float2(f[2 * k], f[2 * k + 1]);
+        } else if constexpr (VEC == 1) {
+            v[0] = make_float2(E::load(&w), 0.f);
+        } else if constexpr (sizeof(T) == 4) {
+            v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+        } else {
+            v[0] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
         }
     }
     __device__ __forceinline__ static Word pack(const float2 (&v)[P]) {
-        if constexpr (VEC == 1) {
-            Word w;
-            E::store(&w, v[0].x);
-            return w;
-        } else {
+        if constexpr (kWhole) {
             float f[VEC];
 #pragma unroll
             for (int k = 0; k < P; ++k) f[2 * k] = v[k].x, f[2 * k + 1] = v[k].y;
             return E::pack(f);
+        } else if constexpr (VEC == 1) {
+            Word w;
+            E::store(&w, v[0].x);
+            return w;
+        } else if constexpr (sizeof(T) == 4) {
+            return make_uint2(__float_as_uint(v[0].x), __float_as_uint(v[0].y));
+        } else {
+            return pack_bf16x2(v[0].x, v[0].y);
         }
     }
     __device__ __forceinline__ static void put(T* p, const float2 (&v)[P]) {
-        if constexpr (VEC == 1) E::store(p, v[0].x);
-        else st_stream16(p, pack(v));
+        if constexpr (kWhole) st_stream16(p, pack(v));
+        else *reinterpret_cast<Word*>(p) = pack(v);
     }
     __device__ __forceinline__ static void keep(Word* p, const float2 (&v)[P]) { *p = pack(v); }  // shared memory
 };
@@ -104,7 +113,7 @@ template <typename T, int VEC, int P>
 __device__ __forceinline__ void load_affine(const T* p, int c, float dflt, float2 (&v)[P]) {
     using V = Vec<T, VEC>;
     if (!p) each_channel<VEC>(v, [&](int) { return dflt; });
-    else if (VEC > 1 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) V::get(V::load(p + c), v);
+    else if (VEC > 1 && reinterpret_cast<uintptr_t>(p) % sizeof(typename V::Word) == 0) V::get(V::load(p + c), v);
     else each_channel<VEC>(v, [&](int e) { return Elem<T>::load(p + c + e); });
 }
 

@@ -21,7 +21,7 @@ namespace rowops {
 // A thread's n positions, `step` elements apart, of N tensors: run(f) calls f(words)
 // for each in order. Vectors come through a ring of copies, D positions on their
 // way, the first of them asked for by the constructor: what else a pass needs first
-// (its parameters, a wait) goes between. Single elements: U at a time.
+// (its parameters, a wait) goes between. One or two elements: U positions at a time.
 template <typename T, int VEC, int D, int N>
 struct Walk {
     using V = Vec<T, VEC>;
@@ -33,7 +33,7 @@ struct Walk {
         : step(step_), n(n_), at(slots + threadIdx.x) {
 #pragma unroll
         for (int k = 0; k < N; ++k) p[k] = from[k];
-        if constexpr (VEC > 1)
+        if constexpr (V::kWhole)
 #pragma unroll
             for (int d = 0; d < D - 1; ++d) ask(d, d);
     }
@@ -48,11 +48,11 @@ struct Walk {
     }
     // for a walk that does not run
     __device__ __forceinline__ void drop() const {
-        if constexpr (VEC > 1) asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (V::kWhole) asm volatile("cp.async.wait_all;" ::: "memory");
     }
     template <typename F>
     __device__ __forceinline__ void run(F f) {
-        if constexpr (VEC > 1) {
+        if constexpr (V::kWhole) {
             // unrolled over the ring, so that a slot's place is a constant
 #pragma unroll 1
             for (int i = 0; i < n; i += D) {
@@ -89,9 +89,9 @@ struct Walk {
         }
     }
 };
-template <int VEC, int D, int N>
+template <typename T, int VEC, int D, int N>
 constexpr size_t walk_smem() {
-    return VEC > 1 ? size_t(D) * N * kGnBlock * 16 : 0;
+    return Vec<T, VEC>::kWhole ? size_t(D) * N * kGnBlock * 16 : 0;
 }
 
 // The workspace: the item counter and counters for each sample (zeroed before the
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
     constexpr int P = V::P, D = kGnStreamDepth;
     extern __shared__ __align__(16) uint4 slots[];  // the positions on their way, then:
     const int W = a.tx * VEC;
-    float* pm = reinterpret_cast<float*>(slots) + walk_smem<VEC, D, 1>() / 4;  // [ty][W] the threads' means
+    float* pm = reinterpret_cast<float*>(slots) + walk_smem<T, VEC, D, 1>() / 4;  // [ty][W] the threads' means
     float* pq = pm + a.ty * W;                               // [ty][W] and squares
     float2* col = reinterpret_cast<float2*>(pq + a.ty * W);  // [C] the channels'
     auto sums = [&](const GnItem& it, const GnShare& k, auto walked) {
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
     constexpr int P = V::P, D = kGnStreamDepthBwd;
     extern __shared__ __align__(16) uint4 slots[];  // the positions on their way, then:
     const int W = a.tx * VEC;
-    float2* red = reinterpret_cast<float2*>(slots) + walk_smem<VEC, D, 2>() / 8;  // [ty][W] the threads' A, Q
+    float2* red = reinterpret_cast<float2*>(slots) + walk_smem<T, VEC, D, 2>() / 8;  // [ty][W] the threads' A, Q
     float2* col = red + a.ty * W;  // [C] the channels', times w
     let_next_start();
     auto sums = [&](const GnItem& it, const GnShare& k, auto walked) {
@@ -548,7 +548,7 @@ cudaError_t gn_forward_stream(const void* x, void* y, const void* w, const void*
     int stall = cfg.stall_row < 0 ? -1 : int(cfg.stall_row / a.S);
     void* args[] = {&x, &y, &w, &b, &stats, &ws, &a, &err, &wait_ns, &stall};
     return gn_stream_launch(reinterpret_cast<const void*>(gn_stream_kernel<T, VEC, ACT>), a, ws, workspace, VEC,
-                            walk_smem<VEC, kGnStreamDepth, 1>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C), false, args,
+                            walk_smem<T, VEC, kGnStreamDepth, 1>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C), false, args,
                             cfg);
 }
 
@@ -563,7 +563,7 @@ cudaError_t gn_backward_stream(const void* x, const void* dy, const void* w, con
     void* args[] = {&x, &dy, &dx, &w, &b, &stats, &ws, &a, &err, &wait_ns, &stall};
     const cudaError_t e =
         gn_stream_launch(reinterpret_cast<const void*>(gn_bwd_stream_kernel<T, VEC, ACT>), a, ws, workspace, VEC,
-                         walk_smem<VEC, kGnStreamDepthBwd, 2>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C), true, args,
+                         walk_smem<T, VEC, kGnStreamDepthBwd, 2>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C), true, args,
                          cfg);
     return e == cudaSuccess ? gn_reduce_channels(ws.chans, int64_t(a.B) * a.chunks, a.C, dw, db, cfg) : e;
 }

@@ -1130,13 +1130,13 @@ struct GnChoice {
     GnFused f;
 };
 const GnChoice& gn_choose(int64_t B, int64_t S, int64_t C, int64_t G, int es, int tensors, int vec, int knob) {
-    static thread_local GnChoice kept[8];
+    static thread_local GnChoice kept[16];
     static thread_local unsigned next = 0;
     for (const GnChoice& k : kept)
         if (k.B == B && k.S == S && k.C == C && k.G == G && k.es == es && k.tensors == tensors && k.vec == vec &&
             k.knob == knob)
             return k;
-    GnChoice& k = kept[next++ % 8];
+    GnChoice& k = kept[next++ % 16];
     k = GnChoice{};
     k.B = B, k.S = S, k.C = C, k.G = G, k.es = es, k.tensors = tensors, k.vec = vec, k.knob = knob;
     const GnArgs a = gn_plan(B, S, C, G, C, es, tensors, 0.f);
@@ -1150,7 +1150,7 @@ const GnChoice& gn_choose(int64_t B, int64_t S, int64_t C, int64_t G, int es, in
 // every CTA of a cluster.
 size_t gn_bytes(int64_t B, int64_t S, int64_t C, int64_t G, int es, int tensors, int knob) {
     size_t most = 0;
-    for (const int vec : {1, 16 / es}) {
+    for (const int vec : {1, 2, 16 / es}) {
         if (C % vec) continue;
         const GnChoice& k = gn_choose(B, S, C, G, es, tensors, vec, knob);
         most = std::max(most, !k.one ? gn_stream_bytes(gn_plan(B, S, C, G, C, es, tensors, 0.f), tensors)
@@ -1167,12 +1167,20 @@ rowops_status_t make_mask(float p, uint64_t seed, uint64_t offset, const uint64_
     return ROWOPS_OK;
 }
 
-// Rows of 16-byte vectors for the operators that go by them or by elements.
-bool vector_rows(const Tuning& tn, int64_t N, int64_t ld, int es, std::initializer_list<const void*> ptrs) {
-    if (tn.family == Family::Looped || N % (16 / es) != 0 || (ld * es) % 16 != 0) return false;
+// Rows of whole vectors of n elements, for the operators that go by them or by elements.
+bool rows_of(int n, const Tuning& tn, int64_t N, int64_t ld, int es, std::initializer_list<const void*> ptrs) {
+    if (tn.family == Family::Looped || N % n != 0 || ld % n != 0) return false;
     for (const void* p : ptrs)
-        if (!aligned(p, 16)) return false;
+        if (!aligned(p, size_t(n) * es)) return false;
     return true;
+}
+bool vector_rows(const Tuning& tn, int64_t N, int64_t ld, int es, std::initializer_list<const void*> ptrs) {
+    return rows_of(16 / es, tn, N, ld, es, ptrs);
+}
+// The elements of the widest access: 16 bytes of them, two or one (group norm's
+// backward pass, fp32 S13107 C990: by two 75 us, by one 107).
+int row_access(const Tuning& tn, int64_t N, int64_t ld, int es, std::initializer_list<const void*> ptrs) {
+    return vector_rows(tn, N, ld, es, ptrs) ? 16 / es : rows_of(2, tn, N, ld, es, ptrs) ? 2 : 1;
 }
 }  // namespace
 
@@ -1205,10 +1213,10 @@ rowops_status_t rowops_groupnorm_act(const void* x, void* y, const void* w, cons
     const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
-    const bool vec = vector_rows(tn, C, ld, es, {x, y});
+    const int vec = row_access(tn, C, ld, es, {x, y});
     const GnForwardLaunch fn = dtype == ROWOPS_F32 ? gn_forward_f32(vec, act) : gn_forward_bf16(vec, act);
     const GnArgs a = gn_plan(B, S, C, G, ld, es, 1, eps);
-    const GnChoice& k = gn_choose(B, S, C, G, es, 1, vec ? 16 / es : 1, tn.groupnorm);
+    const GnChoice& k = gn_choose(B, S, C, G, es, 1, vec, tn.groupnorm);
     return finish(fn(x, y, w, b, stats, workspace, a, k.one ? &k.f : nullptr, cfg));
 }
 
@@ -1252,10 +1260,10 @@ rowops_status_t rowops_groupnorm_act_backward(const void* x, const void* dy, con
     const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
-    const bool vec = vector_rows(tn, C, ld, es, {x, dy, dx});
+    const int vec = row_access(tn, C, ld, es, {x, dy, dx});
     const GnBackwardLaunch fn = dtype == ROWOPS_F32 ? gn_backward_f32(vec, act) : gn_backward_bf16(vec, act);
     const GnArgs a = gn_plan(B, S, C, G, ld, es, 2, 0.f);
-    const GnChoice& k = gn_choose(B, S, C, G, es, 2, vec ? 16 / es : 1, tn.groupnorm);
+    const GnChoice& k = gn_choose(B, S, C, G, es, 2, vec, tn.groupnorm);
     return finish(fn(x, dy, w, b, stats, dx, dw, db, workspace, a, k.one ? &k.f : nullptr, cfg));
 }
 

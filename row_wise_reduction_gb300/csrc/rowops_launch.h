@@ -358,7 +358,7 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
     for (int blocks = 1; blocks <= a.G; ++blocks) {
         if (a.G % blocks) continue;
         const int W = a.C / blocks, tx = (W + vec - 1) / vec;
-        if (W % vec || tx > kGnBlock || (vec > 1 && W * es > 2048)) continue;
+        if (W % vec || tx > kGnBlock || (vec * es == 16 && W * es > 2048)) continue;
         if (blocks > 1 && W * es < 64) break;
         for (int cl = 0; cl <= 4; ++cl) {
             const int cluster = 1 << cl;
@@ -373,13 +373,13 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
             f.inv_tx = (65536 + tx - 1) / tx;
             f.rows = int(rows);
             // four copies where they are worth it, of at most 256 rows; slots of 128 bytes
-            f.boxes = vec == 1 ? 1 : int(std::max<int64_t>(rows * W * es >= 16384 ? 4 : 1, (rows + 255) / 256));
+            f.boxes = vec * es < 16 ? 1 : int(std::max<int64_t>(rows * W * es >= 16384 ? 4 : 1, (rows + 255) / 256));
             f.box = int((rows + f.boxes - 1) / f.boxes);
             if (f.boxes > 1) f.box = std::min((f.box + 7) / 8 * 8, 256);  // whole slots, one after the other
             f.boxes = int((rows + f.box - 1) / f.box);
             if (f.boxes > kGnMaxBoxes) continue;
             const int unit = 128 / (vec * es);
-            f.pitch = vec == 1 ? f.box * tx : (f.box * tx + unit - 1) / unit * unit;
+            f.pitch = vec * es < 16 ? f.box * tx : (f.box * tx + unit - 1) / unit * unit;
             f.tile = (size_t(tensors) * f.boxes * f.pitch * vec * es + 127) / 128 * 128;
             const size_t groups = size_t(W / a.L);
             f.smem = f.tile + size_t(f.ty) * W * 8 + size_t(W) * 8 + groups * 8 * (1 + 2 * cluster) + f.boxes * 8 +
@@ -392,7 +392,7 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
             const double slabs = double(a.B) * blocks, held = std::min(slabs, double(kGnClusters[per_sm - 1][cl]));
             const double turns = std::ceil(slabs / held), slots = std::ceil(double(rows) / f.ty);
             const double ctas_sm = std::ceil(held * cluster / kGnSms);
-            const double slot = (tensors == 1 ? 0.26 : ctas_sm > 1 ? 0.52 : 0.7) * (vec == 1 ? 0.4 : es == 4 ? 0.67 : 1.0);
+            const double slot = (tensors == 1 ? 0.26 : ctas_sm > 1 ? 0.52 : 0.7) * (vec <= 2 ? 0.4 : es == 4 ? 0.67 : 1.0);
             const double exchange = cluster > 1 ? 2.0 : 1.0;
             double t = std::max(all / 6.8e6, turns * (ctas_sm * slots * slot + exchange / ctas_sm)) + 4.5 + exchange / 2;
             if (least < 0 || t < least) {
@@ -417,10 +417,11 @@ using GnForwardLaunch = cudaError_t (*)(const void* x, void* y, const void* w, c
 using GnBackwardLaunch = cudaError_t (*)(const void* x, const void* dy, const void* w, const void* b,
                                          const float* stats, void* dx, float* dw, float* db, void* ws, GnArgs a,
                                          const GnFused* f, const LaunchCfg& cfg);
-GnForwardLaunch gn_forward_f32(bool vec, int act);
-GnForwardLaunch gn_forward_bf16(bool vec, int act);
-GnBackwardLaunch gn_backward_f32(bool vec, int act);
-GnBackwardLaunch gn_backward_bf16(bool vec, int act);
+// vec: elements of a thread's access: 16 bytes of them, two or one
+GnForwardLaunch gn_forward_f32(int vec, int act);
+GnForwardLaunch gn_forward_bf16(int vec, int act);
+GnBackwardLaunch gn_backward_f32(int vec, int act);
+GnBackwardLaunch gn_backward_bf16(int vec, int act);
 
 // dynamic shared memory of the row-pipeline kernels
 inline size_t tma_row_bytes(int64_t N, int es) { return size_t((N * es + 127) / 128 * 128); }
