@@ -85,7 +85,9 @@
  *                                 split softmax on full chunks the same for work item <row>,
  *                                 i.e. chunk (row mod nchunks) of row row / nchunks; in the
  *                                 single-read split softmax CTA 0 withholds that row's partial,
- *                                 in the row-group form the CTA of its first slice does).
+ *                                 in the row-group form the CTA of its first slice does; group
+ *                                 norm, rows as B * S positions: the copy in that holds it, or,
+ *                                 streamed, the results of its sample).
  *                                 Nothing faults or hangs: the wait gives up at its limit, the
  *                                 kernel records ROWOPS_ERR_TIMEOUT and returns.
  */
@@ -193,8 +195,8 @@ rowops_status_t rowops_row_max(const void* x, float* out, int64_t M, int64_t N, 
  * Synchronises `stream`, then reads and clears the library's device error word
  * on the current device. Kernels that wait on asynchronous copies (the TMA-fed
  * row pipeline behind rowops_softmax, rowops_layernorm_gelu and the RMSNorm
- * entry points, and the chunked LayerNorm+GELU of short rows) bound every
- * wait; if one gives up, the kernel stops, records ROWOPS_ERR_TIMEOUT there,
+ * entry points, the chunked LayerNorm+GELU of short rows, and group norm) bound
+ * every wait; if one gives up, the kernel stops, records ROWOPS_ERR_TIMEOUT there,
  * and the outputs of that call are unspecified. Returns ROWOPS_OK,
  * ROWOPS_ERR_TIMEOUT, or ROWOPS_ERR_CUDA if a CUDA call fails.
  */
@@ -437,8 +439,8 @@ rowops_status_t rowops_fused_residual_rmsnorm(const void* x, const void* residua
  *           (overwritten; 0 where one kernel does it: NULL will do), apart from the
  *           other tensors; calls sharing it must be ordered on one stream.
  * C is at most 8192 and B at most 2^30 (ROWOPS_ERR_UNSUPPORTED beyond), C a
- * multiple of G. B == 0
- * or S == 0 is a no-op. A NaN or an infinity in a group makes that group of that
+ * multiple of G. B == 0 or S == 0 is a no-op. 16-byte aligned positions of whole
+ * 16-byte vectors are the fastest, an even C and ld the next. A NaN or an infinity in a group makes that group of that
  * sample NaN. The variance is merged from centred partial sums, so a mean far
  * from zero costs it no precision.
  */
@@ -502,8 +504,8 @@ rowops_status_t rowops_groupnorm_act_backward(const void* x, const void* dy, con
  *              kernel adds to `offset` (mod 2^64): a captured graph replays with
  *              new masks when the caller changes it between replays.
  * M is at most 2^32 (ROWOPS_ERR_UNSUPPORTED beyond). 16-byte aligned rows and N a
- * multiple of the 16-byte vector take vector accesses, other layouts single
- * elements.
+ * multiple of the 16-byte vector are the fastest; rows at changing offsets from a
+ * 16-byte boundary, the same in x, residual and y, still move as vectors inside.
  */
 rowops_status_t rowops_bias_dropout_residual(const void* x, const void* residual, const void* bias, void* y, float p,
                                              uint64_t seed, uint64_t offset, const uint64_t* device_offset,

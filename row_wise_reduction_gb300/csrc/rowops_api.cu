@@ -160,6 +160,15 @@ struct OccEntry {
     int blocks_per_sm;
 };
 std::vector<OccEntry> g_occ;
+// Under g_mu. Group norm's shared memory follows the shape, so a program of many
+// shapes would make the search longer and longer: it starts again at 256.
+void keep_occupancy(const OccEntry& e) {
+    if (g_occ.size() >= 256) g_occ.clear();
+    try {
+        g_occ.push_back(e);
+    } catch (...) {  // not kept: asked for again
+    }
+}
 
 struct SmemEntry {
     const void* func;
@@ -493,7 +502,7 @@ int ctas_per_sm(const void* func, int block, size_t smem, const LaunchCfg& cfg) 
         cudaGetLastError();
         n = 0;
     }
-    g_occ.push_back(OccEntry{func, cfg.ctx, block, smem, n});
+    keep_occupancy(OccEntry{func, cfg.ctx, block, smem, n});
     return n;
 }
 
@@ -518,7 +527,7 @@ int clusters_on_device(const void* func, int block, size_t smem, int cluster, co
         n = 0;
     }
     if (n < 1) n = 1;
-    g_occ.push_back(OccEntry{func, cfg.ctx, key, smem, n});
+    keep_occupancy(OccEntry{func, cfg.ctx, key, smem, n});
     return n;
 }
 
@@ -1167,6 +1176,9 @@ rowops_status_t make_mask(float p, uint64_t seed, uint64_t offset, const uint64_
     return ROWOPS_OK;
 }
 
+// One row has no stride: whatever a caller gives, a copy's descriptor takes at most 2^40 bytes.
+int64_t row_stride(int64_t M, int64_t C, int64_t ld) { return M == 1 ? (C + 15) / 16 * 16 : ld; }
+
 // Rows of whole vectors of n elements, for the operators that go by them or by elements.
 bool rows_of(int n, const Tuning& tn, int64_t N, int64_t ld, int es, std::initializer_list<const void*> ptrs) {
     if (tn.family == Family::Looped || N % n != 0 || ld % n != 0) return false;
@@ -1210,6 +1222,7 @@ rowops_status_t rowops_groupnorm_act(const void* x, void* y, const void* w, cons
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ROWOPS_ERR_WORKSPACE;
     if (need && !apart_from({workspace, workspace_bytes}, {{x, rows}, {y, rows}, {w, row}, {b, row}, {stats, sb}}))
         return ROWOPS_ERR_INVALID_VALUE;
+    ld = row_stride(M, C, ld);
     const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
@@ -1257,6 +1270,7 @@ rowops_status_t rowops_groupnorm_act_backward(const void* x, const void* dy, con
         if (need && !apart(workspace, workspace_bytes, r.p, r.n)) return ROWOPS_ERR_INVALID_VALUE;
     if (need && !apart_from({workspace, workspace_bytes}, {{dx, rows}, {dw, sums}, {db, sums}}))
         return ROWOPS_ERR_INVALID_VALUE;
+    ld = row_stride(M, C, ld);
     const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;

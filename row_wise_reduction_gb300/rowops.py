@@ -298,7 +298,7 @@ def _xy(x: torch.Tensor, y: Optional[torch.Tensor]):
     else:
         if y.dtype is not dt or y.get_device() != dev or y.shape != sh:
             raise ValueError("y must match x in shape, dtype and device")
-        if M > 1 and y.stride() != st:
+        if y.stride() != st and (M > 1 or (N > 1 and y.stride(1) != 1)):
             raise ValueError("x and y must share the row stride")
     return M, N, (st[0] if M > 1 else max(N, st[0])), y, code, dev
 
@@ -671,7 +671,7 @@ def _like_positions(x: torch.Tensor, ld: int, t: Optional[torch.Tensor], name: s
         return torch.empty_strided(x.shape, (x.shape[1] * ld, ld, 1), dtype=x.dtype, device=x.device)
     if t.dtype is not x.dtype or t.get_device() != x.get_device() or t.shape != x.shape:
         raise ValueError(f"{name} must match x in shape, dtype and device")
-    if t.stride() != x.stride() and x.shape[0] * x.shape[1] > 1 and _positions(t, name)[3] != ld:
+    if t.stride() != x.stride() and _positions(t, name)[3] != ld and x.shape[0] * x.shape[1] > 1:
         raise ValueError(f"x and {name} must share the stride of their positions")
     return t
 
@@ -807,7 +807,9 @@ def rowops_bias_dropout_residual(
                           device_offset=device_offset)
     M, N, ld, y, code, dev = _xy(x, y)
     if residual is not None and (residual.dtype is not x.dtype or residual.get_device() != dev
-                                 or residual.shape != x.shape or (M > 1 and residual.stride() != x.stride())):
+                                 or residual.shape != x.shape
+                                 or (residual.stride() != x.stride()
+                                     and (M > 1 or (N > 1 and residual.stride(1) != 1)))):
         raise ValueError("residual must match x in shape, dtype, device and row stride")
     st = (_calls or _hot_calls()).bias_dropout_residual(
         x.data_ptr(), None if residual is None else residual.data_ptr(), _affine(bias, x, N, dev, "bias"),

@@ -178,3 +178,19 @@ def test_no_rows_and_refusals():
         ro.rowops_bias_dropout_residual(x, device_offset=torch.zeros(1, device="cuda"))
     with pytest.raises(ValueError):
         ro.rowops_bias_dropout_residual_backward(x, dbias=torch.zeros(24, device="cuda"), bias_grad=False)
+
+
+@pytest.mark.parametrize("what", ["y", "residual", "dx"])
+def test_one_row_of_spread_columns_is_refused(what):
+    """A single row has no row stride to compare, but its columns must be neighbours."""
+    x = torch.ones(1, 24, device="cuda")
+    spread = torch.zeros(1, 48, device="cuda")[:, ::2]
+    with pytest.raises(ValueError):
+        if what == "y":
+            ro.rowops_bias_dropout_residual(x, y=spread)
+        elif what == "residual":
+            ro.rowops_bias_dropout_residual(x, spread)
+        else:
+            ro.rowops_bias_dropout_residual_backward(x, dx=spread)
+    wide = torch.as_strided(torch.zeros(24, device="cuda"), (1, 24), (1000, 1))  # its stride leads nowhere: no matter
+    assert torch.equal(ro.rowops_bias_dropout_residual(x, wide, p=0.0, y=torch.empty_like(wide)), x)

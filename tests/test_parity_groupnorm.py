@@ -235,6 +235,32 @@ def test_refusals_of_the_binding():
         ro.rowops_groupnorm_act(x, 5)
 
 
+def test_one_position():
+    """One position has no stride: any that a caller gives does, but its channels must
+    be neighbours."""
+    x = torch.arange(16, device="cuda").float().view(1, 1, 16)
+    want = ro.rowops_groupnorm_act(x, 2)
+    far = torch.as_strided(x, (1, 1, 16), (1 << 45, 1 << 45, 1))
+    assert torch.equal(ro.rowops_groupnorm_act(far, 2, y=torch.empty_like(x)), want)
+    stats = torch.empty(1, 2, 2, device="cuda")
+    ro.rowops_groupnorm_act(far, 2, y=torch.empty_like(x), stats=stats)
+    dx = ro.rowops_groupnorm_act_backward(far, x, stats, 2, dx=torch.empty_like(x))[0]
+    assert torch.equal(dx, ro.rowops_groupnorm_act_backward(x, x, stats, 2)[0])
+    spread = torch.zeros(1, 1, 32, device="cuda")[..., ::2]
+    with pytest.raises(ValueError):
+        ro.rowops_groupnorm_act(x, 2, y=spread)
+    with pytest.raises(ValueError):
+        ro.rowops_groupnorm_act_backward(x, spread, stats, 2)
+
+
+def test_many_shapes():
+    """More shapes than the launch choices that are kept: the same results again."""
+    x = torch.randn(1, 700, 32, device="cuda")
+    first = [ro.rowops_groupnorm_act(x[:, :s], 4) for s in range(1, 700)]
+    for s in (1, 2, 77, 350, 699):
+        assert torch.equal(ro.rowops_groupnorm_act(x[:, :s], 4), first[s - 1])
+
+
 FORMS = ["fused", "stream"]
 
 
