@@ -280,15 +280,19 @@ struct GnArgs {
     int64_t chunk_rows;         // positions of a chunk
 };
 
-// The streaming form's chunks: of about 128 KiB, whole waves of CTAs where there are
-// few (two CTAs for each SM backward, three forward), at least 16 KiB.
+// The streaming form's chunks: large, as an item's start and end cost a CTA some 4 us,
+// but not so large that the second read misses L2; whole waves of CTAs where there are
+// few (two CTAs for each SM backward, three forward), at least 16 KiB. Chunks of 128,
+// 256, 512 KiB, bf16: B32 S4096 C320 backward 98, 85, 78 us, B128 342, 294, 271;
+// B8 S65536 C128 159, 126, 115; of 128, 192, 384 KiB, forward, the last two 164, 160,
+// 175 and 81, 75, 75.
 inline GnArgs gn_plan(int64_t B, int64_t S, int64_t C, int64_t G, int64_t ld, int es, int tensors, float eps) {
     GnArgs a{};
     a.S = S, a.ld = ld, a.B = int(B), a.C = int(C), a.G = int(G), a.L = int(C / G), a.eps = eps;
     a.inv_L = 1.f / a.L, a.inv_S = float(1.0 / S), a.inv_m = float(1.0 / (double(S) * a.L));
     const double sample = double(S) * C * es * tensors;
     const int64_t ctas = (tensors > 1 ? 2 : 3) * kGnSms;
-    int64_t n = int64_t(std::ceil(sample / (128.0 * 1024)));
+    int64_t n = int64_t(std::ceil(sample / (tensors > 1 ? 512.0 * 1024 : 192.0 * 1024)));
     if (B * n < 4 * ctas) n = std::max(int64_t(1), std::max(int64_t(1), B * n / ctas) * ctas / B);
     n = std::min(n, std::max(int64_t(1), int64_t(sample / 16384)));
     n = std::min(n, S);
@@ -405,11 +409,11 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
 }
 
 // The streaming form's modelled time: launches and the ends of the sums, and its
-// traffic at what it measured. Modelled and measured in us, the same sizes: 25 and 25,
-// 38 and 34, with B32 49 and 49, 101 and 100; odd C (21 and 22).
+// traffic at what it measured. Modelled and measured in us, the same sizes: 26 and 25,
+// 33 and 32, with B32 52 and 48, 80 and 78; odd C 20 and 21.
 inline double gn_stream_time(const GnArgs& a, int es, int tensors) {
     const double in = double(a.B) * a.S * a.C * es * tensors;
-    return 17.0 + (in + in / tensors) / (tensors == 1 ? 5.2e6 : 3.0e6);
+    return 17.0 + (in + in / tensors) / (tensors == 1 ? 4.8e6 : 4.0e6);
 }
 
 using GnForwardLaunch = cudaError_t (*)(const void* x, void* y, const void* w, const void* b, float* stats, void* ws,
