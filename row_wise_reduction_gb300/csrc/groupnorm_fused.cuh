@@ -19,6 +19,12 @@
 // all CTAs of the cluster and then meets them at one cluster barrier; each adds
 // up what it got in order of rank. Sums are joined as (mean, squares about it) about
 // one of their own members, so no more than the count of members cancels.
+//
+// bf16 SiLU B8 S4096 C320: 16 us (2.7 TB/s), backward 33 us (1.9 TB/s); B2 S64 C1280
+// 6.2 us, a launch and an exchange. Bound by the arithmetic of the two passes (16 warps
+// an SM; the special-function and FMA pipes) and, with few slabs, by the latency of
+// copy, exchange and copy out, which follow one another. Two CTAs for each SM: one alone, with
+// slabs of twice the size, took 29 us for the first.
 #pragma once
 
 #include "groupnorm_kernels.cuh"

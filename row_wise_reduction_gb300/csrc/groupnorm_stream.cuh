@@ -10,6 +10,12 @@
 // chunks, in order. An apply item that comes too early waits (with a limit); it
 // waits for items before it in the sequence alone, and sums never wait, so the
 // waits end whatever CTAs run at the same time.
+//
+// bf16 SiLU B32 S4096 C320: 48 us (3.4 TB/s of what must be moved once), backward 78 us
+// (3.2 TB/s); B1 S262144 C128: 51 us. The reads of the sums run at 5 TB/s beside the
+// write-back of what the last call wrote; the second pass takes as long from L2
+// as the first from memory; one sample alone has nothing to do while its sums are
+// joined (7 us).
 #pragma once
 
 #include "async_ring.cuh"

@@ -12,6 +12,10 @@
 // shared memory and leave one partial row per cluster; a second kernel adds
 // those in a fixed order and forms the loss. A problem that one cluster takes
 // finishes in the first kernel.
+//
+// fp32 131072 x 256, 8 choices: 31 us (4.6 TB/s with the choices), of which the second
+// kernel's launch and latency are about 4; its gradient 47 us (5.7 TB/s). 64 x 8: 4.1
+// and 3.4 us, a launch's latency.
 #include <algorithm>
 #include <type_traits>
 
