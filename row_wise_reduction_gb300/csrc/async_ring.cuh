@@ -18,6 +18,19 @@ __device__ __forceinline__ void copy_async(void* smem, const void* global) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(global), "n"(BYTES) : "memory");
 }
 
+// 16 bytes under an L2 policy
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void copy_async16(void* smem, const void* global, uint64_t policy) {
+    const unsigned to = unsigned(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2;" ::"r"(to), "l"(global),
+                 "l"(policy)
+                 : "memory");
+}
+
 template <int D, int N, int THREADS>
 struct Ring {
     uint4* at;  // [D][N][THREADS], this thread's

@@ -11,8 +11,8 @@
 // waits for items before it in the sequence alone, and sums never wait, so the
 // waits end whatever CTAs run at the same time.
 //
-// bf16 SiLU B32 S4096 C320: 48 us (3.4 TB/s of what must be moved once), backward 78 us
-// (3.2 TB/s); B1 S262144 C128: 51 us. The reads of the sums run at 5 TB/s beside the
+// bf16 SiLU B32 S4096 C320: 47 us (3.6 TB/s of what must be moved once), backward 77 us
+// (3.3 TB/s); B1 S262144 C128: 50 us. The reads of the sums run at 5 TB/s beside the
 // write-back of what the last call wrote; the second pass takes as long from L2
 // as the first from memory; one sample alone has nothing to do while its sums are
 // joined (7 us).
@@ -24,21 +24,24 @@
 
 namespace rowops {
 
-// A thread's n positions, `step` elements apart, of N tensors: run(f) calls f(words)
+// A thread's n positions, `step` elements apart, of N tensors (LAST: for the last time, so
+// that they give up their places in L2 first: 2% on every size measured): run(f) calls f(words)
 // for each in order. Vectors come through a ring of copies, D positions on their
 // way, the first of them asked for by the constructor: what else a pass needs first
 // (its parameters, a wait) goes between. One or two elements: U positions at a time.
-template <typename T, int VEC, int D, int N>
+template <typename T, int VEC, int D, int N, bool LAST>
 struct Walk {
     using V = Vec<T, VEC>;
     const T* p[N];
     int64_t step;
     int n;
     uint4* at;
+    uint64_t policy = 0;
     __device__ __forceinline__ Walk(const T* const (&from)[N], int64_t step_, int n_, uint4* slots)
         : step(step_), n(n_), at(slots + threadIdx.x) {
 #pragma unroll
         for (int k = 0; k < N; ++k) p[k] = from[k];
+        if constexpr (LAST && V::kWhole) policy = evict_first_policy();
         if constexpr (V::kWhole)
 #pragma unroll
             for (int d = 0; d < D - 1; ++d) ask(d, d);
@@ -47,7 +50,8 @@ struct Walk {
         if (i < n)
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                copy_async<16>(at + (d * N + k) * kGnBlock, p[k]);
+                if constexpr (LAST) copy_async16(at + (d * N + k) * kGnBlock, p[k], policy);
+                else copy_async<16>(at + (d * N + k) * kGnBlock, p[k]);
                 p[k] += step;
             }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             if (k.n > 0 && c < a.C) {
                 const T* const from[1] = {x + k.first + c};
                 bool first = true;
-                Walk<T, VEC, D, 1> walk(from, k.step, k.n, slots);
+                Walk<T, VEC, D, 1, false> walk(from, k.step, k.n, slots);
                 walk.run([&](const typename V::Word (&wd)[1]) {
                     float2 v[P];
                     V::get(wd[0], v);
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             const bool mine = k.n > 0 && c < a.C;
             const int64_t at = mine ? k.first + c : 0;
             const T* const from[1] = {x + at};
-            Walk<T, VEC, D, 1> walk(from, k.step, mine ? k.n : 0, slots);
+            Walk<T, VEC, D, 1, true> walk(from, k.step, mine ? k.n : 0, slots);
             float2 mean[P], mul[P], add[P], rstd[P];
             load_affine<T, VEC>(w, mine ? c : 0, 1.f, mul);
             load_affine<T, VEC>(b, mine ? c : 0, 0.f, add);
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
             for (int j = 0; j < P; ++j) sa[j] = sq[j] = slope.rstd[j] = f2(0.f);
             if (k.n > 0 && c < a.C) {
                 const T* const from[2] = {x + k.first + c, dy + k.first + c};
-                Walk<T, VEC, D, 2> walk(from, k.step, k.n, slots);
+                Walk<T, VEC, D, 2, false> walk(from, k.step, k.n, slots);
                 slope.load(w, b, stats + int64_t(it.sample) * a.G, c, c, a);
                 walk.run([&](const typename V::Word (&wd)[2]) { slope.add(wd[0], wd[1], sa, sq); });
             }
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
             const bool mine = k.n > 0 && c < a.C;
             const int64_t at = mine ? k.first + c : 0;
             const T* const from[2] = {x + at, dy + at};
-            Walk<T, VEC, D, 2> walk(from, k.step, mine ? k.n : 0, slots);
+            Walk<T, VEC, D, 2, true> walk(from, k.step, mine ? k.n : 0, slots);
             GnSlope<T, VEC, ACT> slope;
             slope.load(w, b, stats + int64_t(it.sample) * a.G, mine ? c : 0, mine ? c : 0, a);
             if (tile == 0 && !ready()) return walk.drop();

@@ -345,10 +345,10 @@ constexpr int kGnClusters[2][5] = {{152, 76, 36, 15, 7}, {304, 152, 74, 36, 14}}
 // microseconds; `tensors`: 1 forward, 2 backward (read and held). Returns the
 // modelled time, or a negative number where no split holds the slab. The model:
 // the traffic at the card's copy rate, or the turns of the clusters, each with the
-// arithmetic of an SM's CTAs (0.28 us for a vector of every thread forward, 0.55
-// backward, two thirds of it in fp32, less for single elements) and an exchange; and
+// arithmetic of an SM's CTAs (0.28 us for a vector of every thread forward, 0.57
+// backward, 0.7 of it in fp32, less for single elements) and an exchange; and
 // a launch. Modelled and measured in us: B8 S4096 C320 bf16 SiLU 18 and 16, its
-// backward pass 32 and 33, with B32 57 and 58, 110 and 105; B3 S1155 C330 fp32
+// backward pass 33 and 33, with B32 57 and 58, 114 and 105; B3 S1155 C330 fp32
 // backward, odd ld, 16 and 15.
 inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFused* best) {
     double least = -1.0;
@@ -396,7 +396,7 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
             const double slabs = double(a.B) * blocks, held = std::min(slabs, double(kGnClusters[per_sm - 1][cl]));
             const double turns = std::ceil(slabs / held), slots = std::ceil(double(rows) / f.ty);
             const double ctas_sm = std::ceil(held * cluster / kGnSms);
-            const double slot = (tensors == 1 ? 0.28 : ctas_sm > 1 ? 0.55 : 0.75) * (vec <= 2 ? 0.4 : es == 4 ? 0.67 : 1.0);
+            const double slot = (tensors == 1 ? 0.28 : ctas_sm > 1 ? 0.57 : 0.75) * (vec <= 2 ? 0.4 : es == 4 ? 0.7 : 1.0);
             const double exchange = cluster > 1 ? 2.0 : 1.0;
             double t = std::max(all / 6.8e6, turns * (ctas_sm * slots * slot + exchange / ctas_sm)) + 4.5 + exchange / 2;
             if (least < 0 || t < least) {
@@ -410,10 +410,10 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
 
 // The streaming form's modelled time: launches and the ends of the sums, and its
 // traffic at what it measured. Modelled and measured in us, the same sizes: 26 and 25,
-// 32 and 33, with B32 52 and 48, 79 and 78; odd ld 19 and 21.
+// 32 and 32, with B32 52 and 47, 79 and 77; odd ld 19 and 21.
 inline double gn_stream_time(const GnArgs& a, int es, int tensors) {
     const double in = double(a.B) * a.S * a.C * es * tensors;
-    return (tensors == 1 ? 17.0 : 16.0) + (in + in / tensors) / (tensors == 1 ? 4.8e6 : 4.0e6);
+    return (tensors == 1 ? 17.0 : 16.0) + (in + in / tensors) / (tensors == 1 ? 4.8e6 : es == 4 ? 4.4e6 : 4.0e6);
 }
 
 using GnForwardLaunch = cudaError_t (*)(const void* x, void* y, const void* w, const void* b, float* stats, void* ws,
