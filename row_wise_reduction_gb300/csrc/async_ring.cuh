@@ -31,12 +31,22 @@ __device__ __forceinline__ void copy_async16(void* smem, const void* global, uin
                  : "memory");
 }
 
+// the first `bytes` of 16 (no others are read), zeros behind them
+__device__ __forceinline__ void copy_async_part(void* smem, const void* global, unsigned bytes) {
+    const unsigned to = unsigned(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(to), "l"(global), "r"(bytes)
+                 : "memory");
+}
+
 template <int D, int N, int THREADS>
 struct Ring {
     uint4* at;  // [D][N][THREADS], this thread's
     int in = 0, out = 0;
     __device__ __forceinline__ explicit Ring(uint4* smem) : at(smem + threadIdx.x) {}
     __device__ __forceinline__ void ask(int n, const void* p) { copy_async<16>(at + (in * N + n) * THREADS, p); }
+    __device__ __forceinline__ void ask_part(int n, const void* p, unsigned bytes) {
+        copy_async_part(at + (in * N + n) * THREADS, p, bytes);
+    }
     // the step's copies are all asked for (or there were none)
     __device__ __forceinline__ void asked() {
         asm volatile("cp.async.commit_group;" ::: "memory");

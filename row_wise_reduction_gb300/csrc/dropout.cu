@@ -279,8 +279,9 @@ __global__ void __launch_bounds__(kWarps * 32)
 // keep their columns. Lane l holds the aligned 16-byte vector v = 31 segment + l,
 // columns head + V v .. of its rows, and makes the block of random bits that they
 // begin in; where they run into the next block its bits come from lane l + 1, whose
-// block that is (lane 31 has only that to do). The elements before the first and
-// after the last whole vector go one by one. Two rows of column sums for each
+// block that is (lane 31 has only that to do). What is left behind the last whole
+// vector comes as a part of one; the elements before the first go one by one, a row
+// ahead. Two rows of column sums for each
 // chunk, one from even segments and one from odd: with their columns shifted from
 // warp to warp, neighbours overlap.
 constexpr int kSegVecs = 31;
@@ -305,11 +306,12 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     const uint32_t block = uint32_t(col >> 3);
     const int at = int(col & 7);
     const bool whole = lane < kSegVecs && v < geo.nvec;
-    // single elements: the tail behind the last vector (its lane), the head (the
-    // first segment's lanes, one each)
     const int tail = lane < kSegVecs && v == geo.nvec ? geo.tail : 0;
-    const bool head = blockIdx.x == 0 && lane < geo.head;
-    float bias[V], acc[V] = {}, head_bias = 0.f, head_acc = 0.f;
+    const bool held = whole || tail;
+    const unsigned bytes = whole ? 16u : unsigned(tail * E::kBytes);
+    const bool head = blockIdx.x == 0 && lane < geo.head;  // the first segment's lanes, one element each
+    float bias[V], head_bias = 0.f, head_acc = 0.f;
+    float2 acc[V / 2] = {};
 #pragma unroll
     for (int e = 0; e < V; ++e) bias[e] = b && (whole || e < tail) ? E::load(b + col + e) : 0.f;
     if (b && head) head_bias = E::load(b + lane);
@@ -319,25 +321,26 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     T* py = y + at0;
     int64_t ahead = r0;
     auto ask = [&] {
-        if (ahead < r1 && whole) {
-            ring.ask(0, px);
-            if constexpr (RES) ring.ask(1, pr);
+        if (ahead < r1 && held) {
+            ring.ask_part(0, px, bytes);
+            if constexpr (RES) ring.ask_part(1, pr, bytes);
         }
         ring.asked();
         ahead += kWarps;
         px += step;
         if constexpr (RES) pr += step;
     };
-    // column i of the row at p: kept, with its bias, and with the residual
-    auto single = [&](const T* p, const T* q, T* o, bool kept, float bias_, float& sum) {
-        float v = kept ? (E::load(p) + bias_) * a.scale : 0.f;
-        if constexpr (SUM) sum += v;
-        if constexpr (RES) v += E::load(q);
-        E::store(o, v);
+    float head_x = 0.f, head_r = 0.f;
+    auto ask_head = [&](int64_t row) {
+        if (head && row < r1) {
+            head_x = E::load(x + row * a.ld + lane);
+            if constexpr (RES) head_r = E::load(r + row * a.ld + lane);
+        }
     };
     const bool any_head = blockIdx.x == 0 && geo.head > 0;  // the warp's
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) ask();
+    ask_head(r0);
 #pragma unroll 1
     for (int64_t row = r0; row < r1; row += kWarps, py += step) {
         ask();
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
             keep = (own | __shfl_down_sync(0xffffffffu, own, 1) << 8) >> at;
         }
         ring.wait();
-        if (whole) {
+        if (held) {
             float o[V];
             E::unpack(ring.get(0), o);
 #pragma unroll
@@ -358,10 +361,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
                 if constexpr (RNG) t = make_float2(keep >> e & 1u ? t.x : 0.f, keep >> (e + 1) & 1u ? t.y : 0.f);
                 o[e] = t.x;
                 o[e + 1] = t.y;
-                if constexpr (SUM) {
-                    acc[e] += t.x;
-                    acc[e + 1] += t.y;
-                }
+                if constexpr (SUM) acc[e / 2] = f2_add(acc[e / 2], t);
             }
             if constexpr (RES) {
                 float q[V];
@@ -369,40 +369,52 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
 #pragma unroll
                 for (int e = 0; e < V; ++e) o[e] += q[e];
             }
-            st_stream16(py, E::pack(o));
-        } else if (tail) {
-            const int64_t i = row * a.ld + col;
+            if (whole) {
+                st_stream16(py, E::pack(o));
+            } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (e < tail) single(x + i + e, r + i + e, y + i + e, keep >> e & 1u, bias[e], acc[e]);
+                for (int e = 0; e < V; ++e)
+                    if (e < tail) E::store(py + e, o[e]);
+            }
         }
         if (any_head) {
             if constexpr (RNG) own = __shfl_sync(0xffffffffu, own, 0);  // the head's block
-            const int64_t i = row * a.ld + lane;
-            if (head) single(x + i, r + i, y + i, own >> lane & 1u, head_bias, head_acc);
+            if (head) {
+                float h = own >> lane & 1u ? (head_x + head_bias) * a.scale : 0.f;
+                if constexpr (SUM) head_acc += h;
+                if constexpr (RES) h += head_r;
+                E::store(y + row * a.ld + lane, h);
+            }
+            ask_head(row + kWarps);
         }
         ring.done();
     }
 
     if constexpr (SUM) {
-        // in order of the warps; columns from SPAN segment on
-        __shared__ float red[SPAN + V];
-        for (int i = threadIdx.x; i < SPAN + V; i += kWarps * 32) red[i] = 0.f;
-        for (int w = 0; w < kWarps; ++w) {
-            __syncthreads();
-            if (warp != w || r0 >= r1) continue;
-            const int at0 = geo.head + V * lane;  // within the segment's columns
+        // each warp's, columns from SPAN segment on; then over the warps in order
+        __shared__ float reds[kWarps][SPAN + V];
+        float* red = reds[warp];
+        for (int i = lane; i < SPAN + V; i += 32) red[i] = 0.f;
+        __syncwarp();
+        if (r0 < r1) {
+            float* at0 = red + geo.head + V * lane;
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (whole || e < tail) red[at0 + e] += acc[e];
-            if (head) red[lane] += head_acc;
+                if (whole || e < tail) at0[e] = e & 1 ? acc[e / 2].y : acc[e / 2].x;
+            if (head) red[lane] = head_acc;
         }
         __syncthreads();
+        auto sum = [&](int i) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += reds[w][i];
+            return s;
+        };
         // the segment's part of its row, up to where the next one of that row begins
         float* out = part + (int64_t(blockIdx.y) * 2 + (blockIdx.x & 1)) * a.N;
         const int64_t c0 = int64_t(blockIdx.x) * SPAN;
         for (int i = threadIdx.x; i < 2 * SPAN; i += kWarps * 32)
-            if (c0 + i < a.N) out[c0 + i] = i < SPAN + V ? red[i] : 0.f;
+            if (c0 + i < a.N) out[c0 + i] = i < SPAN + V ? sum(i) : 0.f;
         // odd segments' row has nothing before the first of them
         if (blockIdx.x == 0)
             for (int i = threadIdx.x; i < SPAN && i < a.N; i += kWarps * 32)
