@@ -24,8 +24,8 @@
 // flight take no registers. With four rows in flight in registers the kernel held
 // half as many warps and bf16 16384 x 8192 with column sums took 124.8 us. Now 88 us
 // (6.1 TB/s); forward, with bias and residual, 120 us (6.7 TB/s); bf16 4001 x 4097 with
-// column sums, rows at odd offsets, 28 us: bound by the decisions' bit operations
-// (without dropping, p = 0 and no column sums, 13 us).
+// column sums, rows at odd offsets, 23 us: bound by the generator's and the decisions'
+// instructions (without dropping, p = 0 and no column sums, 13 us).
 #include <algorithm>
 
 #include "async_ring.cuh"
@@ -457,8 +457,8 @@ struct DropCall {
 // leaves partial rows, and fewer are better: of the vector form two CTAs an SM, whose
 // rings keep the memory busy (bf16 16384 x 8192 88 us, with four 99, in two waves of
 // those 92; 4096 x 1024 8 us, 9.6 and 11); of the others, which have more to compute, as
-// many as fit, and twice as many where a chunk still has 32 rows (bf16 4001 x 4097 28
-// us, one wave 30; 1000 x 1025 10 us and 9). Whole steps of the CTA unless that leaves
+// many as fit, and twice as many where a chunk still has 32 rows (bf16 4001 x 4097 23
+// us, one wave 26, four 26; 1000 x 1025 8.2 us and 7.5). Whole steps of the CTA unless that leaves
 // CTAs idle.
 template <typename T>
 cudaError_t launch(DropKernel<T> kern, size_t smem, int64_t gx, int64_t step, int64_t unit, int partials,
