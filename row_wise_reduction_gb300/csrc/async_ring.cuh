@@ -1,5 +1,5 @@
-// A thread's ring of data on its way into shared memory: D steps of N 16-byte words,
-// in slots of its own, so no barrier stands between a copy and its use and what is
+// A thread's ring of data on its way into shared memory: D steps of N words (of 16
+// bytes, or 4), in slots of its own, so no barrier stands between a copy and its use and what is
 // in flight takes no registers.
 #pragma once
 
@@ -38,12 +38,14 @@ __device__ __forceinline__ void copy_async_part(void* smem, const void* global, 
                  : "memory");
 }
 
-template <int D, int N, int THREADS>
+template <int D, int N, int THREADS, typename Word = uint4>
 struct Ring {
-    uint4* at;  // [D][N][THREADS], this thread's
+    Word* at;  // [D][N][THREADS], this thread's
     int in = 0, out = 0;
-    __device__ __forceinline__ explicit Ring(uint4* smem) : at(smem + threadIdx.x) {}
-    __device__ __forceinline__ void ask(int n, const void* p) { copy_async<16>(at + (in * N + n) * THREADS, p); }
+    __device__ __forceinline__ explicit Ring(Word* smem) : at(smem + threadIdx.x) {}
+    __device__ __forceinline__ void ask(int n, const void* p) {
+        copy_async<sizeof(Word)>(at + (in * N + n) * THREADS, p);
+    }
     __device__ __forceinline__ void ask_part(int n, const void* p, unsigned bytes) {
         copy_async_part(at + (in * N + n) * THREADS, p, bytes);
     }
@@ -54,7 +56,7 @@ struct Ring {
     }
     // the oldest step's copies are here, D - 1 later ones may not be
     __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory"); }
-    __device__ __forceinline__ uint4 get(int n) const { return at[(out * N + n) * THREADS]; }
+    __device__ __forceinline__ Word get(int n) const { return at[(out * N + n) * THREADS]; }
     __device__ __forceinline__ void done() { out = out + 1 == D ? 0 : out + 1; }
 };
 

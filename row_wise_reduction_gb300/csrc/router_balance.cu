@@ -15,7 +15,8 @@
 //
 // fp32 131072 x 256, 8 choices: 31 us (4.6 TB/s with the choices), of which the second
 // kernel's launch and latency are about 4; its gradient 47 us (5.7 TB/s). 64 x 8: 4.1
-// and 3.4 us, a launch's latency.
+// and 3.4 us, a launch's latency. bf16 131072 x 60, rows that are no whole vectors: 16
+// and 13 us by pairs, 21 and 16 by single elements.
 #include <algorithm>
 #include <type_traits>
 
@@ -34,12 +35,15 @@ constexpr int kBlock = 256;
 constexpr int kCluster = 8;
 
 // A lane's share of a row: NV vectors of VEC elements, vector j holding columns
-// VEC (TL j + tl) .. FULL: every lane's vectors lie within the row. Values are kept
+// VEC (TL j + tl) .. (16 bytes, a pair of bf16, or one element). FULL: every lane's
+// vectors lie within the row. Values are kept
 // as pairs for the packed arithmetic (a lone element with a -inf).
 template <typename T, int VEC, int NV, bool FULL>
 struct Row {
     using E = Elem<T>;
-    using Word = std::conditional_t<VEC == 1, T, uint4>;
+    static constexpr bool kWhole = VEC * sizeof(T) == 16;
+    static_assert(kWhole || VEC == 1 || VEC * sizeof(T) == 4, "");
+    using Word = std::conditional_t<kWhole, uint4, std::conditional_t<VEC == 1, T, uint32_t>>;
     static constexpr int N = NV * VEC, P = N == 1 ? 1 : N / 2;
     Word w[NV];
     __device__ __forceinline__ static int column(int j, int tl, int TL) { return VEC * (TL * j + tl); }
@@ -49,8 +53,14 @@ struct Row {
         if constexpr (N == 1) f[1] = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if constexpr (VEC == 1) f[j] = E::load(&w[j]);
-            else E::unpack(w[j], f + j * VEC);
+            if constexpr (kWhole) {
+                E::unpack(w[j], f + j * VEC);
+            } else if constexpr (VEC == 1) {
+                f[j] = E::load(&w[j]);
+            } else {
+                f[2 * j] = __uint_as_float(w[j] << 16);
+                f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
             if constexpr (!FULL) {
                 const bool in = column(j, tl, TL) < E_;
 #pragma unroll
@@ -67,6 +77,8 @@ struct Row {
             if (!FULL && c >= E_) continue;
             if constexpr (VEC == 1) {
                 E::store(row + c, j & 1 ? v[j / 2].y : v[j / 2].x);
+            } else if constexpr (VEC == 2) {
+                *reinterpret_cast<uint32_t*>(row + c) = pack_bf16x2(v[j].x, v[j].y);
             } else {
                 float f[VEC];
 #pragma unroll
@@ -87,15 +99,16 @@ struct Row {
 };
 
 // A warp's rows one after the other, `step` apart, kDepth of them on their way: through
-// a ring of copies (vectors), or one row ahead in registers (single elements). With
-// one row ahead in either form the kernels waited for memory two thirds of the time.
+// a ring of copies, or (single bf16) one row ahead in registers. With one row ahead in
+// either form the kernels waited for memory two thirds of the time.
 constexpr int kDepth = 4;
 
 template <typename T, typename I, int VEC, int NV, bool FULL>
 struct Rows {
     using R = Row<T, VEC, NV, FULL>;
-    static constexpr bool kRing = VEC > 1;
-    Ring<kDepth, NV, kBlock> ring;
+    using Word = typename R::Word;
+    static constexpr bool kRing = sizeof(Word) >= 4;
+    Ring<kDepth, NV, kBlock, Word> ring;
     I* choices;  // [kDepth][threads], this thread's
     int64_t rows, step, ahead, ld;
     const T* from;
@@ -106,8 +119,8 @@ struct Rows {
     // choice: NULL where the choices are not wanted
     __device__ __forceinline__ Rows(void* smem, const T* logits, const I* experts, int64_t first, int64_t step_,
                                     int64_t rows_, int E_, int K_, int64_t ld_, int tl_, int TL_)
-        : ring(static_cast<uint4*>(smem)),
-          choices(reinterpret_cast<I*>(static_cast<uint4*>(smem) + kDepth * NV * kBlock) + threadIdx.x),
+        : ring(static_cast<Word*>(smem)),
+          choices(reinterpret_cast<I*>(static_cast<Word*>(smem) + kDepth * NV * kBlock) + threadIdx.x),
           rows(rows_), step(step_), ahead(first), ld(ld_), from(logits + first * ld_),
           choice(experts ? experts + first * K_ : nullptr), E(E_), K(K_), tl(tl_), TL(TL_) {
 #pragma unroll
@@ -151,9 +164,10 @@ struct Rows {
         }
     }
 };
-template <typename I, int VEC, int NV>
+template <typename T, typename I, int VEC, int NV>
 constexpr size_t rows_smem() {
-    return VEC == 1 ? 0 : size_t(kDepth) * kBlock * (NV * 16 + sizeof(I));
+    constexpr size_t word = VEC * sizeof(T);
+    return word < 4 ? 0 : size_t(kDepth) * kBlock * (NV * word + sizeof(I));
 }
 
 __device__ __forceinline__ float team_max(float v, int TL) {
@@ -221,7 +235,7 @@ __global__ void __launch_bounds__(kBlock, NV * VEC <= 16 ? 3 : 1)
     using R = Row<T, VEC, NV, FULL>;
     extern __shared__ __align__(16) unsigned char sm[];  // the rows on their way, then:
     __shared__ float red[kBlock / 32];
-    float* P = reinterpret_cast<float*>(sm + rows_smem<I, VEC, NV>());  // [kBlock / 32][E], row 0 the CTA's
+    float* P = reinterpret_cast<float*>(sm + rows_smem<T, I, VEC, NV>());  // [kBlock / 32][E], row 0 the CTA's
     int* cnt = reinterpret_cast<int*>(P + kBlock / 32 * E);  // [E + 1]
     float* Ps = reinterpret_cast<float*>(cnt + E + 1);      // [E] and [E + 1]: the cluster's, in rank 0
     int* cs = reinterpret_cast<int*>(Ps + E);
@@ -411,12 +425,11 @@ struct Shape {
     int nv, tl_log2;  // vectors of a lane (a power of two), lanes of a team
 };
 
-// About 16 (vectors) or 4 (single elements) elements a lane: the wider the
-// lane's share, the fewer shuffles a row takes; a team's vector access covers at
-// least a 32-byte sector.
-Shape choose(int E, int vec) {
-    const int nvec = (E + vec - 1) / vec, per = vec == 1 ? 4 : 16 / vec;
-    int l = vec == 1 ? 0 : 1;
+// About 16 elements a lane, in vectors, or 4 words: the wider the lane's share, the
+// fewer shuffles a row takes; a team's access covers a 32-byte sector.
+Shape choose(int E, int vec, bool whole) {
+    const int nvec = (E + vec - 1) / vec, per = whole ? 16 / vec : 4;
+    int l = whole ? 1 : 0;
     while (l < 5 && (per << l) < nvec) ++l;
     int nv = 1;
     while ((nv << l) < nvec) nv <<= 1;
@@ -430,7 +443,7 @@ cudaError_t launch_fwd(const void* logits, const void* experts, const uint8_t* m
                        int64_t ld, int tl_log2, float coef, float* loss, int64_t* counts, void* ws,
                        const LaunchCfg& cfg) {
     auto kern = balance_kernel<T, I, VEC, NV, FULL>;
-    const size_t smem = balance_smem(E) + rows_smem<I, VEC, NV>();
+    const size_t smem = balance_smem(E) + rows_smem<T, I, VEC, NV>();
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, cfg);
     if (e != cudaSuccess) return e;
     const int64_t rows_per_cta = int64_t(kBlock / 32) * (32 >> tl_log2);
@@ -483,7 +496,7 @@ cudaError_t launch_bwd(const void* logits, const int64_t* counts, const float* d
                        const LaunchCfg& cfg) {
     auto kern = balance_backward_kernel<T, VEC, NV, FULL>;
     const int64_t rows_per_cta = int64_t(kBlock / 32) * (32 >> tl_log2);
-    const size_t smem = rows_smem<int32_t, VEC, NV>();
+    const size_t smem = rows_smem<T, int32_t, VEC, NV>();
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, cfg);
     if (e != cudaSuccess) return e;
     const int grid = grid_for(reinterpret_cast<const void*>(kern), kBlock, smem,
@@ -515,23 +528,27 @@ cudaError_t by_nv(int nv, F f) {
     return cudaErrorInvalidValue;
 }
 
-// f(VEC, NV, FULL) of a shape; full rows have instantiations of their own with vectors
+// f(VEC, NV, FULL) of a shape; full rows have instantiations of their own with vectors.
+// vec: elements of the widest access; a pair of fp32 goes as two.
 template <typename T, typename F>
-cudaError_t by_shape(int E, bool vec, F f, Shape* shape) {
-    constexpr int V = Elem<T>::kVec;
-    const Shape s = choose(E, vec ? V : 1);
+cudaError_t by_shape(int E, int vec, F f, Shape* shape) {
+    constexpr int V = Elem<T>::kVec, PAIR = sizeof(T) == 2 ? 2 : 1;
+    vec = vec == V ? V : (vec >= PAIR ? PAIR : 1);
+    const Shape s = choose(E, vec, vec == V);
     *shape = s;
     using Yes = std::true_type;
     using No = std::false_type;
-    if (!vec) return by_nv<T, 1>(s.nv, [&](auto nv) { return f(std::integral_constant<int, 1>(), nv, No()); });
     using Vec = std::integral_constant<int, V>;
+    if (vec == 1) return by_nv<T, 1>(s.nv, [&](auto nv) { return f(std::integral_constant<int, 1>(), nv, No()); });
+    if (vec == PAIR)
+        return by_nv<T, PAIR>(s.nv, [&](auto nv) { return f(std::integral_constant<int, PAIR>(), nv, No()); });
     if ((V * s.nv) << s.tl_log2 == E) return by_nv<T, V>(s.nv, [&](auto nv) { return f(Vec(), nv, Yes()); });
     return by_nv<T, V>(s.nv, [&](auto nv) { return f(Vec(), nv, No()); });
 }
 
 template <typename T>
 cudaError_t balance(const void* logits, const void* experts, bool wide, const uint8_t* mask, int64_t rows, int E,
-                    int K, int64_t ld, float coef, float* loss, int64_t* counts, void* ws, bool vec,
+                    int K, int64_t ld, float coef, float* loss, int64_t* counts, void* ws, int vec,
                     const LaunchCfg& cfg) {
     Shape s;
     return by_shape<T>(
@@ -549,7 +566,7 @@ cudaError_t balance(const void* logits, const void* experts, bool wide, const ui
 
 template <typename T>
 cudaError_t balance_backward(const void* logits, const int64_t* counts, const float* dloss, const uint8_t* mask,
-                             void* dlogits, int64_t rows, int E, int K, int64_t ld, float coef, bool vec,
+                             void* dlogits, int64_t rows, int E, int K, int64_t ld, float coef, int vec,
                              const LaunchCfg& cfg) {
     Shape s;
     return by_shape<T>(

@@ -1377,7 +1377,7 @@ rowops_status_t rowops_router_balance_loss(const void* logits, const void* exper
     const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
-    const bool vec = vector_rows(tn, E, ld, es, {logits});
+    const int vec = row_access(tn, E, ld, es, {logits});
     const BalanceLaunch fn = dtype == ROWOPS_F32 ? balance_f32() : balance_bf16();
     return finish(fn(logits, experts, index_bytes == 8, mask, T, int(E), int(K), ld, coef, loss, counts, workspace,
                      vec, cfg));
@@ -1399,7 +1399,7 @@ rowops_status_t rowops_router_balance_loss_backward(const void* logits, const in
     const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
-    const bool vec = vector_rows(tn, E, ld, es, {logits, dlogits});
+    const int vec = row_access(tn, E, ld, es, {logits, dlogits});
     const BalanceBackwardLaunch fn = dtype == ROWOPS_F32 ? balance_backward_f32() : balance_backward_bf16();
     return finish(fn(logits, counts, dloss, mask, dlogits, T, int(E), int(K), ld, coef, vec, cfg));
 }

@@ -250,14 +250,15 @@ DropoutLaunch dropout_bf16();
 constexpr int kBalanceMaxExperts = 1024;
 constexpr int kBalanceMaxClusters = 128;
 constexpr int64_t kBalanceOneCluster = int64_t(512) << 10;
+// vec: elements of the widest access the rows allow (16 bytes of them, 2 or 1)
 using BalanceLaunch = cudaError_t (*)(const void* logits, const void* experts, bool wide, const uint8_t* mask,
                                       int64_t rows, int E, int K, int64_t ld, float coef, float* loss,
-                                      int64_t* counts, void* ws, bool vec, const LaunchCfg& cfg);
+                                      int64_t* counts, void* ws, int vec, const LaunchCfg& cfg);
 BalanceLaunch balance_f32();
 BalanceLaunch balance_bf16();
 using BalanceBackwardLaunch = cudaError_t (*)(const void* logits, const int64_t* counts, const float* dloss,
                                               const uint8_t* mask, void* dlogits, int64_t rows, int E, int K,
-                                              int64_t ld, float coef, bool vec, const LaunchCfg& cfg);
+                                              int64_t ld, float coef, int vec, const LaunchCfg& cfg);
 BalanceBackwardLaunch balance_backward_f32();
 BalanceBackwardLaunch balance_backward_bf16();
 

@@ -75,6 +75,14 @@ def test_strides_and_alignment(dtype, pad, offset):
     check(300, 20, 4, dtype, pad=pad, offset=offset)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,pad,offset", [(2, 0, 0), (6, 2, 2), (62, 0, 0), (92, 4, 0), (510, 0, 2), (1022, 0, 0),
+                                          (1021, 0, 1), (33, 2, 0)])
+def test_rows_of_short_words(dtype, E, pad, offset):
+    """Rows that are no whole vectors, several of them a warp and ten a thread."""
+    check(5003, E, min(E, 3), dtype, pad=pad, offset=offset)
+
+
 @pytest.mark.parametrize("kind", [torch.bool, torch.uint8])
 @pytest.mark.parametrize("T", [50, 9000])
 def test_padded_rows(kind, T):
