@@ -397,7 +397,7 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
             const double slabs = double(a.B) * blocks, held = std::min(slabs, double(kGnClusters[per_sm - 1][cl]));
             const double turns = std::ceil(slabs / held), slots = std::ceil(double(rows) / f.ty);
             const double ctas_sm = std::ceil(held * cluster / kGnSms);
-            const double slot = (tensors == 1 ? 0.28 : ctas_sm > 1 ? 0.57 : 0.75) * (vec <= 2 ? 0.4 : es == 4 ? 0.7 : 1.0);
+            const double slot = (tensors == 1 ? 0.28 : ctas_sm > 1 ? 0.57 : 0.75) * (vec == 1 ? 0.4 : vec == 2 ? 0.7 : es == 4 ? 0.7 : 1.0);
             const double exchange = cluster > 1 ? 2.0 : 1.0;
             double t = std::max(all / 6.8e6, turns * (ctas_sm * slots * slot + exchange / ctas_sm)) + 4.5 + exchange / 2;
             if (least < 0 || t < least) {
@@ -414,7 +414,8 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
 // 32 and 32, with B32 52 and 47, 79 and 77; odd ld 19 and 21.
 inline double gn_stream_time(const GnArgs& a, int es, int tensors) {
     const double in = double(a.B) * a.S * a.C * es * tensors;
-    return (tensors == 1 ? 17.0 : 16.0) + (in + in / tensors) / (tensors == 1 ? 4.8e6 : es == 4 ? 4.4e6 : 4.0e6);
+    if (tensors > 1) return 16.0 + 1.5 * in / (es == 4 ? 4.4e6 : 4.0e6);
+    return es == 4 ? 12.0 + 2.0 * in / 4.4e6 : 17.0 + 2.0 * in / 4.8e6;
 }
 
 using GnForwardLaunch = cudaError_t (*)(const void* x, void* y, const void* w, const void* b, float* stats, void* ws,
