@@ -441,8 +441,9 @@ rowops_status_t rowops_fused_residual_rmsnorm(const void* x, const void* residua
  * C is at most 8192 and B at most 2^30 (ROWOPS_ERR_UNSUPPORTED beyond), C a
  * multiple of G. B == 0 or S == 0 is a no-op. 16-byte aligned positions of whole
  * 16-byte vectors are the fastest, an even C and ld the next. A NaN or an infinity in a group makes that group of that
- * sample NaN. The variance is merged from centred partial sums, so a mean far
- * from zero costs it no precision.
+ * sample NaN. The variance is merged from centred partial sums, and their means
+ * as differences from a value of the group, so a mean far from zero (10^6 times the
+ * spread) costs it no precision; the output then carries the fp32 mean's rounding.
  */
 typedef enum rowops_act {
     ROWOPS_ACT_NONE = 0,

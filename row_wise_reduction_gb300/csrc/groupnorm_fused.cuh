@@ -84,6 +84,11 @@ struct GnTile {
         sample = n;
         at = first() * a.ld + int64_t(block) * f.W + tx * VEC;
     }
+    // element offset of a slab's first channel at its sample's first position
+    __device__ __forceinline__ int64_t origin(unsigned s) const {
+        const unsigned n = s / unsigned(f.blocks);
+        return int64_t(n) * a.S * a.ld + int64_t(s - n * f.blocks) * f.W;
+    }
     __device__ __forceinline__ int64_t first() const { return sample * a.S + int64_t(rank) * f.rows; }
     __device__ __forceinline__ bool more() const { return slabs - slab > stride; }
     __device__ __forceinline__ void next() {
@@ -248,12 +253,17 @@ __global__ void __launch_bounds__(kGnBlock, 2)
     float2* gots = gs + Gb;                                   // [2][cluster][Gb]: every CTA's mean, squares
     uint64_t* bars = reinterpret_cast<uint64_t*>(gots + 2 * f.cluster * Gb);  // [boxes]
     float* count = reinterpret_cast<float*>(bars + f.boxes);  // [ty] positions of the threads
+    float* refs = count + f.ty;                               // [Gb] what the means are kept less of
     const RowsMap* const maps[1] = {&mx};
     const T* const from[1] = {x};
     const typename V::Word* const tiles[1] = {tile};
     const float inv_rows = k.rows ? 1.f / float(k.rows) : 0.f;
     const int c = k.tx * VEC;
     int fail = 0;
+    // the slab's first refs, a slab ahead; not by the warp that asks for the boxes
+    const int own = k.t - 32;
+    const bool ahead = own >= 0 && own < Gb;
+    float ref = ahead ? Elem<T>::load(x + k.origin(k.slab) + own * a.L) : 0.f;
     for (; k.slab < k.slabs; k.next()) {
         gn_fetch<T, VEC, 1>(k, maps, from, tile, bars, stall_row);
         // two sets, as a CTA may be one exchange behind
@@ -264,7 +274,10 @@ __global__ void __launch_bounds__(kGnBlock, 2)
             load_affine<T, VEC>(w, cb, 1.f, mul);
             load_affine<T, VEC>(b, cb, 0.f, shift);
         }
-        if (k.turn == 0) __syncthreads();  // the barriers are set up
+        if (own >= 0)
+            for (int g = own; g < Gb; g += kGnBlock - 32)
+                refs[g] = g == own ? ref : Elem<T>::load(x + k.origin(k.slab) + g * a.L);
+        __syncthreads();  // they are there, and the barriers are set up
 
         Shifted<P> sums;
         sums.clear();
@@ -277,7 +290,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
             ++n;
         });
         if (k.active) {
-            sums.template leave<VEC>(n, pm + k.ty * f.W + c, pq + k.ty * f.W + c);
+            sums.template leave<VEC>(n, Groups<VEC>(c, a), refs, pm + k.ty * f.W + c, pq + k.ty * f.W + c);
             if (k.tx == 0) count[k.ty] = float(n);
         }
         const int before = fail;
@@ -322,7 +335,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
             const float2 s = lanes_sum(make_float2(m * d, fmaf(m * float(a.L) * d, d, v.y)), f.cluster);
             if (live && r == 0) {
                 const float2 u = joined(ref, s, float(a.L), a.inv_S);
-                gs[g] = make_float2(u.x, rsqrtf(u.y * a.inv_m + a.eps));
+                gs[g] = make_float2(refs[g] + u.x, rsqrtf(u.y * a.inv_m + a.eps));
                 if (stats_out && k.rank == 0) stats_out[k.sample * a.G + k.block * Gb + g] = gs[g];
             }
         });
@@ -336,6 +349,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
 #pragma unroll
             for (int j = 0; j < P; ++j) mul[j] = f2_mul(mul[j], rstd[j]);
         }
+        if (ahead && k.more()) ref = Elem<T>::load(x + k.origin(k.slab + k.stride) + own * a.L);
         T* py = y + k.at;
         gn_write<2>(k, maps, &my, tile, tiles, bars, fail,
                     [&](const typename V::Word (&wd)[1], int at, int r, bool whole) {

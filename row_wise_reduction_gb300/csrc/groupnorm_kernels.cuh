@@ -16,7 +16,11 @@
 // number of channels, straddling vectors. The variance is never a difference of
 // large sums: a thread sums x - k and (x - k)^2 about its own first value k, and
 // (count, mean, sum of squares about the mean) are merged from there on, each
-// merge taking the squares of the means' differences. Arithmetic on packed pairs.
+// merge taking the squares of the means' differences. All these means are kept less
+// one value of the group, its first channel at the sample's first position, which is
+// within sqrt(m) spreads of the mean as it is one of the m values: rounded as they are,
+// means of 10^6 spreads would lose the variance's fourth digit. The value is added
+// back where the results are made. Arithmetic on packed pairs.
 #pragma once
 
 #include <type_traits>
@@ -137,15 +141,17 @@ struct Shifted {
             s2[j] = f2_fma(d, d, s2[j]);
         }
     }
-    // the means and the squares about them of n positions, per channel
+    // the means, less their groups' refs, and the squares about them of n positions, per
+    // channel; k and ref are values, whose difference is exact where they are close
     template <int VEC>
-    __device__ __forceinline__ void leave(int n, float* mean, float* m2) const {
+    __device__ __forceinline__ void leave(int n, const Groups<VEC>& g, const float* refs, float* mean,
+                                          float* m2) const {
         const float inv = n ? 1.f / float(n) : 0.f;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const float s = e & 1 ? s1[e / 2].y : s1[e / 2].x, d = s * inv;
             const float q = fmaf(-s, d, e & 1 ? s2[e / 2].y : s2[e / 2].x);
-            mean[e] = d - (e & 1 ? k[e / 2].y : k[e / 2].x);
+            mean[e] = d - ((e & 1 ? k[e / 2].y : k[e / 2].x) + refs[g.g[e]]);
             m2[e] = q < 0.f ? 0.f : q;  // a NaN stays
         }
     }

@@ -178,16 +178,18 @@ __device__ __forceinline__ bool gn_last(unsigned* done, int sets, unsigned* word
 }
 
 // The CTA adds up n sets of sums of G groups, in order; set i is of `rows` positions,
-// S in all. Forward (MEANS: a group's mean and squares about it) the means enter less
-// the first set's; to[g] is the same of all sets or, `last`, mean and rstd. Backward the
+// S in all. Forward (MEANS: a group's mean, less its first value, and squares about it) the
+// means enter less the first set's; to[g] is the same of all sets or, `last`, mean and
+// rstd (x: the sample's first position). Backward the
 // plain sums, times -inv_m at the last. A function of its own, and a short one: it runs
 // once or twice in a CTA, and its time is that of fetching its code and waiting for
 // its loads.
-template <bool MEANS>
+template <bool MEANS, typename T>
 __device__ __noinline__ void gn_join(const float2* sets, int n, int64_t S, int64_t rows, bool last, float2* to,
-                                     float2* also, const GnArgs& a) {
+                                     float2* also, const T* x, const GnArgs& a) {
     by_teams(a.G, a.last_log2, [&](int g, int lane, bool live) {
         const float2* p = sets + g;
+        const float first = MEANS && last ? Elem<T>::load(x + g * a.L) : 0.f;
         const float ref = MEANS ? __ldcg(p).x : 0.f;
         const int step = 1 << a.last_log2;
         float2 s = f2(0.f);
@@ -214,7 +216,7 @@ __device__ __noinline__ void gn_join(const float2* sets, int n, int64_t S, int64
         if (!live || lane != 0) return;
         if constexpr (MEANS) {
             s = joined(ref, s, float(a.L), 1.f / float(S));
-            if (last) s.y = rsqrtf(s.y * a.inv_m + a.eps);
+            if (last) s = make_float2(first + s.x, rsqrtf(s.y * a.inv_m + a.eps));
         } else if (last) {
             s = make_float2(-s.x * a.inv_m, -s.y * a.inv_m);
         }
@@ -224,9 +226,9 @@ __device__ __noinline__ void gn_join(const float2* sets, int n, int64_t S, int64
 }
 
 // A sample's chunks' sums (or a bunch's, where chunks go in bunches) are in: joins them.
-template <bool MEANS>
-__device__ __forceinline__ bool gn_joined(const GnItem& it, const GnArgs& a, const GnStreamWs& ws, float2* stats,
-                                          unsigned* word) {
+template <bool MEANS, typename T>
+__device__ __forceinline__ bool gn_joined(const GnItem& it, const GnArgs& a, const GnStreamWs& ws, const T* x,
+                                          float2* stats, unsigned* word) {
     const float2* part = ws.part + int64_t(it.sample) * a.chunks * a.G;
     int n = a.chunks;
     int64_t rows = a.chunk_rows;
@@ -236,14 +238,14 @@ __device__ __forceinline__ bool gn_joined(const GnItem& it, const GnArgs& a, con
         float2* to = ws.bunch + int64_t(it.sample) * a.bunches * a.G;
         const int64_t at = first * rows, left = a.S - at;
         gn_join<MEANS>(part + int64_t(first) * a.G, size, left < a.bunch * rows ? left : a.bunch * rows, rows, false,
-                       to + k * a.G, nullptr, a);
+                       to + k * a.G, nullptr, x, a);
         part = to;
         n = a.bunches;
         rows *= a.bunch;
     }
     if (!gn_last(&ws.done[it.sample], n, word)) return false;
     gn_join<MEANS>(part, n, a.S, rows, true, ws.result + int64_t(it.sample) * a.G,
-                   stats ? stats + int64_t(it.sample) * a.G : nullptr, a);
+                   stats ? stats + int64_t(it.sample) * a.G : nullptr, x + it.sample * a.S * a.ld, a);
     __syncthreads();
     return true;
 }
@@ -327,27 +329,33 @@ __global__ void __launch_bounds__(kGnBlock, 3)
     float* pm = reinterpret_cast<float*>(slots) + walk_smem<T, VEC, D, 1>() / 4;  // [ty][W] the threads' means
     float* pq = pm + a.ty * W;                               // [ty][W] and squares
     float2* col = reinterpret_cast<float2*>(pq + a.ty * W);  // [C] the channels'
+    float* refs = reinterpret_cast<float*>(col + a.C);       // [G] what the means are kept less of
     auto sums = [&](const GnItem& it, const GnShare& k, auto walked) {
         const float inv_rows = 1.f / float(k.rows);
         for (int tile = 0; tile < a.tiles; ++tile) {
             const int c0 = tile * W, c = c0 + k.tx * VEC;
             Shifted<P> s;
             s.clear();
-            if (k.n > 0 && c < a.C) {
-                const T* const from[1] = {x + k.first + c};
-                bool first = true;
-                Walk<T, VEC, D, 1, false> walk(from, k.step, k.n, slots);
-                walk.run([&](const typename V::Word (&wd)[1]) {
-                    float2 v[P];
-                    V::get(wd[0], v);
-                    if (first) s.start(v);
-                    first = false;
-                    s.add(v);
-                });
+            const bool mine = k.n > 0 && c < a.C;
+            const T* const from[1] = {x + (mine ? k.first + c : 0)};
+            bool first = true;
+            Walk<T, VEC, D, 1, false> walk(from, k.step, mine ? k.n : 0, slots);
+            if (tile == 0) {  // while the first copies are on their way
+                const T* origin = x + it.sample * a.S * a.ld;
+                for (int g = threadIdx.x; g < a.G; g += kGnBlock) refs[g] = Elem<T>::load(origin + g * a.L);
+                __syncthreads();
             }
+            walk.run([&](const typename V::Word (&wd)[1]) {
+                float2 v[P];
+                V::get(wd[0], v);
+                if (first) s.start(v);
+                first = false;
+                s.add(v);
+            });
             if (tile == a.tiles - 1) walked();
             if (k.ty < a.ty)
-                s.template leave<VEC>(c < a.C ? k.n : 0, pm + k.ty * W + k.tx * VEC, pq + k.ty * W + k.tx * VEC);
+                s.template leave<VEC>(c < a.C ? k.n : 0, Groups<VEC>(c < a.C ? c : 0, a), refs,
+                                      pm + k.ty * W + k.tx * VEC, pq + k.ty * W + k.tx * VEC);
             __syncthreads();
             const int each = k.rows / a.ty, more = k.rows - each * a.ty;  // positions of row r: each + (r < more)
             by_teams(min(W, a.C - c0), a.parts_log2, [&](int ch, int lane, bool live) {
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(kGnBlock, 3)
             if (live && lane == 0) out[g] = joined(ref, s, m, a.inv_L);
         });
     };
-    auto join = [&](const GnItem& it, unsigned* word) { return gn_joined<true>(it, a, ws, stats_out, word); };
+    auto join = [&](const GnItem& it, unsigned* word) { return gn_joined<true>(it, a, ws, x, stats_out, word); };
     auto apply = [&](const GnItem& it, const GnShare& k, auto ready) {
         for (int tile = 0; tile < a.tiles; ++tile) {
             const int c = (tile * a.tx + k.tx) * VEC;
@@ -462,7 +470,7 @@ __global__ void __launch_bounds__(kGnBlock, 2)
             if (live && lane == 0) ws.part[slot * a.G + g] = s;
         });
     };
-    auto join = [&](const GnItem& it, unsigned* word) { return gn_joined<false>(it, a, ws, nullptr, word); };
+    auto join = [&](const GnItem& it, unsigned* word) { return gn_joined<false>(it, a, ws, x, nullptr, word); };
     auto apply = [&](const GnItem& it, const GnShare& k, auto ready) {
         for (int tile = 0; tile < a.tiles; ++tile) {
             const int c = (tile * a.tx + k.tx) * VEC;
@@ -570,7 +578,8 @@ cudaError_t gn_forward_stream(const void* x, void* y, const void* w, const void*
     int stall = cfg.stall_row < 0 ? -1 : int(cfg.stall_row / a.S);
     void* args[] = {&x, &y, &w, &b, &stats, &ws, &a, &err, &wait_ns, &stall};
     return gn_stream_launch(reinterpret_cast<const void*>(gn_stream_kernel<T, VEC, ACT>), a, ws, workspace, VEC,
-                            walk_smem<T, VEC, kGnStreamDepth, 1>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C), false, args,
+                            walk_smem<T, VEC, kGnStreamDepth, 1>() + 8 * (size_t(a.ty) * a.tx * VEC + a.C) + 4 * size_t(a.G),
+                            false, args,
                             cfg);
 }
 

@@ -388,7 +388,7 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
             f.tile = (size_t(tensors) * f.boxes * f.pitch * vec * es + 127) / 128 * 128;
             const size_t groups = size_t(W / a.L);
             f.smem = f.tile + size_t(f.ty) * W * 8 + size_t(W) * 8 + groups * 8 * (1 + 2 * cluster) + f.boxes * 8 +
-                     size_t(f.ty) * 4;
+                     size_t(f.ty) * 4 + groups * 4;
             if (f.smem > kGnSmem) continue;
             f.parts_log2 = W >= kGnBlock ? 0 : std::min(5, log2_floor(std::min(kGnBlock / W, f.ty)));
             f.team_log2 = std::min(std::min(5, log2_floor(kGnBlock / std::min<int>(kGnBlock, int(groups)))),

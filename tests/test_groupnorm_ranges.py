@@ -79,3 +79,30 @@ def test_the_activations_keep_a_nan(monkeypatch):
                 dw = ro.rowops_groupnorm_act_backward(x, torch.ones_like(x), stats, 4, w, b, act)[1]
                 if act != "none":
                     assert torch.isnan(dw[9]) and torch.isfinite(dw[:8]).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,spreads", [("f32", 1e2), ("f32", 1e4), ("f32", 1e6), ("bf16", 1e2)])
+@pytest.mark.parametrize("B,S,C,G", [(2, 2048, 64, 4), (1, 40000, 32, 2), (3, 1155, 33, 3), (2, 700, 62, 1)])
+def test_group_means_many_spreads_from_zero(B, S, C, G, dtype, spreads, form, monkeypatch):
+    """All channels of a group share one mean, `spreads` standard deviations from
+    zero: 1 / sd keeps its precision (1e-5, as near zero), the mean is right to 4e-6
+    of the spread and its own rounding, and the output is off by that rounding
+    (2^-24 |mean|, in spreads) beside the usual 1e-5."""
+    monkeypatch.setenv("ROWOPS_GROUPNORM", form)
+    rng = np.random.default_rng(8)
+    v = rng.normal(size=(B, S, G, C // G)) + spreads * rng.choice([-1.0, 1.0], size=(B, 1, G, 1))
+    x = torch.from_numpy(v.reshape(B, S, C)).to("cuda", TYPES[dtype])
+    stats = torch.empty(B, G, 2, device="cuda")
+    y = ro.rowops_groupnorm_act(x, G, eps=0.0, act="none", stats=stats)
+    st, got = O.groupnorm_stats(f64(x), G, 0.0), f64(stats)
+    near(got[..., 1] / st[..., 1], np.ones((B, G)), 1e-5, "1 / sd")
+    near(got[..., 0], st[..., 0], 4e-6 / st[..., 1] + 2.0**-23 * np.abs(st[..., 0]), "mean")
+    ref = O.groupnorm_act(f64(x), G, eps=0.0, name="none")
+    wide = np.repeat(2.0**-24 * np.abs(st[..., 0]) * st[..., 1], C // G, axis=1)[:, None]
+    u = 2.0**-8 if dtype == "bf16" else 0.0
+    near(f64(y), ref, (1e-5 + wide) * np.maximum(1, np.abs(ref)) + u * np.abs(ref), "y")
+    z = x.clone()  # in place: the value that the means are kept less of is overwritten in the end
+    stats2 = torch.empty_like(stats)
+    assert torch.equal(ro.rowops_groupnorm_act(z, G, eps=0.0, act="none", y=z, stats=stats2), y)
+    assert torch.equal(stats, stats2)
