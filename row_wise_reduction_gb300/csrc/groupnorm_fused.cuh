@@ -169,7 +169,7 @@ __device__ __forceinline__ void gn_fetch(const GnTile<T, VEC>& k, const RowsMap*
 }
 
 // The first pass: g over the thread's positions as the boxes arrive; nonzero in the
-// threads whose wait ran out.
+// threads whose wait ran out, which wait for no further box.
 template <int U, typename T, int VEC, int N, typename F>
 __device__ __forceinline__ int gn_read(const GnTile<T, VEC>& k, const typename Vec<T, VEC>::Word* const (&tiles)[N],
                                        uint64_t* bars, int fail, unsigned long long wait_ns, F g) {
@@ -179,7 +179,7 @@ __device__ __forceinline__ int gn_read(const GnTile<T, VEC>& k, const typename V
         [&](int end) {
             if constexpr (Vec<T, VEC>::kWhole)
                 for (; q * k.f.box < end; ++q)
-                    if (!fail) late |= !mbar_wait(&bars[q], k.turn & 1, wait_ns);
+                    if (!fail && !late) late = !mbar_wait(&bars[q], k.turn & 1, wait_ns);
         },
         g, [](int) {});
     return late;
@@ -225,11 +225,15 @@ __device__ __forceinline__ void gn_write(const GnTile<T, VEC>& k, const RowsMap*
 }
 
 // After a wait that ran out: nothing more is asked for or written; the copies still
-// in flight get one more wait, and the error word is set.
+// in flight get one more wait, of one limit for them all, and the error word is set.
 template <typename T, int VEC>
 __device__ __forceinline__ void break_waits(const GnTile<T, VEC>& k, uint64_t* bars, unsigned* err, unsigned long long wait_ns) {
     if (!Vec<T, VEC>::kWhole || k.t != 0) return;
-    for (int q = 0; q * k.f.box < k.rows; ++q) mbar_wait(&bars[q], k.turn & 1, wait_ns);
+    const unsigned long long t0 = global_ns();
+    for (int q = 0; q * k.f.box < k.rows; ++q) {
+        const unsigned long long spent = global_ns() - t0;
+        mbar_wait(&bars[q], k.turn & 1, spent < wait_ns ? wait_ns - spent : 0);
+    }
     atomicExch(err, kDeviceErrTimeout);
 }
 

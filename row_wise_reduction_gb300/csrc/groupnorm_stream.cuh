@@ -275,7 +275,9 @@ __device__ __forceinline__ bool gn_ready(const unsigned* done, unsigned long lon
 // The sequence's items, one after the other: sums(item, share, walked), which leaves a
 // chunk's sums and calls walked() once it has read the chunk, join(item), true where
 // that made a sample's results, and apply(item, share, ready), which calls ready()
-// before it uses them and ends where that is false. (Chunks applied in two parts, for
+// before it uses them and ends where that is false: its CTA then takes no further item
+// and leaves none to the others, whose own waits, one each at most, end the same way.
+// (Chunks applied in two parts, for
 // a more even end, cost B1 S262144 C128 bf16 59 us instead of 52: an item's start and
 // end are the dearer.)
 template <typename Sums, typename Join, typename Apply>
@@ -296,11 +298,15 @@ __device__ __forceinline__ void gn_sequence(const GnArgs& a, const GnStreamWs& w
         const GnItem it(i, a);
         const GnShare k(a, it);
         if (it.apply) {
-            apply(it, k, [&] {
-                const bool there = gn_ready(&ws.done[it.sample], wait_ns);
-                if (!there && t == 0) atomicExch(err, kDeviceErrTimeout);
-                return there;
-            });
+            bool there = true;
+            apply(it, k, [&] { return there = gn_ready(&ws.done[it.sample], wait_ns); });
+            if (!there) {
+                if (t == 0) {
+                    atomicExch(ws.next, items);
+                    atomicExch(err, kDeviceErrTimeout);
+                }
+                return;
+            }
         } else {
             sums(it, k, [&] {
                 if (t == 0 && !a.early) after = atomicAdd(ws.next, 1u);
