@@ -1218,12 +1218,12 @@ rowops_status_t rowops_groupnorm_act(const void* x, void* y, const void* w, cons
     if (!apart_from({y, rows}, {{w, row}, {b, row}}) ||
         !apart_from({stats, sb}, {{x, rows}, {y, rows}, {w, row}, {b, row}}))
         return ROWOPS_ERR_INVALID_VALUE;
-    const size_t need = rowops_groupnorm_act_workspace_bytes(B, S, C, G, dtype);
+    const Tuning tn = tuning();  // once: the workspace checked is that of the form chosen
+    const size_t need = gn_bytes(B, S, C, G, es, 1, tn.groupnorm);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ROWOPS_ERR_WORKSPACE;
     if (need && !apart_from({workspace, workspace_bytes}, {{x, rows}, {y, rows}, {w, row}, {b, row}, {stats, sb}}))
         return ROWOPS_ERR_INVALID_VALUE;
     ld = row_stride(M, C, ld);
-    const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
     const int vec = row_access(tn, C, ld, es, {x, y});
@@ -1264,14 +1264,14 @@ rowops_status_t rowops_groupnorm_act_backward(const void* x, const void* dy, con
         st = zero(dw, C, stream);
         return st == ROWOPS_OK ? zero(db, C, stream) : st;
     }
-    const size_t need = rowops_groupnorm_act_backward_workspace_bytes(B, S, C, G, dtype);
+    const Tuning tn = tuning();
+    const size_t need = gn_bytes(B, S, C, G, es, 2, tn.groupnorm);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return ROWOPS_ERR_WORKSPACE;
     for (const Range& r : in)
         if (need && !apart(workspace, workspace_bytes, r.p, r.n)) return ROWOPS_ERR_INVALID_VALUE;
     if (need && !apart_from({workspace, workspace_bytes}, {{dx, rows}, {dw, sums}, {db, sums}}))
         return ROWOPS_ERR_INVALID_VALUE;
     ld = row_stride(M, C, ld);
-    const Tuning tn = tuning();
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
     const int vec = row_access(tn, C, ld, es, {x, dy, dx});
