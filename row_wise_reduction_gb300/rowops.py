@@ -623,6 +623,8 @@ def _elsewhere(fn, stream, dev, *args, **kwargs):
             return fn(*args, **kwargs)
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        elif stream.device.index != dev:
+            raise ValueError("stream must belong to the device of the call's tensors")
         with torch.cuda.stream(stream):
             return fn(*args, **kwargs)
 
