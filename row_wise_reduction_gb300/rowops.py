@@ -298,7 +298,7 @@ def _xy(x: torch.Tensor, y: Optional[torch.Tensor]):
     else:
         if y.dtype is not dt or y.get_device() != dev or y.shape != sh:
             raise ValueError("y must match x in shape, dtype and device")
-        if y.stride() != st and (M > 1 or (N > 1 and y.stride(1) != 1)):
+        if y.stride() != st and (M > 1 or (M == 1 and N > 1 and y.stride(1) != 1)):
             raise ValueError("x and y must share the row stride")
     return M, N, (st[0] if M > 1 else max(N, st[0])), y, code, dev
 
@@ -811,7 +811,7 @@ def rowops_bias_dropout_residual(
     if residual is not None and (residual.dtype is not x.dtype or residual.get_device() != dev
                                  or residual.shape != x.shape
                                  or (residual.stride() != x.stride()
-                                     and (M > 1 or (N > 1 and residual.stride(1) != 1)))):
+                                     and (M > 1 or (M == 1 and N > 1 and residual.stride(1) != 1)))):
         raise ValueError("residual must match x in shape, dtype, device and row stride")
     st = (_calls or _hot_calls()).bias_dropout_residual(
         x.data_ptr(), None if residual is None else residual.data_ptr(), _affine(bias, x, N, dev, "bias"),
