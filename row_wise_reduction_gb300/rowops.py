@@ -252,7 +252,8 @@ def _out_like(x: torch.Tensor, y: Optional[torch.Tensor]) -> torch.Tensor:
         return torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device)
     if y.dtype is not x.dtype or y.get_device() != x.get_device() or y.shape != x.shape:
         raise ValueError("y must match x in shape, dtype and device")
-    if y.shape[0] > 1 and y.stride() != x.stride():
+    M, N = y.shape
+    if y.stride() != x.stride() and (M > 1 or (M == 1 and N > 1 and y.stride(1) != 1)):
         raise ValueError("x and y must share the row stride")
     return y
 
