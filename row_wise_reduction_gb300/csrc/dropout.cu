@@ -415,13 +415,10 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         const int64_t c0 = int64_t(blockIdx.x) * SPAN;
         for (int i = threadIdx.x; i < 2 * SPAN; i += kWarps * 32)
             if (c0 + i < a.N) out[c0 + i] = i < SPAN + V ? sum(i) : 0.f;
-        // odd segments' row has nothing before the first of them
+        // odd segments' row has nothing before the first of them (one segment alone has
+        // fewer than SPAN columns)
         if (blockIdx.x == 0)
             for (int i = threadIdx.x; i < SPAN && i < a.N; i += kWarps * 32)
-                part[(int64_t(blockIdx.y) * 2 + 1) * a.N + i] = 0.f;
-        // and, where there is one segment alone, nothing at all
-        if (gridDim.x == 1)
-            for (int64_t i = SPAN + threadIdx.x; i < a.N; i += kWarps * 32)
                 part[(int64_t(blockIdx.y) * 2 + 1) * a.N + i] = 0.f;
     }
 }
