@@ -7,12 +7,7 @@
 
 namespace rowops {
 
-// the larger of z and lo; the nearest to z within bound of 0; a NaN stays
-__device__ __forceinline__ float at_least(float z, float lo) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(lo));
-    return y;
-}
+// the nearest to z within bound of 0; a NaN stays
 __device__ __forceinline__ float within(float z, float bound) {
     float y;
     asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(bound));
@@ -20,26 +15,23 @@ __device__ __forceinline__ float within(float z, float bound) {
 }
 
 // e = 2^a and q = 1 / (1 + e) of two values from one reciprocal, that of the
-// product (1 + e_x) (1 + e_y). a is kept to 60 (a NaN as well, which would pass to the
-// other value; the callers' z carries it on), so the product stays finite and normal,
-// and q at 2^-60 where it is smaller: z q then has to be built from a z kept within
-// bounds as well. One and a half special-function results a value instead of
-// two, which an SM makes 16 of a cycle: a pass that reads from L2 and the backward
-// pass, which evaluates the slope twice, would be bound by them.
+// product (1 + e_x) (1 + e_y). a is kept to 84 (a NaN as well, which would pass to the
+// other value; the callers' z carries it on), so q stays at 2^-84 where it is smaller.
+// Where the product passes 2^126, its reciprocal and with it both q are 0: one is at
+// 2^-84 there and the other below 2^-42. What is built from q, z q or z q (1 - q), is then
+// off by at most |z| 2^-84 (5e-6 at |z| = 10^20) or 7e-12. One and a half special-function
+// results a value instead of two, which an SM makes 16 of a cycle: a pass that reads
+// from L2 and the backward pass, which evaluates the slope twice, would be bound by them.
 __device__ __forceinline__ float2 sigmoids2(float2 a, float2& e) {
-    e = make_float2(ex2_approx(fminf(a.x, 60.f)), ex2_approx(fminf(a.y, 60.f)));
+    e = make_float2(ex2_approx(fminf(a.x, 84.f)), ex2_approx(fminf(a.y, 84.f)));
     const float2 d = f2_add(e, f2(1.f));
     const float r = rcp_approx(d.x * d.y);
     return f2_mul(make_float2(d.y, d.x), f2(r));
 }
 
-// z for SiLU and its slope: not below -41.5, where a = -z log2(e) is 59.9. Both are
-// within 5e-17 of 0 there and beyond, and no factor z is left to make q's 2^-60 large.
-__device__ __forceinline__ float2 silu_range(float2 z) { return make_float2(at_least(z.x, -41.5f), at_least(z.y, -41.5f)); }
-
 // z for the slope of the tanh form: within 7.4 of 0, where a is 58.8 (and -58.8: e =
 // 2^-58.8). The slope is within 2.1e-16 of 0 (or 1) there and beyond, and its cubic
-// factor z (1 + 3 k1 z^2) stays below 100: kept at large z it would make of q's 2^-60,
+// factor z (1 + 3 k1 z^2) stays below 100: kept at large z it would make of q's 2^-84,
 // or of e = 0 once it overflows, any number or a NaN.
 __device__ __forceinline__ float2 tanh_slope_range(float2 z) {
     return make_float2(within(z.x, 7.4f), within(z.y, 7.4f));
@@ -49,7 +41,6 @@ template <int ACT>
 __device__ __forceinline__ float2 act_of2(float2 z) {
     if constexpr (ACT == ROWOPS_ACT_SILU) {
         float2 e;
-        z = silu_range(z);
         return f2_mul(z, sigmoids2(f2_mul(z, f2(-kLog2eF)), e));
     } else if constexpr (ACT == ROWOPS_ACT_GELU) {
         return gelu_erf2(z);
@@ -68,7 +59,6 @@ template <int ACT>
 __device__ __forceinline__ float2 act_grad2(float2 z) {
     if constexpr (ACT == ROWOPS_ACT_SILU) {
         float2 e;
-        z = silu_range(z);
         const float2 q = sigmoids2(f2_mul(z, f2(-kLog2eF)), e);
         return f2_fma(f2_mul(z, q), f2_mul(e, q), q);
     } else if constexpr (ACT == ROWOPS_ACT_GELU) {
