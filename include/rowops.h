@@ -539,6 +539,8 @@ rowops_status_t rowops_bias_dropout_residual_backward(const void* dy, void* dx, 
  * of logits and the K experts chosen for each, over the n rows that take part:
  *   p_t = softmax(logits_t);  counts[e] = how often e was chosen
  *   loss = coef E sum_e (counts[e] / (n K)) (sum_t p_te / n)
+ * (so even counts and probabilities give coef; a definition without the division by
+ * K gives K times as much: a coefficient that belongs to it is to be multiplied by K).
  * n = 0 gives 0. Rows follow rowops_softmax: -inf logits have p = 0, a row of
  * -inf alone adds nothing to the sums, a NaN makes the loss NaN. (No counterpart
  * on the source pages: rowops_softmax followed by column sums.)

@@ -6,8 +6,7 @@
 // offset) and key seed, and is kept where they reach round(65536 p). The mask is
 // a function of position alone: never stored, and the same for every layout,
 // launch shape and type. Sixteen bits an element instead of 32 halve the
-// generator's share of the instructions: ten rounds cost about 60 instructions
-// for eight elements.
+// generator's share of the instructions: ten rounds of four for eight elements.
 //
 // A team of TL lanes holds 8 TL consecutive columns of a row; lane l makes the
 // block of columns 8 l .. 8 l + 7. Each lane moves the columns that coalesce best
@@ -18,14 +17,16 @@
 // loaded once and column sums stay in registers until the chunk's end; they leave
 // one partial row per chunk, added up by a second kernel in a fixed order.
 //
-// Bound by traffic, with the instructions not far behind (about 90 for a 16-byte
-// vector of bf16, of which the generator is 40): rows come in through a ring of
+// Bound by traffic, with the instructions not far behind (for a 16-byte vector of bf16
+// 112 backward, 138 with bias and residual; the generator's 40 among them): rows come in through a ring of
 // copies into shared memory, a slot for each thread alone, so that the rows in
 // flight take no registers. With four rows in flight in registers the kernel held
 // half as many warps and bf16 16384 x 8192 with column sums took 124.8 us. Now 88 us
-// (6.1 TB/s); forward, with bias and residual, 120 us (6.7 TB/s); bf16 4001 x 4097 with
-// column sums, rows at odd offsets, 23 us: bound by the generator's and the decisions'
-// instructions (without dropping, p = 0 and no column sums, 13 us).
+// (6.1 TB/s); forward, with bias and residual, 120 us (6.7 TB/s). bf16 4001 x 4097 with
+// column sums, rows at odd offsets: 23 us for a floor of 9.6 (p = 0 without column
+// sums 13 us), bound by neither memory (15%) nor issue (45%): 17 x 63 CTAs leave a warp
+// eight rows, of which the ring's start is five, and the shifted form takes 29
+// instructions an element where the vector form takes 14.
 #include <algorithm>
 
 #include "async_ring.cuh"

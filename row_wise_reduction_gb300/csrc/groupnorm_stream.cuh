@@ -1,21 +1,25 @@
 // Group norm + activation and its backward for samples too large to hold: one
-// persistent kernel that reads the tensors twice, the second time from L2.
+// persistent kernel that reads the tensors twice, forward the second time from L2.
 //
 // The work is a sequence of items, each a chunk of a sample's positions: one that
 // adds up ("sums") and one that writes ("apply"). CTAs take them off the sequence
 // with a counter. An apply item stands behind all sums of its sample, by as much as
-// the CTAs have in hand, so its sample's results are there when it is taken and its
-// chunk is still in L2; sums of later samples and writes of earlier ones share
-// the memory system meanwhile. Whoever finishes a sample's last sums adds up its
+// the CTAs have in hand, so its sample's results are there when it is taken. In batches
+// of more chunks than that (a sample's and one for every CTA), sums of later samples and
+// writes of earlier ones share the memory system meanwhile; in all others the two kinds
+// are two phases, one after the other. Forward at most 456 chunks of 192 KiB and a sample
+// lie between a chunk's two reads, 90 MB, which L2 (129 MB) holds; backward 304 of 512
+// KiB, 160 MB and more, so x and dy come from memory a second time (shorter distances by
+// smaller chunks cost more than that: gn_plan). Whoever finishes a sample's last sums adds up its
 // chunks, in order. An apply item that comes too early waits (with a limit); it
 // waits for items before it in the sequence alone, and sums never wait, so the
 // waits end whatever CTAs run at the same time.
 //
-// bf16 SiLU B32 S4096 C320: 47 us (3.6 TB/s of what must be moved once), backward 77 us
-// (3.3 TB/s); B1 S262144 C128: 50 us. The reads of the sums run at 5 TB/s beside the
-// write-back of what the last call wrote; the second pass takes as long from L2
-// as the first from memory; one sample alone has nothing to do while its sums are
-// joined (7 us).
+// bf16 SiLU B32 S4096 C320: 47.4 us (3.5 TB/s of what must be moved once), backward 77 us
+// (3.3 TB/s); B1 S262144 C128: 50.6 us. The reads of the sums run at 5 TB/s beside the
+// write-back of what the last call wrote; forward the second pass takes as long from L2
+// as the first from memory; where there are two phases nothing is done while the sums
+// are joined (7 us).
 #pragma once
 
 #include "async_ring.cuh"

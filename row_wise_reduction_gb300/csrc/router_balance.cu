@@ -14,7 +14,10 @@
 // finishes in the first kernel.
 //
 // fp32 131072 x 256, 8 choices: 31 us (4.6 TB/s with the choices), of which the second
-// kernel's launch and latency are about 4; its gradient 47 us (5.7 TB/s). 64 x 8: 4.1
+// kernel's launch and latency are about 4; its gradient 47 us (5.7 TB/s). With 256 experts
+// a CTA has 85 KB of shared memory, so two share an SM, and of clusters of eight 36 fit:
+// 288 CTAs, 24% of an SM's warps, where the gradient, with the same shuffles a row and no
+// cluster, has 456 and 34%. 64 x 8: 4.1 to 4.8
 // and 3.4 us, a launch's latency. bf16 131072 x 60, rows that are no whole vectors: 16
 // and 13 us by pairs, 21 and 16 by single elements.
 #include <algorithm>
@@ -228,6 +231,8 @@ __device__ __forceinline__ void finish_loss(const float* P, const int* c, int E,
     }
 }
 
+// (Registers for three CTAs an SM; in fp32 the shared memory leaves two from some 100
+// experts on.)
 template <typename T, typename I, int VEC, int NV, bool FULL>
 __global__ void __launch_bounds__(kBlock, NV * VEC <= 16 ? 3 : 1)
     balance_kernel(const T* logits, const I* experts, const uint8_t* mask, int64_t rows, int E, int K, int64_t ld,
@@ -455,7 +460,8 @@ cudaError_t launch_fwd(const void* logits, const void* experts, const uint8_t* m
         grid = cl;
     } else {
         cl = kCluster;
-        // one wave: 456 CTAs where 408 fit took nearly twice the time
+        // one wave: with a few clusters more than fit (then 57 where 51 did) the kernel took
+        // nearly twice the time
         int n = clusters_on_device(reinterpret_cast<const void*>(kern), kBlock, smem, cl, cfg);
         if (n > kBalanceMaxClusters) n = kBalanceMaxClusters;
         grid = int(std::min<int64_t>((items + cl - 1) / cl, n)) * cl;

@@ -281,8 +281,9 @@ struct GnArgs {
     int64_t chunk_rows;         // positions of a chunk
 };
 
-// The streaming form's chunks: large, as an item's start and end cost a CTA some 4 us,
-// but not so large that the second read misses L2; whole waves of CTAs where there are
+// The streaming form's chunks: large, as an item's start and end cost a CTA some 4 us;
+// forward not so large that the second read misses L2 (backward it does miss it, which
+// costs less than the smaller chunks' starts and ends); whole waves of CTAs where there are
 // few (two CTAs for each SM backward, three forward), at least 16 KiB. Chunks of 128,
 // 256, 512 KiB, bf16: B32 S4096 C320 backward 98, 85, 78 us, B128 342, 294, 271;
 // B8 S65536 C128 159, 126, 115; of 128, 192, 384 KiB, forward, the last two 164, 160,
@@ -411,7 +412,8 @@ inline double gn_fused_plan(const GnArgs& a, int es, int tensors, int vec, GnFus
 
 // The streaming form's modelled time: launches and the ends of the sums, and its
 // traffic at what it measured. Modelled and measured in us, the same sizes: 26 and 25,
-// 32 and 32, with B32 52 and 47, 79 and 77; odd ld 19 and 21.
+// 32 and 32, with B32 52 and 47, 79 and 77; odd ld 19 and 21. One sample of middle size,
+// which no cluster holds, takes half as long again: B1 S16671 C544 25 and 38.
 inline double gn_stream_time(const GnArgs& a, int es, int tensors) {
     const double in = double(a.B) * a.S * a.C * es * tensors;
     if (tensors > 1) return 16.0 + 1.5 * in / (es == 4 ? 4.4e6 : 4.0e6);

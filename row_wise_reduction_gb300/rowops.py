@@ -900,7 +900,9 @@ def rowops_router_balance_loss(
     """Balance loss of a router from its ``logits`` (T, E) and the chosen
     ``experts`` (T, K) (int32 or int64): ``(loss, counts)``, loss float32 (1,),
     counts int64 (E + 1,): the experts' counts and, last, the rows that took
-    part. ``mask``: bool or uint8 (T,), rows with 0 take no part."""
+    part. ``mask``: bool or uint8 (T,), rows with 0 take no part. The counts enter
+    divided by the choices, T K of them, so that an even load gives ``coef`` (a
+    coefficient made for a definition without that K is to be multiplied by it)."""
     dev = logits.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_router_balance_loss, stream, dev, logits, experts, coef, mask, loss, counts,
