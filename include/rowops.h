@@ -581,6 +581,102 @@ rowops_status_t rowops_router_balance_loss_backward(const void* logits, const in
                                                     int64_t E, int64_t K, int64_t ld, rowops_dtype_t dtype,
                                                     cudaStream_t stream);
 
+/*
+ * RMSNorm, with the residual's addition, whose result leaves in 8 bits with scales
+ * (for a product in 8 bits):
+ *   residual_out = x + residual, rounded to `dtype`;  s = that (x without a residual)
+ *   y     = s / sqrt(sum_j s_j^2 / N + eps) * w        (as rowops_rmsnorm, not rounded)
+ *   scale = max(max |y| / 448, 2^-126) over a row, or over `group` columns of it
+ *   q     = e4m3(y / scale), nearest even, so that y is about q * scale
+ * (No counterpart on the source pages: the output form of rowops_fused_residual_rmsnorm.)
+ *
+ *   x, residual, residual_out   device pointers to M rows of `ld` elements; residual
+ *            and residual_out NULL for no residual. residual_out may equal x or residual.
+ *   q        device pointer to M rows of `ldq` bytes (>= N), one e4m3 number each.
+ *   scales   device pointer to M * ceil(N / group) floats, row after row (M for group 0).
+ *   group    0: one scale a row; else a multiple of 32 columns, the last group of a row
+ *            may be shorter. (More than N columns are as N.)
+ *   w, eps   as for rowops_rmsnorm.
+ * q and scales lie apart from each other and from all else. A NaN in a row makes its
+ * scales and its q NaN, an infinity those of its group (y is 0 in the row's others).
+ * 16-byte aligned rows of whole 16-byte vectors (and w, and q rows aligned to as many
+ * bytes as a vector has elements) are the fastest.
+ */
+rowops_status_t rowops_rmsnorm_quant(const void* x, const void* residual, void* q, float* scales, void* residual_out,
+                                     const void* w, float eps, int64_t M, int64_t N, int64_t ld, int64_t ldq,
+                                     int64_t group, rowops_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Attention of one new token a sequence over a paged key-value cache [EX §5.1 attention;
+ * L6 §7.2 online softmax], the values summed along, split over the cache's length. For
+ * sequence b and head h, with kv = h / (heads / kv_heads):
+ *   s_j = scale sum_d q[b, h, d] k[j, kv, d]       first <= j < n, n = lengths[b]
+ *   out[b, h, :] = sum_j p_j v[j, kv, :],  p = softmax(s);  lse[b, h] = log sum_j exp(s_j)
+ * first = 0, or max(0, n - window) with a window. Position j is slot j mod page of the
+ * page page_table[b, j / page].
+ *
+ *   q, out   device pointers to B rows of `ldq`, `ldo` elements of `dtype`: heads * D of
+ *            them each, head after head.
+ *   k, v     device pointers to caches of `pages` pages of `page` slots of kv_heads heads
+ *            of D elements, these next to each other; page_stride, slot_stride and
+ *            head_stride (elements, the same in k and v) say where the others lie.
+ *   page_table   device pointer to B rows of `ldt` int32, max_pages of them each. Entries
+ *            past a sequence's pages are not read, slots past its length do not matter.
+ *   lengths  device pointer to B int32. A length of 0 (or less) gives out 0 and lse
+ *            -infinity. One beyond max_pages * page, or a page outside [0, pages) that
+ *            the sequence attends to, makes its out and lse NaN; nothing outside is read.
+ *   lse      NULL, or B * heads floats.
+ *   window   0, or how many of the last positions are attended to.
+ *   workspace, workspace_bytes   device memory, 256-byte aligned, at least
+ *            rowops_paged_attention_workspace_bytes(...) bytes (overwritten; 0: NULL
+ *            will do), apart from the other tensors; calls sharing it must be ordered
+ *            on one stream.
+ * D is at most 256 (ROWOPS_ERR_UNSUPPORTED beyond). Statistics and sums in fp32, added
+ * up in an order that the lengths of all the call's sequences decide: equal calls give
+ * equal bits, other company may change a sequence's last bits. The lengths are read
+ * on the device, so a captured graph replays with those of the day. k and v at 16-byte
+ * aligned heads of whole 16-byte vectors are the fastest.
+ */
+size_t rowops_paged_attention_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
+                                              rowops_dtype_t dtype);
+rowops_status_t rowops_paged_attention(const void* q, const void* k, const void* v, const int32_t* page_table,
+                                       const int32_t* lengths, void* out, float* lse, float scale, int64_t window,
+                                       int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t ldq, int64_t ldo,
+                                       int64_t pages, int64_t page, int64_t page_stride, int64_t slot_stride,
+                                       int64_t head_stride, int64_t max_pages, int64_t ldt, rowops_dtype_t dtype,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * One token drawn from each row of logits with a given uniform number. With m the row's
+ * maximum and T its temperature, w_j = exp((x_j - m) / T), and the columns ordered by
+ * value, the largest first, equal ones by index, a row keeps the shortest of
+ *   top-k   the first top_k columns                   (0, or N and more: all)
+ *   top-p   of those, the fewest, one at least, whose w reach top_p of their sum
+ *                                                     (1 and more: all)
+ *   min-p   those with w_j >= min_p                   (0: all)
+ * and its token is the first column, by index, at which the running sum of the kept w
+ * exceeds u times their sum. T = 0: the maximum, the first of equal ones. (No
+ * counterpart on the source pages: rowops_softmax followed by a draw.)
+ *
+ *   logits   device pointer to M rows of `ld` elements of `dtype`. A column of -inf is
+ *            never drawn. If there is nothing else in the row, or a NaN in it, its token
+ *            is -1 and its logprob NaN. Columns of +inf are drawn from alone, evenly.
+ *   u        device pointer to M floats in [0, 1) (below: as 0; 1 and more: the last kept).
+ *   temperature, top_k, top_p, min_p   device pointers to M numbers, one a row, or NULL:
+ *            the `_all` number then holds for every row. (On the device, numbers below
+ *            the ranges are as 0, above them as the largest; a NaN temperature is 0, of
+ *            the others no cut.)
+ *   token    device pointer to M int64.
+ *   logprob  NULL, or M floats: the log-probability of the token among those kept.
+ * N is at most 393216 and M at most 2^27 (ROWOPS_ERR_UNSUPPORTED beyond). w is held in
+ * fixed point, 44 bits behind the point and right to 2^-29 of its value, and added up
+ * exactly: the same token for the same row, whatever the batch around it.
+ */
+rowops_status_t rowops_sample(const void* logits, const float* u, const float* temperature, float temperature_all,
+                              const int32_t* top_k, int32_t top_k_all, const float* top_p, float top_p_all,
+                              const float* min_p, float min_p_all, int64_t* token, float* logprob, int64_t M,
+                              int64_t N, int64_t ld, rowops_dtype_t dtype, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

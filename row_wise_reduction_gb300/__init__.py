@@ -3,7 +3,8 @@
 Stable and causal softmax, split-row online softmax, fused LayerNorm -> affine ->
 GELU (tanh or exact) and its backward, fused residual + bias + GELU, RMSNorm and fused residual + RMSNorm, row sums and row
 maxima; group norm + activation, bias + dropout + residual and the router's balance
-loss, each with its backward; exposed through the C ABI of
+loss, each with its backward; RMSNorm with an 8-bit result, attention of one token
+over a paged cache and sampling; exposed through the C ABI of
 ``librowops.so`` (``include/rowops.h``) and the thin ctypes binding in
 :mod:`row_wise_reduction_gb300.rowops`.
 """
@@ -32,12 +33,16 @@ from .rowops import (  # noqa: F401
     rowops_online_softmax_noalloc,
     rowops_online_softmax_status,
     rowops_online_softmax_workspace_bytes,
+    rowops_paged_attention,
+    rowops_paged_attention_workspace_bytes,
     rowops_rmsnorm,
+    rowops_rmsnorm_quant,
     rowops_router_balance_loss,
     rowops_router_balance_loss_backward,
     rowops_router_balance_loss_workspace_bytes,
     rowops_row_max,
     rowops_row_sum,
+    rowops_sample,
     rowops_softmax,
     rowops_softmax_causal,
     rowops_reload_tuning,

@@ -53,6 +53,9 @@ SOURCES = [
     "groupnorm_bf16.cu",
     "dropout.cu",
     "router_balance.cu",
+    "norm_quant.cu",
+    "paged_attention.cu",
+    "sample.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

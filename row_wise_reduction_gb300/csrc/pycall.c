@@ -100,8 +100,8 @@ static PyObject* layernorm_gelu_erf(PyObject* self, PyObject* const* a, Py_ssize
 }
 
 /*
- * The training operators' entry points and workspace queries: the same
- * marshalling, one function each.
+ * The training and serving operators' entry points and workspace queries: the
+ * same marshalling, one function each.
  */
 static int as_f32(PyObject* o, float* out) {
     const double v = PyFloat_AsDouble(o);
@@ -115,7 +115,8 @@ static int as_u64(PyObject* o, uint64_t* out) {
     return (*out == (uint64_t)-1 && PyErr_Occurred()) ? -1 : 0;
 }
 
-#define MOST_ARGS 20
+#define MOST_ARGS 26
+#define BOUND 14
 typedef struct {
     void* p[MOST_ARGS];
     int64_t i[MOST_ARGS];
@@ -137,8 +138,8 @@ static int take(const char* name, const char* form, PyObject* const* a, Py_ssize
     return 0;
 }
 
-/* the addresses, in the order of bind_training's arguments */
-static void* g_training[10];
+/* the addresses, in the order of bind_operators' arguments */
+static void* g_bound[BOUND];
 
 typedef size_t (*gn_bytes_fn)(int64_t, int64_t, int64_t, int64_t, int);
 typedef size_t (*rows_bytes_fn)(int64_t, int64_t, int);
@@ -154,13 +155,21 @@ typedef int (*balance_fn)(const void*, const void*, int, const void*, float, flo
                           int64_t, int, void*, size_t, void*);
 typedef int (*balance_bwd_fn)(const void*, const void*, const float*, const void*, float, void*, int64_t, int64_t,
                               int64_t, int64_t, int, void*);
+typedef int (*quant_fn)(const void*, const void*, void*, float*, void*, const void*, float, int64_t, int64_t, int64_t,
+                        int64_t, int64_t, int, void*);
+typedef size_t (*paged_bytes_fn)(int64_t, int64_t, int64_t, int64_t, int);
+typedef int (*paged_fn)(const void*, const void*, const void*, const void*, const void*, void*, float*, float, int64_t,
+                        int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                        int64_t, int64_t, int64_t, int, void*, size_t, void*);
+typedef int (*sample_fn)(const void*, const void*, const void*, float, const void*, int32_t, const void*, float,
+                         const void*, float, void*, float*, int64_t, int64_t, int64_t, int, void*);
 
-static PyObject* bind_training(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+static PyObject* bind_operators(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     int k;
     (void)self;
-    if (!nargs_ok(n, 10, "bind_training")) return NULL;
-    for (k = 0; k < 10; ++k)
-        if (as_ptr(a[k], &g_training[k])) return NULL;
+    if (!nargs_ok(n, BOUND, "bind_operators")) return NULL;
+    for (k = 0; k < BOUND; ++k)
+        if (as_ptr(a[k], &g_bound[k])) return NULL;
     Py_RETURN_NONE;
 }
 
@@ -169,7 +178,7 @@ static PyObject* bind_training(PyObject* self, PyObject* const* a, Py_ssize_t n)
         args_t v;                                                                                             \
         int r;                                                                                                \
         (void)self;                                                                                           \
-        if (!g_training[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");          \
+        if (!g_bound[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");          \
         if (take(#name, form, a, n, &v)) return NULL;                                                         \
         Py_BEGIN_ALLOW_THREADS                                                                                \
         r = (expr);                                                                                           \
@@ -180,38 +189,50 @@ static PyObject* bind_training(PyObject* self, PyObject* const* a, Py_ssize_t n)
     static PyObject* name(PyObject* self, PyObject* const* a, Py_ssize_t n) {                                 \
         args_t v;                                                                                             \
         (void)self;                                                                                           \
-        if (!g_training[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");          \
+        if (!g_bound[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");          \
         if (take(#name, form, a, n, &v)) return NULL;                                                         \
         return PyLong_FromSize_t(expr);                                                                       \
     }
 
 BYTES(groupnorm_act_workspace_bytes, 0, "iiiii",
-      ((gn_bytes_fn)g_training[0])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
+      ((gn_bytes_fn)g_bound[0])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
 CALL(groupnorm_act, 1, "ppppfiiiiiipipip",
-     ((gn_fn)g_training[1])(v.p[0], v.p[1], v.p[2], v.p[3], v.f[4], v.i[5], v.i[6], v.i[7], v.i[8], v.i[9],
+     ((gn_fn)g_bound[1])(v.p[0], v.p[1], v.p[2], v.p[3], v.f[4], v.i[5], v.i[6], v.i[7], v.i[8], v.i[9],
                             (int)v.i[10], (float*)v.p[11], (int)v.i[12], v.p[13], (size_t)v.i[14], v.p[15]))
 BYTES(groupnorm_act_backward_workspace_bytes, 2, "iiiii",
-      ((gn_bytes_fn)g_training[2])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
+      ((gn_bytes_fn)g_bound[2])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
 CALL(groupnorm_act_backward, 3, "ppppppppiiiiiiipip",
-     ((gn_bwd_fn)g_training[3])(v.p[0], v.p[1], v.p[2], v.p[3], (float*)v.p[4], v.p[5], (float*)v.p[6],
+     ((gn_bwd_fn)g_bound[3])(v.p[0], v.p[1], v.p[2], v.p[3], (float*)v.p[4], v.p[5], (float*)v.p[6],
                                 (float*)v.p[7], v.i[8], v.i[9], v.i[10], v.i[11], v.i[12], (int)v.i[13],
                                 (int)v.i[14], v.p[15], (size_t)v.i[16], v.p[17]))
 CALL(bias_dropout_residual, 4, "ppppfuupiiiip",
-     ((drop_fn)g_training[4])(v.p[0], v.p[1], v.p[2], v.p[3], v.f[4], v.u[5], v.u[6], v.p[7], v.i[8], v.i[9],
+     ((drop_fn)g_bound[4])(v.p[0], v.p[1], v.p[2], v.p[3], v.f[4], v.u[5], v.u[6], v.p[7], v.i[8], v.i[9],
                               v.i[10], (int)v.i[11], v.p[12]))
 BYTES(bias_dropout_residual_backward_workspace_bytes, 5, "iii",
-      ((rows_bytes_fn)g_training[5])(v.i[0], v.i[1], (int)v.i[2]))
+      ((rows_bytes_fn)g_bound[5])(v.i[0], v.i[1], (int)v.i[2]))
 CALL(bias_dropout_residual_backward, 6, "pppfuupiiiipip",
-     ((drop_bwd_fn)g_training[6])(v.p[0], v.p[1], (float*)v.p[2], v.f[3], v.u[4], v.u[5], v.p[6], v.i[7], v.i[8],
+     ((drop_bwd_fn)g_bound[6])(v.p[0], v.p[1], (float*)v.p[2], v.f[3], v.u[4], v.u[5], v.p[6], v.i[7], v.i[8],
                                   v.i[9], (int)v.i[10], v.p[11], (size_t)v.i[12], v.p[13]))
 CALL(router_balance_loss, 7, "ppipfppiiiiipip",
-     ((balance_fn)g_training[7])(v.p[0], v.p[1], (int)v.i[2], v.p[3], v.f[4], (float*)v.p[5], v.p[6], v.i[7],
+     ((balance_fn)g_bound[7])(v.p[0], v.p[1], (int)v.i[2], v.p[3], v.f[4], (float*)v.p[5], v.p[6], v.i[7],
                                  v.i[8], v.i[9], v.i[10], (int)v.i[11], v.p[12], (size_t)v.i[13], v.p[14]))
 CALL(router_balance_loss_backward, 8, "ppppfpiiiiip",
-     ((balance_bwd_fn)g_training[8])(v.p[0], v.p[1], (float*)v.p[2], v.p[3], v.f[4], v.p[5], v.i[6], v.i[7], v.i[8],
+     ((balance_bwd_fn)g_bound[8])(v.p[0], v.p[1], (float*)v.p[2], v.p[3], v.f[4], v.p[5], v.i[6], v.i[7], v.i[8],
                                      v.i[9], (int)v.i[10], v.p[11]))
 BYTES(router_balance_loss_workspace_bytes, 9, "iii",
-      ((rows_bytes_fn)g_training[9])(v.i[0], v.i[1], (int)v.i[2]))
+      ((rows_bytes_fn)g_bound[9])(v.i[0], v.i[1], (int)v.i[2]))
+CALL(rmsnorm_quant, 10, "ppppppfiiiiiip",
+     ((quant_fn)g_bound[10])(v.p[0], v.p[1], v.p[2], (float*)v.p[3], v.p[4], v.p[5], v.f[6], v.i[7], v.i[8], v.i[9],
+                             v.i[10], v.i[11], (int)v.i[12], v.p[13]))
+BYTES(paged_attention_workspace_bytes, 11, "iiiii",
+      ((paged_bytes_fn)g_bound[11])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
+CALL(paged_attention, 12, "pppppppfiiiiiiiiiiiiiiipip",
+     ((paged_fn)g_bound[12])(v.p[0], v.p[1], v.p[2], v.p[3], v.p[4], v.p[5], (float*)v.p[6], v.f[7], v.i[8], v.i[9],
+                             v.i[10], v.i[11], v.i[12], v.i[13], v.i[14], v.i[15], v.i[16], v.i[17], v.i[18], v.i[19],
+                             v.i[20], v.i[21], (int)v.i[22], v.p[23], (size_t)v.i[24], v.p[25]))
+CALL(sample, 13, "pppfpipfpfppiiiip",
+     ((sample_fn)g_bound[13])(v.p[0], v.p[1], v.p[2], v.f[3], v.p[4], (int32_t)v.i[5], v.p[6], v.f[7], v.p[8], v.f[9],
+                              v.p[10], (float*)v.p[11], v.i[12], v.i[13], v.i[14], (int)v.i[15], v.p[16]))
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, "rowops_" #name}
 
@@ -221,7 +242,7 @@ static PyMethodDef methods[] = {
     {"layernorm_gelu", (PyCFunction)(void (*)(void))layernorm_gelu, METH_FASTCALL, "rowops_layernorm_gelu"},
     {"layernorm_gelu_erf", (PyCFunction)(void (*)(void))layernorm_gelu_erf, METH_FASTCALL,
      "rowops_layernorm_gelu_erf"},
-    {"bind_training", (PyCFunction)(void (*)(void))bind_training, METH_FASTCALL, "addresses of the functions below"},
+    {"bind_operators", (PyCFunction)(void (*)(void))bind_operators, METH_FASTCALL, "addresses of the functions below"},
     METHOD(groupnorm_act_workspace_bytes),
     METHOD(groupnorm_act),
     METHOD(groupnorm_act_backward_workspace_bytes),
@@ -232,6 +253,10 @@ static PyMethodDef methods[] = {
     METHOD(router_balance_loss),
     METHOD(router_balance_loss_backward),
     METHOD(router_balance_loss_workspace_bytes),
+    METHOD(rmsnorm_quant),
+    METHOD(paged_attention_workspace_bytes),
+    METHOD(paged_attention),
+    METHOD(sample),
     {NULL, NULL, 0, NULL},
 };
 

@@ -1404,4 +1404,130 @@ rowops_status_t rowops_router_balance_loss_backward(const void* logits, const in
     return finish(fn(logits, counts, dloss, mask, dlogits, T, int(E), int(K), ld, coef, vec, cfg));
 }
 
+// Serving operators -----------------------------------------------------------------------------
+rowops_status_t rowops_rmsnorm_quant(const void* x, const void* residual, void* q, float* scales, void* residual_out,
+                                     const void* w, float eps, int64_t M, int64_t N, int64_t ld, int64_t ldq,
+                                     int64_t group, rowops_dtype_t dtype, cudaStream_t stream) {
+    const bool res = residual != nullptr;
+    rowops_status_t st = check_rows(x, x, M, N, ld, dtype);
+    if (st == ROWOPS_OK && res) st = check_rows(x, residual_out, M, N, ld, dtype);
+    if (st == ROWOPS_OK && res) st = check_rows(residual, residual_out, M, N, ld, dtype);
+    if (st != ROWOPS_OK) return st;
+    if (!(eps >= 0.f) || eps == INFINITY || group < 0 || group % 32 != 0 || ldq < N) return ROWOPS_ERR_INVALID_VALUE;
+    if (M == 0) return ROWOPS_OK;
+    if (M - 1 > (INT64_MAX - N) / ldq) return ROWOPS_ERR_UNSUPPORTED;
+    const int es = elem_bytes(dtype);
+    if (group == 0 || group > N) group = N;
+    const size_t rows = rows_bytes(M, N, ld, es), qb = rows_bytes(M, N, ldq, 1);
+    const size_t sb = size_t(M) * size_t((N + group - 1) / group) * 4, wb = size_t(N) * es;
+    if (!q || !scales || !aligned(scales, 4) || !aligned(w, es) || (!res && residual_out))
+        return ROWOPS_ERR_INVALID_VALUE;
+    const Range in[] = {{x, rows}, {residual, rows}, {w, wb}, {residual_out, rows}};
+    for (const Range& r : in)  // q and the scales lie apart from all else
+        if (!apart_from(r, {{q, qb}, {scales, sb}})) return ROWOPS_ERR_INVALID_VALUE;
+    if (!apart(q, qb, scales, sb) || !apart(w, wb, residual_out, rows)) return ROWOPS_ERR_INVALID_VALUE;
+    const Tuning tn = tuning();
+    LaunchCfg cfg;
+    if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
+    QuantArgs a = {x, residual, w, q, residual_out, scales, eps, M, N, ld, ldq, group};
+    const int vec = 16 / es;
+    const bool whole = vector_rows(tn, N, ld, es, {x, residual, residual_out, w}) && ldq % vec == 0 && aligned(q, vec);
+    return finish((dtype == ROWOPS_F32 ? rms_quant_f32() : rms_quant_bf16())(a, whole, cfg));
+}
+
+namespace {
+// elements from the first to behind the last of n strides' multiples and `last` elements
+bool spans(int64_t* total, std::initializer_list<std::pair<int64_t, int64_t>> count_stride, int64_t last) {
+    int64_t t = last;
+    for (const auto& cs : count_stride) {
+        if (cs.first <= 1) continue;
+        if (cs.second > (INT64_MAX / 16 - t) / (cs.first - 1)) return false;
+        t += (cs.first - 1) * cs.second;
+    }
+    *total = t;
+    return true;
+}
+}  // namespace
+
+size_t rowops_paged_attention_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
+                                              rowops_dtype_t dtype) {
+    if (!valid_dtype(dtype) || B < 1 || kv_heads < 1 || heads < 1 || heads % kv_heads != 0 || D < 1 ||
+        D > kPagedMaxD || B > INT32_MAX / heads)
+        return 0;
+    return paged_bytes(B, heads, kv_heads, D);
+}
+
+rowops_status_t rowops_paged_attention(const void* q, const void* k, const void* v, const int32_t* page_table,
+                                       const int32_t* lengths, void* out, float* lse, float scale, int64_t window,
+                                       int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t ldq, int64_t ldo,
+                                       int64_t pages, int64_t page, int64_t page_stride, int64_t slot_stride,
+                                       int64_t head_stride, int64_t max_pages, int64_t ldt, rowops_dtype_t dtype,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!valid_dtype(dtype) || B < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || D < 1 || pages < 0 ||
+        page < 1 || max_pages < 0 || ldt < max_pages || window < 0 || !std::isfinite(scale) || page_stride < 0 ||
+        slot_stride < 0 || head_stride < 0)
+        return ROWOPS_ERR_INVALID_VALUE;
+    if (D > kPagedMaxD || heads > INT32_MAX / D || B > INT32_MAX / heads || page > INT32_MAX || pages > INT32_MAX ||
+        max_pages > INT32_MAX)
+        return ROWOPS_ERR_UNSUPPORTED;
+    if (ldq < heads * D || ldo < heads * D) return ROWOPS_ERR_INVALID_VALUE;
+    if (B == 0) return ROWOPS_OK;
+    const int es = elem_bytes(dtype);
+    int64_t qn, on, cn, tn_;
+    if (!spans(&qn, {{B, ldq}}, heads * D) || !spans(&on, {{B, ldo}}, heads * D) || !spans(&tn_, {{B, ldt}}, max_pages) ||
+        !spans(&cn, {{pages, page_stride}, {page, slot_stride}, {kv_heads, head_stride}}, D))
+        return ROWOPS_ERR_UNSUPPORTED;
+    if (pages == 0) cn = 0;
+    if (!q || !out || !lengths || (max_pages > 0 && !page_table) || (cn > 0 && (!k || !v)))
+        return ROWOPS_ERR_INVALID_VALUE;
+    for (const void* p : {q, k, v, static_cast<const void*>(out)})
+        if (!aligned(p, es)) return ROWOPS_ERR_INVALID_VALUE;
+    for (const void* p : {static_cast<const void*>(page_table), static_cast<const void*>(lengths),
+                          static_cast<const void*>(lse)})
+        if (!aligned(p, 4)) return ROWOPS_ERR_INVALID_VALUE;
+    const Range o = {out, size_t(on) * es}, l = {lse, size_t(B) * heads * 4};
+    const Range in[] = {{q, size_t(qn) * es}, {k, size_t(cn) * es}, {v, size_t(cn) * es},
+                        {page_table, size_t(tn_) * 4}, {lengths, size_t(B) * 4}};
+    for (const Range& r : in)
+        if (!apart_from(r, {o, l})) return ROWOPS_ERR_INVALID_VALUE;
+    if (!apart(o.p, o.n, l.p, l.n)) return ROWOPS_ERR_INVALID_VALUE;
+    if (const size_t need = paged_bytes(B, heads, kv_heads, D)) {
+        if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ROWOPS_ERR_WORKSPACE;
+        if (!apart_from({workspace, workspace_bytes}, {in[0], in[1], in[2], in[3], in[4], o, l}))
+            return ROWOPS_ERR_INVALID_VALUE;
+    }
+    const Tuning tn = tuning();
+    LaunchCfg cfg;
+    rowops_status_t st = make_cfg(stream, tn, &cfg);
+    if (st != ROWOPS_OK) return st;
+    const PagedArgs a = {q, k, v, page_table, lengths, out, lse, scale, window, B, heads, kv_heads, D, pages, page,
+                         max_pages, ldt, ldq, ldo, page_stride, slot_stride, head_stride};
+    return finish((dtype == ROWOPS_F32 ? paged_attention_f32() : paged_attention_bf16())(a, workspace, cfg));
+}
+
+rowops_status_t rowops_sample(const void* logits, const float* u, const float* temperature, float temperature_all,
+                              const int32_t* top_k, int32_t top_k_all, const float* top_p, float top_p_all,
+                              const float* min_p, float min_p_all, int64_t* token, float* logprob, int64_t M,
+                              int64_t N, int64_t ld, rowops_dtype_t dtype, cudaStream_t stream) {
+    rowops_status_t st = check_rows(logits, logits, M, N, ld, dtype);
+    if (st != ROWOPS_OK) return st;
+    if (!(temperature_all >= 0.f) || top_k_all < 0 || !(top_p_all >= 0.f) || !(min_p_all >= 0.f && min_p_all <= 1.f))
+        return ROWOPS_ERR_INVALID_VALUE;
+    if (N > kSampleMaxN || M > int64_t(1) << 27) return ROWOPS_ERR_UNSUPPORTED;
+    if (M == 0) return ROWOPS_OK;
+    if (!u || !token || !aligned(token, 8)) return ROWOPS_ERR_INVALID_VALUE;
+    const size_t row = size_t(M) * 4;
+    const Range in[] = {{logits, rows_bytes(M, N, ld, elem_bytes(dtype))}, {u, row}, {temperature, row}, {top_k, row},
+                        {top_p, row}, {min_p, row}};
+    for (const Range& r : in)
+        if (!apart_from(r, {{token, 2 * row}, {logprob, row}}) || (&r != in && !aligned(r.p, 4)))
+            return ROWOPS_ERR_INVALID_VALUE;
+    if (!aligned(logprob, 4) || !apart(token, 2 * row, logprob, row)) return ROWOPS_ERR_INVALID_VALUE;
+    LaunchCfg cfg;
+    if ((st = make_cfg(stream, tuning(), &cfg)) != ROWOPS_OK) return st;
+    const SampleArgs a = {logits, u, temperature, top_p, min_p, top_k, temperature_all, top_p_all, min_p_all,
+                          top_k_all, token, logprob, M, ld, int(N)};
+    return finish((dtype == ROWOPS_F32 ? sample_f32() : sample_bf16())(a, cfg));
+}
+
 }  // extern "C"

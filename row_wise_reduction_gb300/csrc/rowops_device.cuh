@@ -185,6 +185,16 @@ struct OpSum {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
 
+// The larger, or NaN where either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+struct OpMaxNan {
+    __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
+};
+
 template <int TPR, class Op>
 __device__ __forceinline__ float group_reduce(float v, float* red, Op op) {
     constexpr int kLanes = TPR < 32 ? TPR : 32;

@@ -431,6 +431,53 @@ GnForwardLaunch gn_forward_bf16(int vec, int act);
 GnBackwardLaunch gn_backward_f32(int vec, int act);
 GnBackwardLaunch gn_backward_bf16(int vec, int act);
 
+// Serving operators. RMSNorm with an 8-bit result: group == N is one scale a row; vec: 16-byte
+// aligned rows of whole vectors, q aligned to a vector's bytes in 8 bits.
+struct QuantArgs {
+    const void *x, *residual, *w;
+    void *q, *residual_out;
+    float* scales;
+    float eps;
+    int64_t M, N, ld, ldq, group;
+};
+using QuantLaunch = cudaError_t (*)(const QuantArgs& a, bool vec, const LaunchCfg& cfg);
+QuantLaunch rms_quant_f32();
+QuantLaunch rms_quant_bf16();
+
+// Attention over a paged cache. Strides in elements.
+constexpr int kPagedMaxD = 256;
+struct PagedArgs {
+    const void *q, *k, *v;
+    const int32_t *table, *lengths;
+    void* out;
+    float* lse;
+    float scale;
+    int64_t window, B, heads, kv_heads, D, pages, page, max_pages, table_ld, ldq, ldo, page_stride, slot_stride,
+        head_stride;
+};
+using PagedLaunch = cudaError_t (*)(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
+inline size_t paged_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+PagedLaunch paged_attention_f32();
+PagedLaunch paged_attention_bf16();
+
+// Sampling: the per-row numbers where given, else the one for all rows. A row is held
+// by a cluster of at most 8 CTAs.
+constexpr int64_t kSampleMaxN = 3 << 17;
+struct SampleArgs {
+    const void* logits;
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t* top_k;
+    float temperature_all, top_p_all, min_p_all;
+    int32_t top_k_all;
+    int64_t* token;
+    float* logprob;
+    int64_t M, ld;
+    int N;
+};
+using SampleLaunch = cudaError_t (*)(const SampleArgs& a, const LaunchCfg& cfg);
+SampleLaunch sample_f32();
+SampleLaunch sample_bf16();
+
 // dynamic shared memory of the row-pipeline kernels
 inline size_t tma_row_bytes(int64_t N, int es) { return size_t((N * es + 127) / 128 * 128); }
 inline size_t tma_ring_smem(int64_t N, int es, int nbuf) { return kTmaRingHeader + size_t(nbuf) * tma_row_bytes(N, es); }

@@ -48,6 +48,10 @@ __all__ = [
     "rowops_router_balance_loss",
     "rowops_router_balance_loss_workspace_bytes",
     "rowops_router_balance_loss_backward",
+    "rowops_rmsnorm_quant",
+    "rowops_paged_attention",
+    "rowops_paged_attention_workspace_bytes",
+    "rowops_sample",
     "rowops_status_string",
     "rowops_reload_tuning",
     "ROWOPS_F32",
@@ -151,6 +155,11 @@ def library() -> ctypes.CDLL:
             ("router_balance_loss", i32,
              [_vp, _vp, i32, _vp, f32, _vp, _vp] + [_i64] * 4 + [i32, _vp, size, _vp]),
             ("router_balance_loss_backward", i32, [_vp] * 4 + [f32, _vp] + [_i64] * 4 + [i32, _vp]),
+            ("rmsnorm_quant", i32, [_vp] * 6 + [f32] + [_i64] * 5 + [i32, _vp]),
+            ("paged_attention_workspace_bytes", size, [_i64] * 4 + [i32]),
+            ("paged_attention", i32, [_vp] * 7 + [f32] + [_i64] * 14 + [i32, _vp, size, _vp]),
+            ("sample", i32, [_vp] * 3 + [f32, _vp, ctypes.c_int32, _vp, f32, _vp, f32] + [_vp] * 2 + [_i64] * 3
+             + [i32, _vp]),
         ):
             f = getattr(L, "rowops_" + name)
             f.restype, f.argtypes = res, args
@@ -159,7 +168,7 @@ def library() -> ctypes.CDLL:
     return _lib
 
 
-_TRAINING = (
+_OPERATORS = (
     "groupnorm_act_workspace_bytes",
     "groupnorm_act",
     "groupnorm_act_backward_workspace_bytes",
@@ -170,6 +179,10 @@ _TRAINING = (
     "router_balance_loss",
     "router_balance_loss_backward",
     "router_balance_loss_workspace_bytes",
+    "rmsnorm_quant",
+    "paged_attention_workspace_bytes",
+    "paged_attention",
+    "sample",
 )
 
 
@@ -178,7 +191,7 @@ class _Calls:
     CPython call module ``_rowops_call`` where it was built (about 0.1 us of
     marshalling per call), else through ctypes (about 2 us)."""
 
-    __slots__ = ("softmax", "layernorm_gelu", "layernorm_gelu_erf", "module") + _TRAINING
+    __slots__ = ("softmax", "layernorm_gelu", "layernorm_gelu_erf", "module") + _OPERATORS
 
 
 _calls: Optional[_Calls] = None
@@ -201,8 +214,8 @@ def _bind_calls(L: ctypes.CDLL) -> None:
         c.softmax, c.layernorm_gelu, c.layernorm_gelu_erf = (L.rowops_softmax, L.rowops_layernorm_gelu,
                                                               L.rowops_layernorm_gelu_erf)
     if fast is not None:
-        fast.bind_training(*(addr(getattr(L, "rowops_" + n)) for n in _TRAINING))
-    for n in _TRAINING:
+        fast.bind_operators(*(addr(getattr(L, "rowops_" + n)) for n in _OPERATORS))
+    for n in _OPERATORS:
         setattr(c, n, getattr(L, "rowops_" + n) if fast is None else getattr(fast, n))
     c.module = fast
     _calls = c
@@ -954,3 +967,194 @@ def rowops_router_balance_loss_backward(
     if st:
         raise RowopsError("rowops_router_balance_loss_backward", st)
     return dlogits
+
+
+# ---------------------------------------------------------------------------
+# Serving operators: RMSNorm with an 8-bit result, attention of one new token
+# over a paged cache, sampling. Devices and streams as for the training operators.
+# ---------------------------------------------------------------------------
+_E4M3 = torch.float8_e4m3fn
+
+
+def rowops_rmsnorm_quant(
+    x: torch.Tensor,
+    residual: Optional[torch.Tensor] = None,
+    w: Optional[torch.Tensor] = None,
+    eps: float = 1e-5,
+    group: int = 0,
+    q: Optional[torch.Tensor] = None,
+    scales: Optional[torch.Tensor] = None,
+    residual_out: Optional[torch.Tensor] = None,
+    *,
+    stream=None,
+):
+    """RMSNorm of ``x`` (+ ``residual``) in 8 bits: ``(q, scales, residual_out)`` with
+    q float8_e4m3fn (M, N), scales float32 (M, groups), one for every ``group``
+    columns (a multiple of 32; 0: one a row), so that the norm is about q * scale,
+    and residual_out = x + residual (None without a residual), which may be ``x``
+    or ``residual`` themselves. A given ``q`` may have a row stride of its own."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(rowops_rmsnorm_quant, stream, dev, x, residual, w, eps, group, q, scales, residual_out)
+    M, N, ld = _rows(x, "x")
+    code = _dtype_code(x)
+    pr = po = None
+    if residual is not None:
+        _out_like(x, residual)  # same shape, dtype, device and row stride
+        residual_out = _out_like(x, residual_out)
+        pr, po = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out is given but residual is not")
+    groups = 1 if group <= 0 else -(-N // group)
+    if q is None:
+        q = torch.empty(M, N, dtype=_E4M3, device=x.device)
+        ldq = N
+    else:
+        if q.dtype is not _E4M3 or q.shape != x.shape or q.get_device() != dev or (N > 1 and q.stride(1) != 1):
+            raise ValueError("q must be a float8_e4m3fn CUDA tensor of x's shape with unit column stride")
+        ldq = q.stride(0) if M > 1 else max(N, q.stride(0))
+    if scales is None:
+        scales = torch.empty(M, groups, dtype=torch.float32, device=x.device)
+    elif scales.numel() != M * groups:
+        raise ValueError("scales must have M * ceil(N / group) entries")
+    st = (_calls or _hot_calls()).rmsnorm_quant(
+        x.data_ptr(), pr, q.data_ptr(), _floats(scales, M * groups, dev, "scales").data_ptr(), po,
+        _affine(w, x, N, dev, "w"), eps, M, N, ld, ldq, group, code, _current_raw_stream(dev))
+    if st:
+        raise RowopsError("rowops_rmsnorm_quant", st)
+    return q, scales, residual_out
+
+
+def _heads(t: torch.Tensor, name: str):
+    """(B, heads, D, stride of a sequence) of a (B, heads, D) tensor, head after head."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D (sequences, heads, D)")
+    B, H, D = t.shape
+    sb, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}'s heads must follow one another")
+    return B, H, D, (sb if B > 1 else max(H * D, sb))
+
+
+def _indices(t: torch.Tensor, dev: int, name: str) -> torch.Tensor:
+    if t.dtype is not torch.int32 or t.get_device() != dev:
+        raise ValueError(f"{name} must be an int32 CUDA tensor on the device of the call's tensors")
+    return t
+
+
+def rowops_paged_attention_workspace_bytes(B: int, heads: int, kv_heads: int, D: int, dtype: torch.dtype) -> int:
+    return int(library().rowops_paged_attention_workspace_bytes(B, heads, kv_heads, D, _DTYPE_CODES.get(dtype, -1)))
+
+
+def rowops_paged_attention(
+    q: torch.Tensor,
+    k_cache: torch.Tensor,
+    v_cache: torch.Tensor,
+    page_table: torch.Tensor,
+    lengths: torch.Tensor,
+    scale: Optional[float] = None,
+    window: int = 0,
+    out: Optional[torch.Tensor] = None,
+    lse: Optional[torch.Tensor] = None,
+    *,
+    workspace: Optional[torch.Tensor] = None,
+    stream=None,
+) -> torch.Tensor:
+    """Attention of one new token a sequence, ``q`` (B, heads, D), over paged caches
+    ``k_cache``, ``v_cache`` (pages, slots, kv_heads, D) (any strides, the same in both,
+    with unit stride in D). ``page_table`` int32 (B, max_pages) names the pages of a
+    sequence's positions in turn, ``lengths`` int32 (B,) its positions, the new token's
+    among them. ``scale``: 1 / sqrt(D) when None; ``window``: only that many last
+    positions (0: all); ``lse``: a float32 (B, heads) tensor that takes the logarithm of
+    the sum of exponentials. ``workspace``: a CUDA tensor of at least
+    ``rowops_paged_attention_workspace_bytes(...)`` bytes, allocated per call when
+    omitted."""
+    dev = q.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(rowops_paged_attention, stream, dev, q, k_cache, v_cache, page_table, lengths, scale, window,
+                          out, lse, workspace=workspace)
+    B, H, D, ldq = _heads(q, "q")
+    code = _dtype_code(q)
+    ks = k_cache.shape
+    if len(ks) != 4 or ks != v_cache.shape or ks[3] != D:
+        raise ValueError("k_cache and v_cache must both be (pages, slots, kv_heads, D)")
+    if (k_cache.dtype is not q.dtype or v_cache.dtype is not q.dtype or k_cache.get_device() != dev
+            or v_cache.get_device() != dev):
+        raise ValueError("k_cache and v_cache must match q in dtype and device")
+    kt, vt = k_cache.stride(), v_cache.stride()
+    if kt != vt and any(n > 1 and a != b for n, a, b in zip(ks, kt, vt)):
+        raise ValueError("k_cache and v_cache must share their strides")
+    if D > 1 and kt[3] != 1:
+        raise ValueError("k_cache and v_cache must have unit stride in D")
+    if page_table.dim() != 2 or page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be (B, max_pages) with unit column stride")
+    if lengths.shape != (B,) or not lengths.is_contiguous():
+        raise ValueError("lengths must be a contiguous (B,) tensor")
+    width = page_table.shape[1]
+    if out is None:
+        out = torch.empty(B, H, D, dtype=q.dtype, device=q.device)
+        ldo = H * D
+    else:
+        if out.dtype is not q.dtype or out.shape != q.shape or out.get_device() != dev:
+            raise ValueError("out must match q in shape, dtype and device")
+        ldo = _heads(out, "out")[3]
+    L = _calls or _hot_calls()
+    ws, wp, wn = _scratch(workspace, L.paged_attention_workspace_bytes(B, H, ks[2], D, code), dev)
+    st = L.paged_attention(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _indices(page_table, dev, "page_table").data_ptr(),
+        _indices(lengths, dev, "lengths").data_ptr(), out.data_ptr(),
+        None if lse is None else _floats(lse, B * H, dev, "lse").data_ptr(), D ** -0.5 if scale is None else scale,
+        window, B, H, ks[2], D, ldq, ldo, ks[0], ks[1], kt[0], kt[1], kt[2], width,
+        page_table.stride(0) if B > 1 else max(width, page_table.stride(0)), code, wp, wn, _current_raw_stream(dev))
+    if st:
+        raise RowopsError("rowops_paged_attention", st)
+    return out
+
+
+def _knob(v, M: int, dtype: torch.dtype, dev: int, name: str):
+    """(device pointer, number) of a number for every row or one a row."""
+    if isinstance(v, torch.Tensor):
+        if v.dtype is not dtype or v.shape != (M,) or not v.is_contiguous() or v.get_device() != dev:
+            raise ValueError(f"{name} must be a number or a contiguous {dtype} CUDA tensor of one entry a row")
+        return v.data_ptr(), 0
+    return None, v
+
+
+def rowops_sample(
+    logits: torch.Tensor,
+    u: torch.Tensor,
+    temperature=1.0,
+    top_k=0,
+    top_p=1.0,
+    min_p=0.0,
+    token: Optional[torch.Tensor] = None,
+    logprob: Optional[torch.Tensor] = None,
+    *,
+    stream=None,
+) -> torch.Tensor:
+    """One token a row of ``logits`` (M, N), drawn with the uniform numbers ``u``
+    (float32 (M,), in [0, 1)): int64 (M,). ``temperature`` (0: the maximum), ``top_k``
+    (0: off), ``top_p`` (1: off; of what top-k keeps) and ``min_p`` (0: off; of the
+    maximum's weight) are numbers, or tensors of one entry a row (float32; top_k int32).
+    ``logprob``: a float32 (M,) tensor that takes the tokens' log-probabilities among
+    what is kept. A row with a NaN, or of -inf alone, gives -1."""
+    dev = logits.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(rowops_sample, stream, dev, logits, u, temperature, top_k, top_p, min_p, token, logprob)
+    M, N, ld = _rows(logits, "logits")
+    f32 = torch.float32
+    if u.dtype is not f32 or u.shape != (M,) or not u.is_contiguous() or u.get_device() != dev:
+        raise ValueError("u must be a contiguous float32 CUDA tensor of one entry a row")
+    if token is None:
+        token = torch.empty(M, dtype=torch.int64, device=logits.device)
+    elif token.dtype is not torch.int64 or token.shape != (M,) or not token.is_contiguous() or token.get_device() != dev:
+        raise ValueError("token must be a contiguous int64 CUDA tensor of one entry a row")
+    st = (_calls or _hot_calls()).sample(
+        logits.data_ptr(), u.data_ptr(), *_knob(temperature, M, f32, dev, "temperature"),
+        *_knob(top_k, M, torch.int32, dev, "top_k"), *_knob(top_p, M, f32, dev, "top_p"),
+        *_knob(min_p, M, f32, dev, "min_p"), token.data_ptr(),
+        None if logprob is None else _floats(logprob, M, dev, "logprob").data_ptr(), M, N, ld, _dtype_code(logits),
+        _current_raw_stream(dev))
+    if st:
+        raise RowopsError("rowops_sample", st)
+    return token
