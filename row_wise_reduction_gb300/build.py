@@ -54,7 +54,10 @@ SOURCES = [
     "dropout.cu",
     "router_balance.cu",
     "norm_quant.cu",
-    "paged_attention.cu",
+    "paged_bf16.cu",
+    "paged_f32_g1.cu",
+    "paged_f32_g4.cu",
+    "paged_f32_g8.cu",
     "sample.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

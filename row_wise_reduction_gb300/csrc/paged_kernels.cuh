@@ -1,0 +1,386 @@
+// Attention of one new token a sequence over a paged key-value cache:
+//   s_j = scale q k_j;  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+// over the positions j in [first, n) of a sequence; position j is slot j mod page of the
+// page that the sequence's table names for j / page. One pass with a running maximum
+// and sum, as the split-row online softmax has, and the weighted values beside them.
+//
+// Bound by the cache's traffic: every key and value attended to is read once, for all
+// heads that share it. The work is a line of tiles: for every sequence, key head
+// and block of its heads (a unit), the unit's positions in tiles. The persistent grid's
+// CTAs take equal stretches of that line, whatever the lengths are: a unit that lies within a stretch is written
+// out at once, of one that crosses a border each CTA leaves its part (maximum, sum, weighted
+// values) in the workspace, and a second kernel joins them, in order. Which CTA has
+// which tiles follows from the lengths alone, so equal calls give equal bits.
+//
+// Within a CTA a warp takes every fourth piece of a tile by itself: it copies the piece's keys
+// and values into a ring of its own in shared memory, several pieces ahead and across
+// units, so no barrier stands in the loop; the warps meet at a unit's end only.
+#pragma once
+
+#include "async_ring.cuh"
+#include "rowops_device.cuh"
+#include "rowops_launch.h"
+
+namespace rowops {
+
+constexpr int kPagedWarps = 4, kPagedBlock = 32 * kPagedWarps;
+
+// A warp's ring: pieces of TOKENS positions, their keys, then their values. Rows lie an odd number
+// of 16-byte vectors apart, so eight rows' vectors lie in different banks.
+template <typename T, int DT, int TOKENS>
+struct PagedRing {
+    static constexpr int kPitch = (DT * int(sizeof(T)) / 16 | 1) * 16;
+    static constexpr int kPart = TOKENS * kPitch;                 // keys, or values
+    static constexpr int kStep = 2 * kPart * kPagedWarps;         // of the CTA
+    static constexpr int kHalf = 104448;                          // what lets two CTAs share an SM
+    static constexpr bool kTwo = kHalf / kStep >= 2;
+    static constexpr int kStages = !kTwo ? 3 : kHalf / kStep > 6 ? 6 : kHalf / kStep;
+    static constexpr int kBytes = kStep * kStages;
+};
+
+// The tiles of one unit of sequence b, which attends to the positions [first, n); they
+// count from `base`.
+template <int TILE>
+__device__ __forceinline__ uint32_t paged_span(const PagedArgs& a, int b, uint32_t* n, uint32_t* first, uint32_t* base) {
+    const int asked = a.lengths[b];
+    const int64_t room = a.max_pages * a.page;
+    *n = asked <= 0 ? 0u : asked < room ? uint32_t(asked) : uint32_t(room);
+    *first = a.window > 0 && *n > a.window ? *n - uint32_t(a.window) : 0u;
+    *base = *first & ~15u;
+    return (*n - *base + TILE - 1) / TILE;
+}
+__device__ __forceinline__ bool paged_beyond(const PagedArgs& a, int b) { return a.lengths[b] > a.max_pages * a.page; }
+
+// The tiles of single units over all sequences, and over those before b. `red`: two int64 a
+// warp. Every thread of the CTA calls it.
+template <int TILE>
+__device__ __forceinline__ void paged_count(const PagedArgs& a, int b, int64_t* red, int64_t* total, int64_t* before) {
+    constexpr int THREADS = kPagedBlock;
+    int64_t all = 0, some = 0;
+    uint32_t n, f, base;
+    for (int i = threadIdx.x; i < a.B; i += THREADS) {
+        const uint32_t t = paged_span<TILE>(a, i, &n, &f, &base);
+        all += t;
+        if (i < b) some += t;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        some += __shfl_xor_sync(0xffffffffu, some, o);
+    }
+    if ((threadIdx.x & 31) == 0) red[2 * (threadIdx.x >> 5)] = all, red[2 * (threadIdx.x >> 5) + 1] = some;
+    __syncthreads();
+    all = some = 0;
+    for (int i = 0; i < THREADS / 32; ++i) all += red[2 * i], some += red[2 * i + 1];
+    *total = all;
+    *before = some;
+}
+
+// CTA c's stretch [begin, end) of the line's `total` tiles, the sequence that it begins in, and
+// the tiles of single units of the sequences before that. `sum`: kPagedWarps int64. Every
+// thread of the CTA calls it.
+template <int TILE>
+__device__ __forceinline__ void paged_find(const PagedArgs& a, int units, int64_t* sum, int64_t* total, int c, int ctas,
+                                           int64_t* begin, int64_t* end, int* b, int64_t* before) {
+    // thread i counts the sequences [i * each, (i + 1) * each)
+    const int each = int((a.B + kPagedBlock - 1) / kPagedBlock), i0 = threadIdx.x * each;
+    int64_t mine = 0;
+    uint32_t n, f, base;
+    for (int i = i0; i < i0 + each && i < a.B; ++i) mine += paged_span<TILE>(a, i, &n, &f, &base);
+    int64_t run = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t other = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += other;
+    }
+    if (lane == 31) sum[warp] = run;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int i = 0; i < kPagedWarps; ++i) {
+        if (i < warp) run += sum[i];
+        all += sum[i];
+    }
+    __syncthreads();
+    *total = all * units;
+    if (ctas > *total) ctas = int(*total);  // every CTA that has a stretch has a tile
+    *begin = c < ctas ? *total * c / ctas : 0;
+    *end = c < ctas ? *total * (c + 1) / ctas : 0;
+    const int64_t at = *begin / units;  // in tiles of single units
+    if (at >= run - mine && at < run) {
+        int64_t p = run - mine;
+        int i = i0;
+        for (;; ++i) {
+            const int64_t t = paged_span<TILE>(a, i, &n, &f, &base);
+            if (at < p + t) break;
+            p += t;
+        }
+        sum[0] = i;
+        sum[1] = p;
+    }
+    __syncthreads();
+    *b = *begin < *end ? int(sum[0]) : 0;
+    *before = sum[1];
+    __syncthreads();
+}
+
+// A place in the line of tiles.
+template <int TILE>
+struct PagedCursor {
+    const PagedArgs& a;
+    int units, b, j;
+    uint32_t n, first, base, tile, tiles;
+    int64_t left;
+    __device__ __forceinline__ PagedCursor(const PagedArgs& a_, int units_, int b_, int64_t in_sequence, int64_t left_)
+        : a(a_), units(units_), b(b_), left(left_) {
+        j = 0, tile = 0, tiles = 1, n = first = base = 0;
+        if (left > 0) {
+            tiles = paged_span<TILE>(a, b, &n, &first, &base);
+            j = int(in_sequence / tiles);
+            tile = uint32_t(in_sequence - int64_t(j) * tiles);
+        }
+    }
+    __device__ __forceinline__ void next() {
+        if (--left <= 0) return;
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++j < units) return;
+        j = 0;
+        do {
+            tiles = paged_span<TILE>(a, ++b, &n, &first, &base);
+        } while (tiles == 0);  // (the stretch has tiles left, so there is a sequence with some)
+    }
+};
+
+// What a unit's part is in the workspace: rows of DT weighted values, then a maximum and a sum each.
+template <int DT, int ROWS>
+__device__ __forceinline__ constexpr int paged_part_floats() {
+    return ROWS * (DT + 2);
+}
+
+template <class P>
+__global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
+    paged_attention_kernel(const __grid_constant__ PagedArgs a, float* parts, int blocks, bool whole) {
+    using T = typename P::T;
+    using E = Elem<T>;
+    using Ring = typename P::Ring;
+    constexpr int TK = P::kTokens, TILE = TK * kPagedWarps, S = Ring::kStages, DT = P::kD, ROWS = P::kRows;
+    extern __shared__ uint4 smem[];
+    char* ring = reinterpret_cast<char*>(smem) + (threadIdx.x >> 5) * (2 * Ring::kPart) * S;
+    float* joined = reinterpret_cast<float*>(reinterpret_cast<char*>(smem) + Ring::kBytes);  // [ROWS][DT]
+    float* scratch = joined + ROWS * DT;                                                     // P's own
+    __shared__ float tops[kPagedWarps][ROWS], sums[kPagedWarps][ROWS];
+    __shared__ int64_t found[kPagedBlock / 32 * 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units = int(a.kv_heads) * blocks;
+    const int group = int(a.heads / a.kv_heads);
+
+    let_next_start();
+    int64_t total, begin, end, before;
+    int b;
+    paged_find<TILE>(a, units, found, &total, blockIdx.x, gridDim.x, &begin, &end, &b, &before);
+    if (begin >= end) return;
+
+    // columns past D stay zero: nothing is copied there
+    if (a.D < DT)
+        for (int i = lane; i < S * 2 * Ring::kPart / 16; i += 32)
+            reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+
+    PagedCursor<TILE> in(a, units, b, begin - before * units, end - begin), at = in;
+    uint32_t bad = 0;  // ring slots with a position whose page is none
+    int page = 0;
+    auto look = [&] {  // the page of this lane's position in the piece to come
+        const uint32_t t = in.base + in.tile * TILE + warp * TK + lane;
+        if (in.left > 0 && lane < TK && t >= in.first && t < in.n)
+            page = a.table[int64_t(in.b) * a.table_ld + t / uint32_t(a.page)];
+    };
+    auto ask = [&](int slot) {
+        if (in.left > 0) {
+            const uint32_t t = in.base + in.tile * TILE + warp * TK + lane;
+            const bool live = lane < TK && t >= in.first && t < in.n, there = live && page >= 0 && page < a.pages;
+            int64_t off = -1;
+            if (there)
+                off = page * a.page_stride + int64_t(t % uint32_t(a.page)) * a.slot_stride +
+                      int64_t(in.j / blocks) * a.head_stride;
+            bad = __any_sync(0xffffffffu, live && !there) ? bad | 1u << slot : bad & ~(1u << slot);
+            char* to = ring + slot * 2 * Ring::kPart;
+            if (whole) {
+                constexpr int kRow = DT * int(sizeof(T)) / 16, kLanes = kRow > 16 ? 32 : kRow > 8 ? 16 : 8;
+                const int r0 = lane / kLanes, v = lane % kLanes, vectors = int(a.D) / E::kVec;
+#pragma unroll
+                for (int r = 0; r < TK; r += 32 / kLanes) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off, r + r0);
+#pragma unroll
+                    for (int i = 0; i < kRow; i += kLanes)
+                        if (v + i < vectors) {
+                            char* k = to + (r + r0) * Ring::kPitch + (v + i) * 16;
+                            const int64_t from = (o < 0 ? 0 : o) + (v + i) * E::kVec;
+                            copy_async_part(k, static_cast<const T*>(a.k) + from, o < 0 ? 0u : 16u);
+                            copy_async_part(k + Ring::kPart, static_cast<const T*>(a.v) + from, o < 0 ? 0u : 16u);
+                        }
+                }
+            } else {
+                for (int r = 0; r < TK; ++r) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                    T* k = reinterpret_cast<T*>(to + r * Ring::kPitch);
+                    T* v = reinterpret_cast<T*>(to + r * Ring::kPitch + Ring::kPart);
+                    for (int d = lane; d < a.D; d += 32) {
+                        k[d] = o < 0 ? T{} : static_cast<const T*>(a.k)[o + d];
+                        v[d] = o < 0 ? T{} : static_cast<const T*>(a.v)[o + d];
+                    }
+                }
+            }
+            in.next();
+            look();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look();
+    for (int s = 0; s < S; ++s) ask(s);
+
+    P p(scratch);
+    const float scale = a.scale * kLog2eF;
+    bool fresh = true, cut = at.tile != 0;  // a unit begins; it began in another CTA
+    for (int slot = 0; at.left > 0; slot = slot + 1 == S ? 0 : slot + 1) {
+        const int head = at.j / blocks * group + at.j % blocks * ROWS;  // the unit's first
+        const int rows = min(ROWS, group - at.j % blocks * ROWS);
+        if (fresh) p.begin(static_cast<const T*>(a.q) + at.b * a.ldq + int64_t(head) * a.D, rows, int(a.D));
+        fresh = false;
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        __syncwarp();
+        const uint32_t t0 = at.base + at.tile * TILE + warp * TK;
+        const char* k = ring + slot * 2 * Ring::kPart;
+        p.step(k, k + Ring::kPart, int(at.first) - int(t0), int(at.n) - int(t0), scale);
+        if (bad >> slot & 1) p.spoil();
+        __syncwarp();
+        ask(slot);
+        const bool done = at.tile + 1 == at.tiles;
+        if (done || at.left == 1) {
+            // the unit's end, or the stretch's: the warps' sums become one
+            p.tell(tops[warp], sums[warp]);
+            __syncthreads();
+            float top[P::kOwn], factor[P::kOwn];
+#pragma unroll
+            for (int i = 0; i < P::kOwn; ++i) {
+                const int r = p.row(i);
+                top[i] = tops[0][r];
+                for (int w = 1; w < kPagedWarps; ++w) top[i] = fmaxf(top[i], tops[w][r]);
+                factor[i] = top[i] == -INFINITY ? 0.f : ex2_approx(tops[warp][r] - top[i]);
+            }
+            for (int w = 0; w < kPagedWarps; ++w) {
+                if (warp == w) p.add(joined, factor, w == 0);
+                __syncthreads();
+            }
+            const bool part = cut || !done;
+            // a CTA leaves two at most: of the unit that it begins in the middle of, and of that which it ends in
+            float* out = parts + (int64_t(blockIdx.x) * 2 + !cut) * paged_part_floats<DT, ROWS>();
+            for (int r = warp; r < rows; r += kPagedWarps) {
+                float m = tops[0][r], l = 0.f;
+                for (int w = 1; w < kPagedWarps; ++w) m = fmaxf(m, tops[w][r]);
+                for (int w = 0; w < kPagedWarps; ++w)
+                    l += m == -INFINITY ? sums[w][r] : sums[w][r] * ex2_approx(tops[w][r] - m);
+                if (part) {
+                    for (int d = lane; d < DT; d += 32) out[r * DT + d] = joined[r * DT + d];
+                    if (lane == 0) out[ROWS * DT + 2 * r] = m, out[ROWS * DT + 2 * r + 1] = l;
+                } else {
+                    if (paged_beyond(a, at.b)) l = NAN;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    T* o = static_cast<T*>(a.out) + at.b * a.ldo + int64_t(head + r) * a.D;
+                    for (int d = lane; d < a.D; d += 32) E::store(o + d, joined[r * DT + d] * inv);
+                    if (lane == 0 && a.lse)
+                        a.lse[at.b * a.heads + head + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+                }
+            }
+            cut = false;
+            fresh = true;
+            __syncthreads();
+        }
+        at.next();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The units that no CTA has written: those cut by a border, joined from their parts in
+// order, and those without a position. CTA (x, y): sequence x, every gridDim.y-th unit.
+template <class P>
+__global__ void __launch_bounds__(kPagedBlock) paged_join_kernel(const __grid_constant__ PagedArgs a, const float* parts,
+                                                                 int blocks, int ctas) {
+    using T = typename P::T;
+    using E = Elem<T>;
+    constexpr int TILE = P::kTokens * kPagedWarps, DT = P::kD, ROWS = P::kRows;
+    __shared__ int64_t red[kPagedWarps * 2];
+    const int b = blockIdx.x, units = int(a.kv_heads) * blocks, group = int(a.heads / a.kv_heads);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t total, before;
+    paged_count<TILE>(a, b, red, &total, &before);
+    total *= units;
+    if (ctas > total) ctas = int(total);
+    uint32_t n, first, base;
+    const int64_t tiles = paged_span<TILE>(a, b, &n, &first, &base);
+    const bool beyond = paged_beyond(a, b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int j = blockIdx.y; j < units; j += gridDim.y) {
+        // tile t is CTA c's where total c / ctas <= t < total (c + 1) / ctas, rounded down
+        const int64_t t0 = before * units + j * tiles, t1 = t0 + tiles - 1;
+        const int c0 = tiles ? int(((t0 + 1) * ctas - 1) / total) : 0, c1 = tiles ? int(((t1 + 1) * ctas - 1) / total) : 0;
+        if (tiles && c0 == c1) continue;
+        const int head = j / blocks * group + j % blocks * ROWS, rows = min(ROWS, group - j % blocks * ROWS);
+        for (int r = warp; r < rows; r += kPagedWarps) {
+            float m = -INFINITY, l = 0.f, acc[(DT + 31) / 32] = {};
+            if (tiles)
+                for (int c = c0; c <= c1; ++c) {
+                    const float* part = parts + (int64_t(c) * 2 + (c == c0)) * paged_part_floats<DT, ROWS>();
+                    const float pm = part[ROWS * DT + 2 * r], pl = part[ROWS * DT + 2 * r + 1];
+                    const float next = fmaxf(m, pm), zero = next == -INFINITY ? 0.f : next;
+                    const float keep = ex2_approx(m - zero), take = ex2_approx(pm - zero);
+                    l = l * keep + (pm == -INFINITY ? pl : pl * take);
+#pragma unroll
+                    for (int i = 0; i < (DT + 31) / 32; ++i)
+                        if (i * 32 + lane < DT) acc[i] = acc[i] * keep + part[r * DT + i * 32 + lane] * take;
+                    m = next;
+                }
+            if (beyond) l = NAN;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            T* o = static_cast<T*>(a.out) + b * a.ldo + int64_t(head + r) * a.D;
+#pragma unroll
+            for (int i = 0; i < (DT + 31) / 32; ++i)
+                if (i * 32 + lane < a.D) E::store(o + i * 32 + lane, acc[i] * inv);
+            if (lane == 0 && a.lse) a.lse[b * a.heads + head + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+        }
+    }
+}
+
+template <class P>
+cudaError_t paged_launch(const PagedArgs& a, void* workspace, int blocks, const LaunchCfg& cfg) {
+    constexpr int TILE = P::kTokens * kPagedWarps;
+    const int V = 16 / int(sizeof(typename P::T));
+    auto even = [&](int64_t count, int64_t stride) { return count <= 1 || stride % V == 0; };
+    const bool whole = a.D % V == 0 && even(a.pages, a.page_stride) && even(a.page, a.slot_stride) &&
+                       even(a.kv_heads, a.head_stride) && reinterpret_cast<uintptr_t>(a.k) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.v) % 16 == 0;
+    const int64_t units = a.kv_heads * blocks, room = a.max_pages * a.page,
+                  most = a.window > 0 ? std::min(room, a.window + 15) : room;
+    const int64_t tiles = std::min<int64_t>((most + TILE - 1) / TILE * units, 1 << 20) * a.B;
+    const size_t smem = P::Ring::kBytes + size_t(P::kRows) * P::kD * 4 + P::kScratch;
+    auto k = paged_attention_kernel<P>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, cfg);
+    if (e != cudaSuccess) return e;
+    LaunchCfg one = cfg;
+    one.ctas_per_sm = 0;
+    const int ctas = std::min(grid_for(reinterpret_cast<const void*>(k), kPagedBlock, smem, tiles, one), kPagedMaxCtas);
+    k<<<ctas, kPagedBlock, smem, cfg.stream>>>(a, static_cast<float*>(workspace), blocks, whole);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(a.B), unsigned(std::min<int64_t>(units, std::max<int64_t>(1, 2048 / a.B))));
+    lc.blockDim = dim3(kPagedBlock);
+    lc.stream = cfg.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, paged_join_kernel<P>, a, static_cast<const float*>(workspace), blocks, ctas);
+}
+
+}  // namespace rowops

@@ -1454,7 +1454,7 @@ size_t rowops_paged_attention_workspace_bytes(int64_t B, int64_t heads, int64_t 
     if (!valid_dtype(dtype) || B < 1 || kv_heads < 1 || heads < 1 || heads % kv_heads != 0 || D < 1 ||
         D > kPagedMaxD || B > INT32_MAX / heads)
         return 0;
-    return paged_bytes(B, heads, kv_heads, D);
+    return paged_bytes(heads / kv_heads, D, elem_bytes(dtype));
 }
 
 rowops_status_t rowops_paged_attention(const void* q, const void* k, const void* v, const int32_t* page_table,
@@ -1468,7 +1468,7 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
         slot_stride < 0 || head_stride < 0)
         return ROWOPS_ERR_INVALID_VALUE;
     if (D > kPagedMaxD || heads > INT32_MAX / D || B > INT32_MAX / heads || page > INT32_MAX || pages > INT32_MAX ||
-        max_pages > INT32_MAX)
+        max_pages > (INT32_MAX - 255) / page)
         return ROWOPS_ERR_UNSUPPORTED;
     if (ldq < heads * D || ldo < heads * D) return ROWOPS_ERR_INVALID_VALUE;
     if (B == 0) return ROWOPS_OK;
@@ -1491,18 +1491,21 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
     for (const Range& r : in)
         if (!apart_from(r, {o, l})) return ROWOPS_ERR_INVALID_VALUE;
     if (!apart(o.p, o.n, l.p, l.n)) return ROWOPS_ERR_INVALID_VALUE;
-    if (const size_t need = paged_bytes(B, heads, kv_heads, D)) {
-        if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ROWOPS_ERR_WORKSPACE;
-        if (!apart_from({workspace, workspace_bytes}, {in[0], in[1], in[2], in[3], in[4], o, l}))
-            return ROWOPS_ERR_INVALID_VALUE;
-    }
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < paged_bytes(heads / kv_heads, D, es))
+        return ROWOPS_ERR_WORKSPACE;
+    if (!apart_from({workspace, workspace_bytes}, {in[0], in[1], in[2], in[3], in[4], o, l}))
+        return ROWOPS_ERR_INVALID_VALUE;
     const Tuning tn = tuning();
     LaunchCfg cfg;
     rowops_status_t st = make_cfg(stream, tn, &cfg);
     if (st != ROWOPS_OK) return st;
     const PagedArgs a = {q, k, v, page_table, lengths, out, lse, scale, window, B, heads, kv_heads, D, pages, page,
                          max_pages, ldt, ldq, ldo, page_stride, slot_stride, head_stride};
-    return finish((dtype == ROWOPS_F32 ? paged_attention_f32() : paged_attention_bf16())(a, workspace, cfg));
+    const int rows = paged_rows(heads / kv_heads, es);
+    return finish((rows == 16  ? paged_attention_bf16
+                   : rows == 8 ? paged_attention_f32_g8
+                   : rows == 4 ? paged_attention_f32_g4
+                               : paged_attention_f32_g1)(a, workspace, cfg));
 }
 
 rowops_status_t rowops_sample(const void* logits, const float* u, const float* temperature, float temperature_all,

@@ -455,10 +455,23 @@ struct PagedArgs {
     int64_t window, B, heads, kv_heads, D, pages, page, max_pages, table_ld, ldq, ldo, page_stride, slot_stride,
         head_stride;
 };
-using PagedLaunch = cudaError_t (*)(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
-inline size_t paged_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
-PagedLaunch paged_attention_f32();
-PagedLaunch paged_attention_bf16();
+// At most kPagedMaxCtas CTAs (three a SM), each of which leaves two parts: for a block of heads their
+// weighted values, a maximum and a sum each, D rounded up to one of the kernels' widths.
+constexpr int kPagedMaxCtas = 3 * 152;
+constexpr int kPagedWidths[] = {64, 80, 96, 128, 160, 192, 256};
+inline int paged_width(int64_t D) {
+    for (int w : kPagedWidths)
+        if (D <= w) return w;
+    return 0;
+}
+inline int paged_rows(int64_t group, int es) { return es == 2 ? 16 : group > 4 ? 8 : group > 1 ? 4 : 1; }
+inline size_t paged_bytes(int64_t group, int64_t D, int es) {
+    return size_t(kPagedMaxCtas) * 2 * paged_rows(group, es) * (paged_width(D) + 2) * 4;
+}
+cudaError_t paged_attention_bf16(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
+cudaError_t paged_attention_f32_g1(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
+cudaError_t paged_attention_f32_g4(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
+cudaError_t paged_attention_f32_g8(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
 
 // Sampling: the per-row numbers where given, else the one for all rows. A row is held
 // by a cluster of at most 8 CTAs.
