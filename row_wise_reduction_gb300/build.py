@@ -53,7 +53,8 @@ SOURCES = [
     "groupnorm_bf16.cu",
     "dropout.cu",
     "router_balance.cu",
-    "norm_quant.cu",
+    "norm_quant_f32.cu",
+    "norm_quant_bf16.cu",
     "paged_bf16.cu",
     "paged_f32_g1.cu",
     "paged_f32_g4.cu",

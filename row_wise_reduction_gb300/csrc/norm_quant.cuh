@@ -1,0 +1,377 @@
+// RMSNorm (with the residual's addition) and its result in 8 bits with scales:
+//   s = x + residual as the I/O type stores it;  y = s w / sqrt(mean(s^2) + eps)
+//   scale = max(max|y| / 448, 2^-126) over a row or `group` columns;  q = e4m3(y / scale)
+// y itself is never rounded nor stored: with inv = 1 / sqrt(...), max|y| = inv max|s w|,
+// so the sum of squares and the largest magnitudes are one pass over the row and one
+// reduction, and the quotients follow from the registers that hold s. Bound by the
+// traffic: x (and the residual, in and out) and one byte out.
+#pragma once
+
+#include <algorithm>
+
+#include "async_ring.cuh"
+#include "e4m3.cuh"
+#include "rowops_device.cuh"
+#include "rowops_launch.h"
+
+namespace rowops {
+
+// A row's vectors, of V = 16 bytes' columns each, move in pieces of 16 bytes, 4, or 2 (single bf16), by the
+// rows' alignment; the rest of the work goes by vectors whatever the pieces.
+template <int PIECE>
+__device__ __forceinline__ uint4 load_vector(const void* p, int bytes) {
+    if constexpr (PIECE == 16) return *static_cast<const uint4*>(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+    if constexpr (PIECE == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * i < bytes) w[i] = static_cast<const uint32_t*>(p)[i];
+    }
+    if constexpr (PIECE == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (2 * i < bytes) w[i / 2] |= uint32_t(static_cast<const uint16_t*>(p)[i]) << (i % 2 * 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int PIECE>
+__device__ __forceinline__ void store_vector(void* p, const uint4& v, int bytes) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (PIECE == 16) st_stream16(p, v);
+    if constexpr (PIECE == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * i < bytes) static_cast<uint32_t*>(p)[i] = w[i];
+    }
+    if constexpr (PIECE == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (2 * i < bytes) static_cast<uint16_t*>(p)[i] = uint16_t(w[i / 2] >> (i % 2 * 16));
+    }
+}
+
+// the first n of N quotients as e4m3 bytes; whole: all of them, at an address aligned to N
+template <int N>
+__device__ __forceinline__ void store_e4m3(uint8_t* q, const float (&f)[N], bool whole, int n) {
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const uint32_t two = to_e4m3x2(f[i], f[i + 1]);
+        w[i / 4] = i % 4 ? w[i / 4] | two << 16 : two;
+    }
+    if (whole) {
+        if constexpr (N == 4) asm volatile("st.global.cs.u32 [%0], %1;" ::"l"(q), "r"(w[0]) : "memory");
+        if constexpr (N == 8) asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(q), "r"(w[0]), "r"(w[1]) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) q[i] = uint8_t(w[i / 4] >> (i % 4 * 8));
+    }
+}
+
+enum QuantMode { kQuantRow, kQuantLanes, kQuantGroups };
+
+constexpr int kQuantThreads = 512;
+// rows of a thread's ring: three, or what the largest CTA's shared memory holds
+__host__ __device__ constexpr int quant_steps(int vectors) {
+    const int most = 200 * 1024 / (16 * vectors * kQuantThreads);
+    return most > 3 ? 3 : most;
+}
+
+// A row for every `tpr` threads, VPT vectors a thread; the vectors come through rings of copies,
+// each thread's its own (single bf16 straight to the registers), the weights stay in registers.
+// kQuantLanes: a group is `lanes` lanes of a warp (a power of two). kQuantGroups:
+// any multiple of 32 columns; the maxima of every 32 columns meet in shared memory, in one of three
+// arrays: a row's is cleared two barriers before it is used again. `aligned`: q's rows start at multiples of V.
+template <typename T, int PIECE, bool RES, int VPT, QuantMode MODE>
+__global__ void __launch_bounds__(kQuantThreads)
+    rms_quant_kernel(const __grid_constant__ QuantArgs a, int tpr, int lanes, int groups, bool aligned) {
+    using E = Elem<T>;
+    constexpr int V = E::kVec, S = RES ? 2 : 1, D = quant_steps(VPT * S);
+    constexpr bool kRing = PIECE >= 4, kKept = VPT <= 4;
+    extern __shared__ uint4 dynamic[];
+    __shared__ float2 red[2][kQuantThreads / 32];
+    const int t = threadIdx.x % tpr, team = threadIdx.x / tpr, teams = blockDim.x / tpr, lane = threadIdx.x & 31,
+              warp = threadIdx.x >> 5, w0 = team * (tpr / 32), warps = tpr / 32;
+    unsigned* tops = reinterpret_cast<unsigned*>(dynamic) + team * 3 * groups;
+    uint4* ring = dynamic + (MODE == kQuantGroups ? (teams * 3 * groups * 4 + 15) / 16 : 0) + threadIdx.x;
+    const int64_t step = int64_t(gridDim.x) * teams;
+    const int N = int(a.N), vectors = (N + V - 1) / V;
+    auto meet = [&] {
+        if (tpr > 32) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(tpr) : "memory");
+        else __syncwarp();
+    };
+    auto bytes = [&](int k) { return PIECE == 16 ? 16 : min(16, (N - k * V) * E::kBytes); };  // of vector k
+    int64_t row = int64_t(blockIdx.x) * teams + team, asked = row;
+    auto ask_vector = [&](uint4* to, const void* tensor, int k) {
+        const char* from = static_cast<const char*>(tensor) + (asked * a.ld + k * V) * E::kBytes;
+        if constexpr (PIECE == 16) {
+            copy_async<16>(to, from);
+        } else if constexpr (PIECE == 4) {
+            const int n = bytes(k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * i < n) copy_async<4>(reinterpret_cast<char*>(to) + 4 * i, from + 4 * i);
+        }
+    };
+    auto ask = [&](int slot) {
+        if constexpr (kRing) {
+            if (asked < a.M) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+                    if (t + j * tpr < vectors) {
+                        ask_vector(ring + (slot * VPT * S + j) * blockDim.x, a.x, t + j * tpr);
+                        if constexpr (RES)
+                            ask_vector(ring + (slot * VPT * S + VPT + j) * blockDim.x, a.residual, t + j * tpr);
+                    }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asked += step;
+        }
+    };
+    if constexpr (PIECE == 4)  // what lies behind a row's end counts as 0
+        for (int i = 0; i < D * VPT * S; ++i) ring[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int d = 0; d < D; ++d) ask(d);
+    uint4 w[kKept ? VPT : 1];
+    auto weights = [&](int k) { return load_vector<PIECE>(static_cast<const T*>(a.w) + k * V, bytes(k)); };
+    if (kKept && a.w) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (t + j * tpr < vectors) w[kKept ? j : 0] = weights(t + j * tpr);
+    }
+    if constexpr (MODE == kQuantGroups) {
+        for (int i = t; i < 3 * groups; i += tpr) tops[i] = 0;
+        meet();
+    }
+    const float inv_n = 1.f / float(N);
+    int slot = 0, third = 0;
+    for (int turn = 0; row < a.M; row += step, turn ^= 1) {
+        if constexpr (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+        uint4 held[VPT];
+        float sum = 0.f, top[MODE == kQuantLanes ? VPT : 1] = {};
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int k = t + j * tpr;
+            float most = 0.f;
+            if (k < vectors) {
+                const int64_t at = row * a.ld + k * V;
+                uint4 x = kRing ? ring[(slot * VPT * S + j) * blockDim.x]
+                                : load_vector<PIECE>(static_cast<const T*>(a.x) + at, bytes(k));
+                float s[V], ws[V];
+                E::unpack(x, s);
+                if constexpr (RES) {
+                    const uint4 r4 = kRing ? ring[(slot * VPT * S + VPT + j) * blockDim.x]
+                                           : load_vector<PIECE>(static_cast<const T*>(a.residual) + at, bytes(k));
+                    float r[V];
+                    E::unpack(r4, r);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[e] += r[e];
+                    x = E::pack(s);
+                    store_vector<PIECE>(static_cast<T*>(a.residual_out) + at, x, bytes(k));
+                    E::unpack(x, s);
+                }
+                held[j] = x;
+                if (a.w) E::unpack(kKept ? w[kKept ? j : 0] : weights(k), ws);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    sum = fmaf(s[e], s[e], sum);
+                    most = max_nan(most, fabsf(a.w ? s[e] * ws[e] : s[e]));
+                }
+            }
+            if constexpr (MODE == kQuantRow) top[0] = max_nan(top[0], most);
+            if constexpr (MODE == kQuantLanes) {
+                for (int o = 1; o < lanes; o <<= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+                top[j] = most;
+            }
+            if constexpr (MODE == kQuantGroups) {  // (bits of what is not negative are in order, a NaN's above all)
+#pragma unroll
+                for (int o = 1; o < 32 / V; o <<= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+                if (k < vectors && lane % (32 / V) == 0)
+                    atomicMax(tops + third * groups + k * V / int(a.group), __float_as_uint(most));
+            }
+        }
+        ask(slot);
+        slot = slot + 1 == D ? 0 : slot + 1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if constexpr (MODE == kQuantRow) top[0] = max_nan(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+        }
+        if (tpr > 32) {
+            if (lane == 0) red[turn][warp] = make_float2(sum, top[0]);
+            meet();
+            sum = 0.f;
+            for (int i = 0; i < warps; ++i) {
+                const float2 o = red[turn][w0 + i];
+                sum += o.x;
+                if constexpr (MODE == kQuantRow) top[0] = max_nan(top[0], o.y);
+            }
+        } else {
+            meet();
+        }
+        const float inv = rsqrtf(sum * inv_n + a.eps);
+        if constexpr (MODE == kQuantGroups) {
+            unsigned* clear = tops + (third == 0 ? 2 : third - 1) * groups;
+            for (int i = t; i < groups; i += tpr) clear[i] = 0;
+        }
+        float scale = MODE == kQuantRow ? quant_scale(top[0] * inv) : 0.f, f = 1.f / scale;
+        if (MODE == kQuantRow && t == 0) a.scales[row] = scale;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int k = t + j * tpr;
+            if (k >= vectors) continue;
+            if constexpr (MODE == kQuantLanes) {
+                scale = quant_scale(top[j] * inv);
+                f = 1.f / scale;
+                if (lane % lanes == 0) a.scales[row * groups + k / lanes] = scale;
+            }
+            if constexpr (MODE == kQuantGroups) {
+                const int g = k * V / int(a.group);
+                scale = quant_scale(__uint_as_float(tops[third * groups + g]) * inv);
+                f = 1.f / scale;
+                if (k * V - g * int(a.group) == 0) a.scales[row * groups + g] = scale;
+            }
+            float s[V], ws[V];
+            E::unpack(held[j], s);
+            if (a.w) E::unpack(kKept ? w[kKept ? j : 0] : weights(k), ws);
+            // inv and f apart: their product may overflow
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[e] = (a.w ? s[e] * ws[e] : s[e]) * inv * f;
+            const int n = bytes(k) / E::kBytes;
+            store_e4m3(static_cast<uint8_t*>(a.q) + row * a.ldq + k * V, s, PIECE == 16 || (aligned && n == V), n);
+        }
+        third = third == 2 ? 0 : third + 1;
+    }
+    if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// One CTA per row, any length and layout: rows of more words than a CTA holds. Pass 1 forms s (writing residual_out)
+// and the sum of squares; then a warp takes a group at a time, its largest
+// magnitude and its quotients (the whole row is one group of the CTA).
+constexpr int kLoopBlock = 512;
+
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kLoopBlock) rms_quant_looped_kernel(const QuantArgs a) {
+    using E = Elem<T>;
+    __shared__ float red[2][2][kLoopBlock / 32];  // alternate per row
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T* w = static_cast<const T*>(a.w);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
+        const T* x = static_cast<const T*>(a.x) + row * a.ld;
+        const T* src = RES ? static_cast<T*>(a.residual_out) + row * a.ld : x;
+        uint8_t* q = static_cast<uint8_t*>(a.q) + row * a.ldq;
+        float sum = 0.f, top = 0.f;
+        for (int64_t c = threadIdx.x; c < a.N; c += kLoopBlock) {
+            float s = E::load(x + c);
+            if constexpr (RES) {
+                s = E::round(s + E::load(static_cast<const T*>(a.residual) + row * a.ld + c));
+                E::store(static_cast<T*>(a.residual_out) + row * a.ld + c, s);
+            }
+            sum = fmaf(s, s, sum);
+            if (a.group == a.N) top = max_nan(top, fabsf(w ? s * E::load(w + c) : s));
+        }
+        sum = group_reduce<kLoopBlock>(sum, red[turn][0], OpSum());
+        const float inv = rsqrtf(sum / float(a.N) + a.eps);
+        if (a.group == a.N) {
+            top = group_reduce<kLoopBlock>(top, red[turn][1], OpMaxNan());
+            const float scale = quant_scale(top * inv);
+            if (threadIdx.x == 0) a.scales[row] = scale;
+            const float f = 1.f / scale;  // (apart from inv: the product of the two may overflow)
+            for (int64_t c = threadIdx.x; c < a.N; c += kLoopBlock) {
+                const float s = E::load(src + c);
+                q[c] = to_e4m3(s * (w ? E::load(w + c) : 1.f) * inv * f);
+            }
+            continue;
+        }
+        const int64_t groups = (a.N + a.group - 1) / a.group;
+        for (int64_t g = warp; g < groups; g += kLoopBlock / 32) {
+            const int64_t c0 = g * a.group, c1 = c0 + a.group < a.N ? c0 + a.group : a.N;
+            top = 0.f;
+            for (int64_t c = c0 + lane; c < c1; c += 32)
+                top = max_nan(top, fabsf(E::load(src + c) * (w ? E::load(w + c) : 1.f)));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float scale = quant_scale(top * inv), f = 1.f / scale;
+            if (lane == 0) a.scales[row * groups + g] = scale;
+            for (int64_t c = c0 + lane; c < c1; c += 32)
+                q[c] = to_e4m3(E::load(src + c) * (w ? E::load(w + c) : 1.f) * inv * f);
+        }
+    }
+}
+
+// Threads of a row and vectors of a thread. Many rows: four vectors a thread, so that a row's
+// reduction costs few instructions a byte; eight for rows of more than 512 such threads. At most one row an
+// SM: as many threads as the row has vectors, up to 512, since one row's latency is what counts then.
+struct QuantShape {
+    int tpr, vpt, teams;
+};
+inline bool quant_shape(int64_t vectors, int64_t M, const LaunchCfg& cfg, QuantShape* s) {
+    int vpt = vectors > int64_t(kQuantThreads) * 4 ? 8 : 4;
+    if (M <= cfg.num_sms)
+        while (vpt > 1 && vectors <= int64_t(kQuantThreads) * (vpt / 2)) vpt /= 2;
+    const int64_t tpr = ((vectors + vpt - 1) / vpt + 31) / 32 * 32;
+    if (tpr > kQuantThreads) return false;
+    s->tpr = int(tpr);
+    s->vpt = vpt;
+    s->teams = int(std::max<int64_t>(1, 256 / tpr));
+    return true;
+}
+
+template <typename T, int PIECE, bool RES, int VPT, QuantMode MODE>
+cudaError_t launch_quant(const QuantArgs& a, const QuantShape& s, int lanes, int groups, const LaunchCfg& cfg) {
+    auto k = rms_quant_kernel<T, PIECE, RES, VPT, MODE>;
+    constexpr int V = Elem<T>::kVec, kVectors = VPT * (RES ? 2 : 1);
+    const int block = s.tpr * s.teams;
+    const size_t tops = MODE == kQuantGroups ? (size_t(s.teams) * 3 * groups * 4 + 15) / 16 * 16 : 0;
+    const size_t smem = tops + (PIECE >= 4 ? size_t(16) * kVectors * quant_steps(kVectors) * block : 0);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, cfg);
+    if (e != cudaSuccess) return e;
+    const int grid = grid_for(reinterpret_cast<const void*>(k), block, smem, (a.M + s.teams - 1) / s.teams, cfg);
+    const bool aligned = reinterpret_cast<uintptr_t>(a.q) % V == 0 && a.ldq % V == 0;
+    k<<<grid, block, smem, cfg.stream>>>(a, s.tpr, lanes, groups, aligned);
+    return cudaGetLastError();
+}
+
+template <typename T, int PIECE, bool RES, int VPT>
+cudaError_t launch_quant_mode(const QuantArgs& a, const QuantShape& s, const LaunchCfg& cfg) {
+    const int groups = int((a.N + a.group - 1) / a.group);
+    if (groups == 1) return launch_quant<T, PIECE, RES, VPT, kQuantRow>(a, s, 0, 1, cfg);
+    const int lanes = int(a.group / Elem<T>::kVec);
+    if (lanes <= 32 && (lanes & (lanes - 1)) == 0)
+        return launch_quant<T, PIECE, RES, VPT, kQuantLanes>(a, s, lanes, groups, cfg);
+    return launch_quant<T, PIECE, RES, VPT, kQuantGroups>(a, s, 0, groups, cfg);
+}
+
+template <typename T, int PIECE>
+cudaError_t launch_quant_vectors(const QuantArgs& a, const QuantShape& s, const LaunchCfg& cfg) {
+    if (a.residual)
+        return s.vpt == 1   ? launch_quant_mode<T, PIECE, true, 1>(a, s, cfg)
+               : s.vpt == 2 ? launch_quant_mode<T, PIECE, true, 2>(a, s, cfg)
+               : s.vpt == 4 ? launch_quant_mode<T, PIECE, true, 4>(a, s, cfg)
+                            : launch_quant_mode<T, PIECE, true, 8>(a, s, cfg);
+    return s.vpt == 1   ? launch_quant_mode<T, PIECE, false, 1>(a, s, cfg)
+           : s.vpt == 2 ? launch_quant_mode<T, PIECE, false, 2>(a, s, cfg)
+           : s.vpt == 4 ? launch_quant_mode<T, PIECE, false, 4>(a, s, cfg)
+                        : launch_quant_mode<T, PIECE, false, 8>(a, s, cfg);
+}
+
+// piece: bytes of the widest access that every row allows; 0: the looped kernel
+template <typename T>
+cudaError_t launch_rms_quant(const QuantArgs& a, int piece, const LaunchCfg& cfg) {
+    QuantShape s;
+    if (piece && a.N <= int64_t(kQuantThreads) * 8 * Elem<T>::kVec &&
+        quant_shape((a.N + Elem<T>::kVec - 1) / Elem<T>::kVec, a.M, cfg, &s)) {
+        if (piece == 16) return launch_quant_vectors<T, 16>(a, s, cfg);
+        if (piece == 4) return launch_quant_vectors<T, 4>(a, s, cfg);
+        if constexpr (sizeof(T) == 2) return launch_quant_vectors<T, 2>(a, s, cfg);
+    }
+    const bool res = a.residual != nullptr;
+    auto k = res ? rms_quant_looped_kernel<T, true> : rms_quant_looped_kernel<T, false>;
+    const int grid = grid_for(reinterpret_cast<const void*>(k), kLoopBlock, 0, a.M, cfg);
+    k<<<grid, kLoopBlock, 0, cfg.stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace rowops

@@ -1430,9 +1430,18 @@ rowops_status_t rowops_rmsnorm_quant(const void* x, const void* residual, void* 
     LaunchCfg cfg;
     if ((st = make_cfg(stream, tn, &cfg)) != ROWOPS_OK) return st;
     QuantArgs a = {x, residual, w, q, residual_out, scales, eps, M, N, ld, ldq, group};
+    // the pieces that rows move in: 16 bytes (with whole vectors and q to match), 4 or one element
+    auto even = [&](int n) {
+        for (const void* p : {x, residual, static_cast<const void*>(residual_out), w})
+            if (!aligned(p, size_t(n) * es)) return false;
+        return ld % n == 0;
+    };
+    int piece = es;
+    if (even(4 / es) && N % (4 / es) == 0) piece = 4;
     const int vec = 16 / es;
-    const bool whole = vector_rows(tn, N, ld, es, {x, residual, residual_out, w}) && ldq % vec == 0 && aligned(q, vec);
-    return finish((dtype == ROWOPS_F32 ? rms_quant_f32() : rms_quant_bf16())(a, whole, cfg));
+    if (even(vec) && N % vec == 0 && ldq % vec == 0 && aligned(q, vec)) piece = 16;
+    if (tn.family == Family::Looped) piece = 0;
+    return finish((dtype == ROWOPS_F32 ? rms_quant_f32 : rms_quant_bf16)(a, piece, cfg));
 }
 
 namespace {

@@ -431,8 +431,8 @@ GnForwardLaunch gn_forward_bf16(int vec, int act);
 GnBackwardLaunch gn_backward_f32(int vec, int act);
 GnBackwardLaunch gn_backward_bf16(int vec, int act);
 
-// Serving operators. RMSNorm with an 8-bit result: group == N is one scale a row; vec: 16-byte
-// aligned rows of whole vectors, q aligned to a vector's bytes in 8 bits.
+// Serving operators. RMSNorm with an 8-bit result: group == N is one scale a row; piece:
+// bytes of the widest access that every row allows (0: the looped kernel).
 struct QuantArgs {
     const void *x, *residual, *w;
     void *q, *residual_out;
@@ -440,9 +440,8 @@ struct QuantArgs {
     float eps;
     int64_t M, N, ld, ldq, group;
 };
-using QuantLaunch = cudaError_t (*)(const QuantArgs& a, bool vec, const LaunchCfg& cfg);
-QuantLaunch rms_quant_f32();
-QuantLaunch rms_quant_bf16();
+cudaError_t rms_quant_f32(const QuantArgs& a, int piece, const LaunchCfg& cfg);
+cudaError_t rms_quant_bf16(const QuantArgs& a, int piece, const LaunchCfg& cfg);
 
 // Attention over a paged cache. Strides in elements.
 constexpr int kPagedMaxD = 256;
