@@ -668,7 +668,7 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
  *            the others no cut.)
  *   token    device pointer to M int64.
  *   logprob  NULL, or M floats: the log-probability of the token among those kept.
- * N is at most 393216 and M at most 2^27 (ROWOPS_ERR_UNSUPPORTED beyond). w is held in
+ * N is at most 327680 and M at most 2^27 (ROWOPS_ERR_UNSUPPORTED beyond). w is held in
  * fixed point, 44 bits behind the point and right to 2^-29 of its value, and added up
  * exactly: the same token for the same row, whatever the batch around it.
  */

@@ -474,7 +474,7 @@ cudaError_t paged_attention_f32_g8(const PagedArgs& a, void* workspace, const La
 
 // Sampling: the per-row numbers where given, else the one for all rows. A row is held
 // by a cluster of at most 8 CTAs.
-constexpr int64_t kSampleMaxN = 3 << 17;
+constexpr int64_t kSampleMaxN = 5 << 16;
 struct SampleArgs {
     const void* logits;
     const float *u, *temperature, *top_p, *min_p;

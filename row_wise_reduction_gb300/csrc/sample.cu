@@ -16,10 +16,14 @@
 // many of the equal ones, by index, still belong.
 //
 // A row is held in the shared memory of a cluster of CTAs, each with a share of its
-// columns, and every sweep is over that copy. The k-th value, and the value at which
-// a mass is reached, are found digit by digit: a histogram of 8 bits of kd (counts, or
-// counts and masses) over what agrees with the digits so far, added up over the
-// cluster through distributed shared memory.
+// columns, and every sweep is over that copy. One histogram of the values' upper 16
+// bits (every value of bf16 a bin of its own) says in which bin the k-th value lies,
+// and in which a mass is reached; the bins are counted by the CTAs and added up
+// through distributed shared memory. Of bf16 the counts are enough: a bin's mass is its count
+// times its value's weight, so weights are computed by the bin and not by the element, and the CTAs'
+// own masses follow from their own counts. fp32 values differ within a bin: masses are
+// added up beside the counts (in three words of 16 bits and more, each a native 32-bit
+// atomic; 64-bit ones in shared memory took fifteen times as long), and the cut's bin is searched digit by digit.
 #include <algorithm>
 #include <type_traits>
 
@@ -36,7 +40,11 @@ namespace {
 
 constexpr int kBlock = 512, kWarps = kBlock / 32;
 constexpr int kCluster = 8;  // the most CTAs of a row
-constexpr int kBins = 256;
+constexpr int kDigit = 256;  // bins of a digit
+// The histogram: 13 binades of 128 bins below the largest magnitude, for either sign, and one
+// bin for what is nearer to zero.
+constexpr int kHalf = 13 * 128, kBins = 2 * kHalf + 1, kBinsHeld = (kBins + 3) / 4 * 4;
+constexpr int kEach = (kBins + kBlock - 1) / kBlock;  // bins of a thread, in the CTA alone
 constexpr int kFraction = 44;
 constexpr uint64_t kOne = uint64_t(1) << kFraction;
 
@@ -81,52 +89,122 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 
 // What the CTAs of a cluster tell one another.
 struct Told {
-    float top;
-    int first;             // greedy: its first column at the maximum
-    uint64_t mass;         // of what lies strictly before the cut
-    uint32_t ties;         // at the cut
+    float top, low;
+    int first;       // greedy: its first column at the maximum
+    uint64_t mass;   // of its part of the bins; of what it holds before the cut
+    uint32_t count;  // of its part of the bins; of what it holds at the cut
+};
+// The bin in which a count or a mass is reached, and what lies before it.
+struct Found {
+    uint32_t bin, count;
+    uint64_t mass;
 };
 
 struct Shared {
     uint64_t roots[16];
-    uint64_t mass[2][kBins];
-    uint32_t count[2][kBins];
+    uint64_t mass[2][kDigit];  // digits: masses, or counts
     uint64_t warp_mass[kWarps];
     uint32_t warp_count[kWarps];
-    float warp_top[kWarps];
-    Told own;               // read by the others
-    Told all[kCluster];     // written by the others
-    // one thread's answers for the CTA
-    uint64_t target, before, total;
-    uint32_t bin, found;
-    float c_hi, c_lo;
+    float warp_top[kWarps], warp_low[kWarps];
+    Told own;             // read by the others
+    uint64_t near_zero;   // bf16: the mass of the bin for it, read by the others
+    Told all[kCluster], kept[kCluster];  // written by the others
+    Found found[2];       // by whoever has the bin
+    uint64_t before;
+    uint32_t bin;
+    float c_hi, c_lo, cutoff;
     uint32_t kd_min_p;
 };
 
-template <typename T>
-struct Digits {
-    static constexpr int kKey = std::is_same_v<T, float> ? 32 : 16;
-};
-
-// A cut: what lies before kd, and the first `ties` at it.
+// A cut: what lies before kd in the order of the values, and the first `ties` at it.
 struct Cut {
     uint32_t kd, ties;
 };
+constexpr uint32_t kNone = 0xffffffffu;
 __device__ __forceinline__ Cut shorter(Cut a, Cut b) {
     return a.kd != b.kd ? (a.kd < b.kd ? a : b) : Cut{a.kd, a.ties < b.ties ? a.ties : b.ties};
+}
+
+// Sums over the CTA's threads, or what lies before a thread; every thread calls them.
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v += red[i];
+    return v;
+}
+template <typename N>
+__device__ __forceinline__ N block_before(N v, N* red, N* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    N run = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const N other = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += other;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = run;
+    __syncthreads();
+    N all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) run += red[i];
+        all += red[i];
+    }
+    *total = all;
+    return run - v;
 }
 
 template <typename T>
 struct Row {
     using E = Elem<T>;
-    static constexpr int kDrop = 32 - Digits<T>::kKey;
+    static constexpr bool kF32 = std::is_same_v<T, float>;
+    static constexpr int kKey = kF32 ? 32 : 16, kDrop = 32 - kKey;
     Shared& sh;
-    const T* x;  // this CTA's columns, -inf behind them up to a whole vector
+    uint32_t* counts;  // [kBinsHeld], and, fp32, three words of each bin's mass
+    const T* x;        // this CTA's columns, -inf behind them up to a whole vector
     int n, C, rank;
     uint32_t top_key;
     Weights w;
+    int most, least;   // upper 15 bits of the magnitudes that have bins: from `least` (1 at least) to `most`
+    int half, bins;    // bins of a sign; of the histogram
 
-    __device__ __forceinline__ uint32_t kd(float v) const { return (top_key >> kDrop) - (ordered(v) >> kDrop); }
+    __device__ __forceinline__ uint32_t key(float v) const { return ordered(v) >> kDrop; }
+    __device__ __forceinline__ uint32_t kd(float v) const { return (top_key >> kDrop) - key(v); }
+    __device__ __forceinline__ float value_at(uint32_t at) const {
+        uint32_t k = ((top_key >> kDrop) - at) << kDrop;
+        if (kDrop && !(k & 0x80000000u)) k |= 0xffffu;  // a negative bf16's lower bits of order are ones
+        return value_of(k);
+    }
+
+    __device__ __forceinline__ void choose_bins(float low) {
+        // (a magnitude's upper 15 bits)
+        const uint32_t t = __float_as_uint(w.m) >> 16 & 0x7fffu, l = __float_as_uint(low) >> 16 & 0x7fffu;
+        most = int(t > l ? t : l);
+        least = most - kHalf + 1 > 1 ? most - kHalf + 1 : 1;
+        if (most < 1) most = 1;
+        half = most - least + 1;
+        bins = 2 * half + 1;
+    }
+    // the bin of a value by the upper 16 bits of its order; bins and more: below all of them
+    __device__ __forceinline__ uint32_t bin_of(uint32_t key16) const {
+        const int up = int(key16) - 0x8000, down = 0x7fff - int(key16);
+        return up >= least ? uint32_t(most - up) : down >= least ? uint32_t(half + 1 + down - least) : uint32_t(half);
+    }
+    // the largest such 16 bits in a bin
+    __device__ __forceinline__ uint32_t bin_top(uint32_t bin) const {
+        return bin < uint32_t(half)   ? 0x8000u + most - bin
+               : bin > uint32_t(half) ? 0x7fffu - least - (bin - half - 1)
+                                      : 0x8000u + least - 1;
+    }
+    __device__ __forceinline__ bool near_zero(uint32_t bin) const { return bin == uint32_t(half); }
+    // whether a bin's elements are equal
+    __device__ __forceinline__ bool single(uint32_t bin) const { return !kF32 && !near_zero(bin); }
+    __device__ __forceinline__ uint32_t bin_kd(uint32_t bin) const { return (top_key >> 16) - bin_top(bin); }  // bf16
 
     template <class F>
     __device__ __forceinline__ void each(F f) const {
@@ -138,128 +216,269 @@ struct Row {
         }
     }
 
-    // The cut at which the counts reach `k` (MASS false), or the masses reach p times
-    // their sum over what `within` keeps. `flip`: which histogram the next level takes;
-    // both are zero here and when it returns.
-    template <bool MASS>
-    __device__ Cut find(cg::cluster_group& cluster, uint32_t k, double p, Cut within, int& flip) {
-        uint32_t prefix = 0;
-        uint64_t before = 0, target = k;
-        for (int shift = Digits<T>::kKey - 8; shift >= 0; shift -= 8, flip ^= 1) {
+    // This CTA's histogram. bf16: counts, and the mass near zero; fp32: what is asked for.
+    __device__ __forceinline__ void count(bool masses) {
+        if constexpr (kF32) {
             each([&](float v) {
-                const uint32_t at = kd(v);
-                if (shift + 8 < Digits<T>::kKey && (at >> (shift + 8)) != prefix) return;
+                const uint32_t bin = bin_of(ordered(v) >> 16);
+                if (bin >= uint32_t(bins)) return;
+                if (masses) {
+                    const uint64_t m = w(v);
+                    if (m == 0) return;
+                    atomicAdd(counts + kBinsHeld + bin, uint32_t(m) & 0xffffu);
+                    atomicAdd(counts + 2 * kBinsHeld + bin, uint32_t(m >> 16) & 0xffffu);
+                    if (m >> 32) atomicAdd(counts + 3 * kBinsHeld + bin, uint32_t(m >> 32));
+                }
+                atomicAdd(counts + bin, 1u);
+            });
+        } else {
+            uint64_t near = 0;
+            for (int k = threadIdx.x; k * E::kVec < n; k += kBlock) {
+                const uint4 u = reinterpret_cast<const uint4*>(x)[k];
+                const uint32_t four[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t b = e & 1 ? four[e / 2] >> 16 : four[e / 2] & 0xffffu;
+                    const int mag = int(b & 0x7fffu);
+                    const uint32_t bin = b & 0x8000u ? uint32_t(half + 1 - least + mag) : uint32_t(most - mag);
+                    if (mag < least) {
+                        atomicAdd(counts + half, 1u);
+                        near += w(__uint_as_float(b << 16));
+                    } else if (bin < uint32_t(bins)) {
+                        atomicAdd(counts + bin, 1u);
+                    }
+                }
+            }
+            near = block_sum(near, sh.warp_mass);
+            if (threadIdx.x == 0) sh.near_zero = near;
+        }
+    }
+
+    // A thread's share of the cluster's bins, added up over its CTAs.
+    struct Share {
+        uint32_t first, count[kEach];
+        uint64_t mass[kEach];
+        int each;
+        uint32_t counts;         // of the share
+        uint64_t masses;
+        uint32_t counts_before;  // in the whole order
+        uint64_t masses_before;
+    };
+    __device__ __forceinline__ void gather(cg::cluster_group& cluster, bool masses, Share& s) const {
+        s.each = (bins + C * kBlock - 1) / (C * kBlock);
+        s.first = uint32_t((rank * kBlock + int(threadIdx.x)) * s.each);
+        s.counts = 0, s.masses = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            s.count[i] = 0, s.mass[i] = 0;
+            const uint32_t bin = s.first + i;
+            if (i < s.each && bin < uint32_t(bins)) {
+                uint64_t mass = 0;
+                for (int r = 0; r < C; ++r) {
+                    const uint32_t* o = cluster.map_shared_rank(counts, r);
+                    s.count[i] += o[bin];
+                    if (kF32 && masses)
+                        mass += o[kBinsHeld + bin] + (uint64_t(o[2 * kBinsHeld + bin]) << 16) +
+                                (uint64_t(o[3 * kBinsHeld + bin]) << 32);
+                    if (!kF32 && near_zero(bin)) mass += cluster.map_shared_rank(&sh, r)->near_zero;
+                }
+                if (!kF32 && !near_zero(bin) && s.count[i]) mass = s.count[i] * w(value_at(bin_kd(bin)));
+                s.mass[i] = mass;
+            }
+            s.counts += s.count[i];
+            s.masses += s.mass[i];
+        }
+    }
+
+    // The thread in whose share the running count (or mass) reaches `goal` tells every CTA.
+    template <bool MASS>
+    __device__ __forceinline__ void tell(cg::cluster_group& cluster, const Share& s, uint64_t goal) const {
+        uint64_t run = MASS ? s.masses_before : s.counts_before;
+        if (run >= goal || run + (MASS ? s.masses : s.counts) < goal) return;
+        Found f{0, s.counts_before, s.masses_before};
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (i >= s.each) break;
+            run += MASS ? s.mass[i] : s.count[i];
+            if (run >= goal) {
+                f.bin = s.first + i;
+                break;
+            }
+            f.count += s.count[i];
+            f.mass += s.mass[i];
+        }
+        for (int r = 0; r < C; ++r) cluster.map_shared_rank(&sh, r)->found[MASS] = f;
+    }
+
+    // The cut in a bin whose elements differ, where the counts (or the masses, of what
+    // `within` keeps) reach `goal`, `before` of it in the bins before: digit by digit of the distance
+    // from the bin's largest key. `flip`: which digit's bins are next; both sets
+    // are zero here and when it returns.
+    template <bool MASS>
+    __device__ Cut find(cg::cluster_group& cluster, uint32_t bin, uint64_t goal, uint64_t before, Cut within, int& flip) {
+        const uint32_t top = kF32 ? bin_top(bin) << 16 | 0xffffu : bin_top(bin);
+        const uint32_t width = near_zero(bin) ? (2u * least << (16 - kDrop)) - 1 : 0xffffu;
+        const uint32_t from = (top_key >> kDrop) - top;  // kd of the bin's largest key (mod 2^32: it may be past the maximum's)
+        uint32_t prefix = 0;
+        const int bits = near_zero(bin) ? kKey : 16;
+        for (int shift = bits - 8; shift >= 0; shift -= 8, flip ^= 1) {
+            each([&](float v) {
+                const uint32_t at = top - key(v);
+                if (at > width || (shift + 8 < bits && (at >> (shift + 8)) != prefix)) return;
+                const uint32_t d = at >> shift & 255u;
                 if constexpr (MASS) {
-                    if (at >= within.kd) return;
+                    if (from + at >= within.kd) return;
                     const uint64_t mass = w(v);
-                    if (mass) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[flip][(at >> shift) & 255]), mass);
+                    if (mass) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[flip][d]), mass);
                 } else {
-                    atomicAdd(&sh.count[flip][(at >> shift) & 255], 1u);
+                    atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[flip][d]), 1ull);
                 }
             });
             cluster.sync();
-            // a thread has a bin: its sum over the cluster, then the running sum over the bins
-            uint64_t mine = 0, run;
-            if (threadIdx.x < kBins) {
-                for (int r = 0; r < C; ++r) {
-                    const Shared* o = cluster.map_shared_rank(&sh, r);
-                    mine += MASS ? o->mass[flip][threadIdx.x] : o->count[flip][threadIdx.x];
-                }
+            // a thread has a digit: its sum over the cluster, then what lies before it
+            uint64_t mine = 0;
+            if (threadIdx.x < kDigit) {
+                for (int r = 0; r < C; ++r) mine += cluster.map_shared_rank(&sh, r)->mass[flip][threadIdx.x];
                 if constexpr (MASS) {  // those equal to the k-th value that are among the first k
-                    const bool agrees = shift + 8 == Digits<T>::kKey || (within.kd >> (shift + 8)) == prefix;
-                    if (within.ties && agrees && ((within.kd >> shift) & 255) == threadIdx.x)
+                    const uint32_t at = within.kd - from;
+                    if (within.ties && at <= width && (shift + 8 == bits || (at >> (shift + 8)) == prefix) &&
+                        (at >> shift & 255u) == threadIdx.x)
                         mine += uint64_t(within.ties) * w(value_at(within.kd));
                 }
                 sh.mass[flip ^ 1][threadIdx.x] = 0;
-                sh.count[flip ^ 1][threadIdx.x] = 0;
             }
-            run = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t other = __shfl_up_sync(0xffffffffu, run, o);
-                if ((threadIdx.x & 31) >= o) run += other;
-            }
-            const int warp = threadIdx.x >> 5;
-            if ((threadIdx.x & 31) == 31) sh.warp_mass[warp] = run;
-            __syncthreads();
-            uint64_t total = 0;
-#pragma unroll
-            for (int i = 0; i < kBins / 32; ++i) {
-                if (i < warp) run += sh.warp_mass[i];
-                total += sh.warp_mass[i];
-            }
-            if (MASS && shift + 8 == Digits<T>::kKey) target = uint64_t(ceil(p * double(total)));
-            if (threadIdx.x < kBins && before + run >= target && before + run - mine < target) {
+            uint64_t total;
+            const uint64_t run = before + block_before(mine, sh.warp_mass, &total);
+            if (threadIdx.x < kDigit && run < goal && run + mine >= goal) {
                 sh.bin = threadIdx.x;
-                sh.before = before + run - mine;
+                sh.before = run;
             }
             __syncthreads();
             prefix = prefix << 8 | sh.bin;
             before = sh.before;
         }
-        // both histograms are zero for the next search: the last level's is read until all have been here
+        // the last digit's bins are read until all have been here
         cluster.sync();
-        if (threadIdx.x < kBins) sh.mass[flip ^ 1][threadIdx.x] = 0, sh.count[flip ^ 1][threadIdx.x] = 0;
+        if (threadIdx.x < kDigit) sh.mass[flip ^ 1][threadIdx.x] = 0;
         __syncthreads();
-        uint64_t ties = target - before;
-        if constexpr (MASS) {
-            const uint64_t one = w(value_at(prefix));
-            ties = one ? (ties + one - 1) / one : 1;
-            if (prefix == within.kd && ties > within.ties) ties = within.ties;
-        }
-        return Cut{prefix, uint32_t(ties < 0xffffffffu ? ties : 0xffffffffu)};
+        return reach<MASS>(from + prefix, goal - before, within);
     }
 
-    __device__ __forceinline__ float value_at(uint32_t at) const {
-        uint32_t key = ((top_key >> kDrop) - at) << kDrop;
-        if (kDrop && !(key & 0x80000000u)) key |= 0xffffu;  // a negative bf16's lower bits of order are ones
-        return value_of(key);
+    // the cut at kd of which `rest` is still wanted
+    template <bool MASS>
+    __device__ __forceinline__ Cut reach(uint32_t at, uint64_t rest, Cut within) const {
+        if constexpr (MASS) {
+            const uint64_t one = w(value_at(at));
+            rest = one ? (rest + one - 1) / one : 1;
+            if (at == within.kd && rest > within.ties) rest = within.ties;
+        }
+        return Cut{at, uint32_t(rest < kNone ? rest : kNone)};
+    }
+
+    // the cluster's mass of what lies in `bin` before kd
+    __device__ uint64_t mass_in(cg::cluster_group& cluster, uint32_t bin, uint32_t at) {
+        uint64_t mass = 0;
+        each([&](float v) {
+            if (bin_of(ordered(v) >> 16) == bin && kd(v) < at) mass += w(v);
+        });
+        mass = block_sum(mass, sh.warp_mass);
+        if (int(threadIdx.x) < C) cluster.map_shared_rank(&sh, threadIdx.x)->kept[rank].mass = mass;
+        cluster.sync();
+        mass = 0;
+        for (int r = 0; r < C; ++r) mass += sh.kept[r].mass;
+        cluster.sync();  // (written again by the final sums)
+        return mass;
+    }
+
+    // The sums of what a warp's columns [c0, c1) hold before the cut, and their ties at it.
+    __device__ __forceinline__ void warp_sums(int c0, int c1, Cut cut, uint64_t* mass, uint32_t* ties) const {
+        uint64_t m = 0;
+        uint32_t t = 0;
+        for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32) {
+            const float v = E::load(x + c);
+            const uint32_t at = kd(v);
+            if (at < cut.kd) m += w(v);
+            t += at == cut.kd;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+        *mass = m;
+        *ties = __reduce_add_sync(0xffffffffu, t);
     }
 };
 
+// Of the parts i = 0 .. parts - 1, in order, that in which the running sum exceeds *draw; *draw and *left
+// (the ties that still belong) become what they are at its begin.
+template <class Part>
+__device__ __forceinline__ int which(int parts, uint64_t one, uint64_t* draw, uint32_t* left, Part part) {
+    for (int i = 0;; ++i) {
+        uint64_t mass;
+        uint32_t ties;
+        part(i, &mass, &ties);
+        ties = min(ties, *left);
+        mass += ties * one;
+        if (*draw < mass || i + 1 == parts) return i;
+        *draw -= mass;
+        *left -= ties;
+    }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ SampleArgs a, const __grid_constant__ Roots roots,
-                                                        int share) {
+__global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ SampleArgs a,
+                                                        const __grid_constant__ Roots roots, int share) {
     using E = Elem<T>;
+    using R = Row<T>;
     __shared__ Shared sh;
-    extern __shared__ uint4 held[];
+    extern __shared__ uint4 dynamic[];
+    uint32_t* counts = reinterpret_cast<uint32_t*>(dynamic);
+    T* x = reinterpret_cast<T*>(counts + kBinsHeld * (R::kF32 ? 4 : 1));
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank()), lane = threadIdx.x & 31,
               warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x / C;
     const int lo = rank * share, n = a.N - lo < share ? (a.N > lo ? a.N - lo : 0) : share;
-    T* x = reinterpret_cast<T*>(held);
+    const float temperature = a.temperature ? a.temperature[row] : a.temperature_all;
+    const float min_p = a.min_p ? a.min_p[row] : a.min_p_all, top_p = a.top_p ? a.top_p[row] : a.top_p_all;
+    const int top_k = a.top_k ? a.top_k[row] : a.top_k_all;
     {
         const T* from = static_cast<const T*>(a.logits) + row * a.ld + lo;
         const int whole = (reinterpret_cast<uintptr_t>(from) & 15) == 0 ? n / E::kVec : 0;
         for (int k = threadIdx.x; k < whole; k += kBlock) copy_async<16>(x + k * E::kVec, from + k * E::kVec);
         for (int c = whole * E::kVec + threadIdx.x; c < n; c += kBlock) x[c] = from[c];
         for (int c = n + threadIdx.x; c < (n + E::kVec - 1) / E::kVec * E::kVec; c += kBlock) E::store(x + c, -INFINITY);
-        if (threadIdx.x < kBins)
-            for (int i = 0; i < 2; ++i) sh.mass[i][threadIdx.x] = 0, sh.count[i][threadIdx.x] = 0;
+        if (threadIdx.x < kDigit) sh.mass[0][threadIdx.x] = sh.mass[1][threadIdx.x] = 0;
+        for (int i = threadIdx.x; i < kBinsHeld * (R::kF32 ? 4 : 1); i += kBlock) counts[i] = 0;
         if (threadIdx.x < 16) sh.roots[threadIdx.x] = roots.v[threadIdx.x];
         asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
         __syncthreads();
     }
-    Row<T> r{sh, x, n, C, rank, 0, {}};
+    R r{sh, counts, x, n, C, rank, 0, {}, 0, 0, 0, 0};
 
-    // the maximum, NaN where there is one
-    float top = -INFINITY;
-    r.each([&](float v) { top = max_nan(top, v); });
+    // the maximum, NaN where there is one, and the minimum
+    float top = -INFINITY, low = INFINITY;
+    r.each([&](float v) {
+        top = max_nan(top, v);
+        low = fminf(low, v);
+    });
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) sh.warp_top[warp] = top;
+    for (int o = 16; o > 0; o >>= 1) {
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
+    if (lane == 0) sh.warp_top[warp] = top, sh.warp_low[warp] = low;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < kWarps; ++i) top = max_nan(top, sh.warp_top[i]);
-        sh.own.top = top;
+        for (int i = 1; i < kWarps; ++i) top = max_nan(top, sh.warp_top[i]), low = fminf(low, sh.warp_low[i]);
+        sh.own.top = top, sh.own.low = low;
     }
     cluster.sync();
-    top = -INFINITY;
-    for (int i = 0; i < C; ++i) top = max_nan(top, cluster.map_shared_rank(&sh, i)->own.top);
+    top = -INFINITY, low = INFINITY;
+    for (int i = 0; i < C; ++i) {
+        const Told& o = cluster.map_shared_rank(&sh, i)->own;
+        top = max_nan(top, o.top), low = fminf(low, o.low);
+    }
     top += 0.f;
     const bool none = !(top > -INFINITY);  // a NaN, or nothing to draw from
-    const float temperature = a.temperature ? a.temperature[row] : a.temperature_all;
     const bool greedy = !(temperature > 0.f);
     r.top_key = ordered(top);
 
@@ -288,94 +507,147 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
     }
 
     // the row's numbers in 64 bits, once
-    const float min_p = a.min_p ? a.min_p[row] : a.min_p_all, top_p = a.top_p ? a.top_p[row] : a.top_p_all;
-    const int top_k = a.top_k ? a.top_k[row] : a.top_k_all;
     if (threadIdx.x == 0) {
         const double c = 1.4426950408889634 / double(temperature);
         sh.c_hi = float(c);
         sh.c_lo = float(c - double(sh.c_hi));
+        sh.cutoff = float(double(top) - 43.7 * double(temperature));  // below: weights of 0 (2^-63)
         // the smallest value that min-p keeps: (x - m) / T >= ln(min_p)
-        sh.kd_min_p = 0xffffffffu;
+        sh.kd_min_p = kNone;
         if (min_p > 0.f) {
             const double least = double(top) + double(temperature) * log(double(min_p < 1.f ? min_p : 1.f));
             const float up = least > -3.4028234e38 ? __double2float_ru(least) : -INFINITY;
             uint32_t key = ordered(up);
-            if (Row<T>::kDrop && (key & 0x80000000u)) key += 0xffffu;  // the next bf16 (below zero: cut off, it is that)
-            sh.kd_min_p = (r.top_key >> Row<T>::kDrop) - (key >> Row<T>::kDrop);
+            if (R::kDrop && (key & 0x80000000u)) key += 0xffffu;  // the next bf16 (below zero: cut off, it is that)
+            sh.kd_min_p = (r.top_key >> R::kDrop) - (key >> R::kDrop);
         }
     }
     __syncthreads();
     r.w = Weights{top, sh.c_hi, sh.c_lo, sh.roots};
-    Cut cut{sh.kd_min_p, 0xffffffffu};
-    int flip = 0;
-    Cut within{0xffffffffu, 0u};
-    if (top_k > 0 && top_k < a.N) {
-        within = r.template find<false>(cluster, uint32_t(top_k), 0., within, flip);
-        cut = shorter(cut, within);
+    r.choose_bins(fmaxf(low, sh.cutoff));
+    const bool cut_k = top_k > 0 && top_k < a.N, cut_p = top_p < 1.f;
+    Cut cut{sh.kd_min_p, kNone}, within{kNone, 0u};
+    if (!R::kF32 || cut_k || cut_p) {
+        r.count(cut_p);
     }
-    if (top_p < 1.f) cut = shorter(cut, r.template find<true>(cluster, 0u, top_p > 0.f ? double(top_p) : 1e-300, within, flip));
+    if (cut_k || cut_p) {
+        cluster.sync();
+        int flip = 0;
+        typename R::Share s;
+        r.gather(cluster, cut_p, s);
+        uint32_t counts_here;
+        uint64_t masses_here;
+        s.counts_before = block_before(s.counts, sh.warp_count, &counts_here);
+        s.masses_before = block_before(s.masses, sh.warp_mass, &masses_here);
+        if (int(threadIdx.x) < C) {
+            Told* to = &cluster.map_shared_rank(&sh, threadIdx.x)->all[rank];
+            to->count = counts_here;
+            to->mass = masses_here;
+        }
+        cluster.sync();
+        uint32_t count_all = 0;
+        uint64_t mass_all = 0;
+        for (int i = 0; i < C; ++i) {
+            if (i < rank) s.counts_before += sh.all[i].count, s.masses_before += sh.all[i].mass;
+            count_all += sh.all[i].count;
+            mass_all += sh.all[i].mass;
+        }
+        Found in{kNone, 0, 0};  // the bin of the k-th value
+        if (cut_k && uint32_t(top_k) <= count_all) {  // (else the first k are all that have a weight)
+            r.template tell<false>(cluster, s, uint64_t(top_k));
+            cluster.sync();
+            in = sh.found[0];
+            if (r.single(in.bin)) {
+                within = Cut{r.bin_kd(in.bin), uint32_t(top_k) - in.count};
+                mass_all = in.mass;
+            } else {
+                within = r.template find<false>(cluster, in.bin, uint64_t(top_k), in.count, within, flip);
+                if (cut_p) mass_all = in.mass + r.mass_in(cluster, in.bin, within.kd);
+            }
+            mass_all += uint64_t(within.ties) * r.w(r.value_at(within.kd));
+            cut = shorter(cut, within);
+        }
+        if (cut_p) {
+            const uint64_t goal = uint64_t(ceil((top_p > 0.f ? double(top_p) : 1e-300) * double(mass_all)));
+            Found f = in;
+            if (in.bin == kNone || goal <= in.mass) {
+                r.template tell<true>(cluster, s, goal);
+                cluster.sync();
+                f = sh.found[1];
+            }
+            cut = shorter(cut, r.single(f.bin)
+                                   ? r.template reach<true>(r.bin_kd(f.bin), goal - f.mass, within)
+                                   : r.template find<true>(cluster, f.bin, goal, f.mass, within, flip));
+        }
+    }
 
-    // what is kept, warp by warp in the order of the columns
-    const int part = ((n + kWarps - 1) / kWarps + 31) / 32 * 32, c0 = warp * part, c1 = min(n, c0 + part);
+    // What this CTA holds before the cut and at it. bf16: by its own counts, unless the cut
+    // lies near zero; else by the columns, warp by warp in their order.
+    const int part = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const uint64_t one = cut.kd == kNone ? 0 : r.w(r.value_at(cut.kd));
     uint64_t mass = 0;
     uint32_t ties = 0;
-    for (int c = c0 + lane; c < c1; c += 32) {
-        const float v = E::load(x + c);
-        const uint32_t at = r.kd(v);
-        if (at < cut.kd) mass += r.w(v);
-        ties += at == cut.kd;
+    bool by_bins = false;
+    if constexpr (!R::kF32) {
+        uint32_t end = r.bins;  // the cut's bin
+        if (cut.kd != kNone) end = min(end, r.bin_of((r.top_key >> 16) - cut.kd));
+        by_bins = !r.near_zero(end);
+        if (by_bins) {
+            for (uint32_t b = threadIdx.x; b < end; b += kBlock)
+                if (!r.near_zero(b) && counts[b]) mass += counts[b] * r.w(r.value_at(r.bin_kd(b)));
+            mass = block_sum(mass, sh.warp_mass);
+            if (uint32_t(r.half) < end) mass += sh.near_zero;
+            ties = end < uint32_t(r.bins) ? counts[end] : 0;
+        }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    ties = __reduce_add_sync(0xffffffffu, ties);
-    if (lane == 0) sh.warp_mass[warp] = mass, sh.warp_count[warp] = ties;
-    __syncthreads();
-    if (threadIdx.x < C) {
-        Told t = {};
-        for (int i = 0; i < kWarps; ++i) t.mass += sh.warp_mass[i], t.ties += sh.warp_count[i];
-        Told* to = &cluster.map_shared_rank(&sh, threadIdx.x)->all[rank];
-        to->mass = t.mass;
-        to->ties = t.ties;
+    auto by_warps = [&] {
+        uint64_t m;
+        uint32_t t;
+        r.warp_sums(warp * part, min(n, (warp + 1) * part), cut, &m, &t);
+        __syncthreads();
+        if (lane == 0) sh.warp_mass[warp] = m, sh.warp_count[warp] = t;
+        __syncthreads();
+    };
+    if (!by_bins) {
+        by_warps();
+        for (int i = 0; i < kWarps; ++i) mass += sh.warp_mass[i], ties += sh.warp_count[i];
+    }
+    if (int(threadIdx.x) < C) {
+        Told* to = &cluster.map_shared_rank(&sh, threadIdx.x)->kept[rank];
+        to->mass = mass;
+        to->count = ties;
     }
     cluster.sync();
-    const uint64_t one = cut.kd == 0xffffffffu ? 0 : r.w(r.value_at(cut.kd));
     uint64_t sum = 0;
-    uint32_t tied = 0;  // of all CTAs
+    ties = 0;
     for (int i = 0; i < C; ++i) {
-        sum += sh.all[i].mass;
-        tied += sh.all[i].ties;
+        sum += sh.kept[i].mass;
+        ties += sh.kept[i].count;
     }
-    sum += uint64_t(min(tied, cut.ties)) * one;
+    sum += uint64_t(min(ties, cut.ties)) * one;
     const float u = a.u[row];
     uint64_t draw = u > 0.f ? uint64_t(double(u) * double(sum)) : 0;
     if (draw >= sum) draw = sum - 1;  // u of 1 and above: the last one kept
-    // the CTA, then the warp, then the lane in whose part the running sum exceeds the draw
-    uint32_t left = cut.ties;  // ties that still belong
-    bool here = false;
-    for (int i = 0; i <= rank; ++i) {
-        const uint32_t t = min(sh.all[i].ties, left);
-        const uint64_t m = sh.all[i].mass + t * one;
-        here = draw < m;
-        if (i == rank || here) {
-            here = here && i == rank;
-            break;
-        }
-        draw -= m;
-        left -= t;
+    // the CTA, the warp's columns, and the 32 columns in which the running sum exceeds the draw
+    uint32_t left = cut.ties;
+    if (which(C, one, &draw, &left, [&](int i, uint64_t* m, uint32_t* t) { *m = sh.kept[i].mass, *t = sh.kept[i].count; }) != rank)
+        return;
+    if (by_bins) by_warps();
+    auto of_warps = [&](int i, uint64_t* m, uint32_t* t) { *m = sh.warp_mass[i], *t = sh.warp_count[i]; };
+    int c0 = which(kWarps, one, &draw, &left, of_warps) * part;
+    int c1 = min(n, c0 + part);
+    if (part > 4 * 32) {  // every warp a sixteenth of them
+        const int less = ((c1 - c0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+        uint64_t m;
+        uint32_t t;
+        r.warp_sums(c0 + warp * less, min(c1, c0 + (warp + 1) * less), cut, &m, &t);
+        __syncthreads();
+        if (lane == 0) sh.warp_mass[warp] = m, sh.warp_count[warp] = t;
+        __syncthreads();
+        c0 += which(kWarps, one, &draw, &left, of_warps) * less;
+        c1 = min(c1, c0 + less);
     }
-    if (!here) return;
-    for (int i = 0; i <= warp; ++i) {
-        const uint32_t t = min(sh.warp_count[i], left);
-        const uint64_t m = sh.warp_mass[i] + t * one;
-        here = draw < m;
-        if (i == warp || here) {
-            here = here && i == warp;
-            break;
-        }
-        draw -= m;
-        left -= t;
-    }
-    if (!here) return;
+    if (warp != 0) return;
     for (int c = c0; c < c1; c += 32) {
         const float v = c + lane < c1 ? E::load(x + c + lane) : -INFINITY;
         const uint32_t at = r.kd(v);
@@ -410,10 +682,13 @@ cudaError_t launch(const SampleArgs& a, const LaunchCfg& cfg) {
         return t;
     }();
     constexpr int V = Elem<T>::kVec;
+    // Shares of 64 KB at most; while the CTAs are fewer than two an SM, of at least 4096 columns.
     int C = 1;
-    while (C < kCluster && (a.N + C - 1) / C * int(sizeof(T)) > 64 * 1024) C *= 2;
+    while (C < kCluster && ((a.N + C - 1) / C * int(sizeof(T)) > 64 * 1024 ||
+                            (a.M * C * 2 <= 2 * cfg.num_sms && a.N >= 2 * C * 4096)))
+        C *= 2;
     const int share = ((a.N + C - 1) / C + V - 1) / V * V;
-    const size_t smem = size_t(share) * sizeof(T);
+    const size_t smem = size_t(share) * sizeof(T) + size_t(kBinsHeld) * 4 * (sizeof(T) == 4 ? 4 : 1);
     auto k = sample_kernel<T>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, cfg);
     if (e != cudaSuccess) return e;

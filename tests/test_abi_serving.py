@@ -83,6 +83,6 @@ def test_sample_refusals(lib):
                 dict(token=TP), dict(token=MP), dict(token=LP), dict(lp=X + 64), dict(lp=U), dict(lp=T),
                 dict(lp=TK + 4), dict(lp=TP), dict(lp=MP)):
         assert f(*args(**bad)) == INVALID, bad
-    for bad in (dict(N=393217, ld=393217), dict(M=(1 << 27) + 1)):
+    for bad in (dict(N=327681, ld=327681), dict(M=(1 << 27) + 1)):
         assert f(*args(**bad)) == UNSUPPORTED, bad
     assert f(*args(M=0, x=None, u=None, token=None)) == OK

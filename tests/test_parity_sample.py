@@ -68,7 +68,7 @@ def test_widths(dtype, N):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("N", [65536, 131072, 200000, 393216])
+@pytest.mark.parametrize("N", [65536, 131072, 200000, 327680])
 def test_long_rows(dtype, N):
     x, u = place(rows(5, N, 3), dtype), uniform(5, 4)
     check(x, u)
@@ -256,7 +256,7 @@ def test_refusals():
     x, u = torch.zeros(4, 64, device="cuda"), torch.zeros(4, device="cuda")
     S = ro.rowops_sample
     for call in (lambda: S(x, u, temperature=-1.0), lambda: S(x, u, top_k=-1), lambda: S(x, u, top_p=-0.5),
-                 lambda: S(x, u, min_p=1.5), lambda: S(torch.zeros(1, 393217, device="cuda"), u[:1])):
+                 lambda: S(x, u, min_p=1.5), lambda: S(torch.zeros(1, 327681, device="cuda"), u[:1])):
         with pytest.raises(ro.RowopsError):
             call()
     for call in (lambda: S(x, u[:3]), lambda: S(x, u.double()), lambda: S(x, u, temperature=u[:3]),
