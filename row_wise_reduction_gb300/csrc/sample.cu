@@ -43,8 +43,7 @@ constexpr int kCluster = 8;  // the most CTAs of a row
 constexpr int kDigit = 256;  // bins of a digit
 // The histogram: 13 binades of 128 bins below the largest magnitude, for either sign, and one
 // bin for what is nearer to zero.
-constexpr int kHalf = 13 * 128, kBins = 2 * kHalf + 1, kBinsHeld = (kBins + 3) / 4 * 4;
-constexpr int kEach = (kBins + kBlock - 1) / kBlock;  // bins of a thread, in the CTA alone
+constexpr int kHalf = 13 * 128, kBins = 2 * kHalf + 1, kBinsHeld = (kBins + 1 + 31) / 32 * 32;
 constexpr int kFraction = 44;
 constexpr uint64_t kOne = uint64_t(1) << kFraction;
 
@@ -87,6 +86,18 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
+// two bf16 at a time; the maximum NaN where there is one
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // What the CTAs of a cluster tell one another.
 struct Told {
     float top, low;
@@ -112,7 +123,8 @@ struct Shared {
     Found found[2];       // by whoever has the bin
     uint64_t before;
     uint32_t bin;
-    float c_hi, c_lo, cutoff;
+    float c_hi, c_lo;
+    double min_p_below;   // T ln(min_p)
     uint32_t kd_min_p;
 };
 
@@ -123,6 +135,12 @@ struct Cut {
 constexpr uint32_t kNone = 0xffffffffu;
 __device__ __forceinline__ Cut shorter(Cut a, Cut b) {
     return a.kd != b.kd ? (a.kd < b.kd ? a : b) : Cut{a.kd, a.ties < b.ties ? a.ties : b.ties};
+}
+
+// All of the row's threads: what one has written in its CTA's shared memory, or in another's, is there.
+__device__ __forceinline__ void meet(cg::cluster_group& cluster) {
+    if (cluster.num_blocks() > 1) cluster.sync();
+    else __syncthreads();
 }
 
 // Sums over the CTA's threads, or what lies before a thread; every thread calls them.
@@ -159,6 +177,10 @@ __device__ __forceinline__ N block_before(N v, N* red, N* total) {
     return run - v;
 }
 
+// 32-bit words of the histogram: counts, and three of every bin's mass, or one and a half of its weight
+template <typename T>
+constexpr int kHeldWords = std::is_same_v<T, float> ? 4 * kBinsHeld : kBinsHeld / 2 * 5;
+
 template <typename T>
 struct Row {
     using E = Elem<T>;
@@ -166,6 +188,8 @@ struct Row {
     static constexpr int kKey = kF32 ? 32 : 16, kDrop = 32 - kKey;
     Shared& sh;
     uint32_t* counts;  // [kBinsHeld], and, fp32, three words of each bin's mass
+    uint64_t* part_masses;  // [bins / C], and their counts
+    uint32_t* part_counts;
     const T* x;        // this CTA's columns, -inf behind them up to a whole vector
     int n, C, rank;
     uint32_t top_key;
@@ -236,77 +260,115 @@ struct Row {
             for (int k = threadIdx.x; k * E::kVec < n; k += kBlock) {
                 const uint4 u = reinterpret_cast<const uint4*>(x)[k];
                 const uint32_t four[4] = {u.x, u.y, u.z, u.w};
+                bool any = false;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t b = e & 1 ? four[e / 2] >> 16 : four[e / 2] & 0xffffu;
-                    const int mag = int(b & 0x7fffu);
-                    const uint32_t bin = b & 0x8000u ? uint32_t(half + 1 - least + mag) : uint32_t(most - mag);
-                    if (mag < least) {
-                        atomicAdd(counts + half, 1u);
-                        near += w(__uint_as_float(b << 16));
-                    } else if (bin < uint32_t(bins)) {
-                        atomicAdd(counts + bin, 1u);
-                    }
+                    const int bin = held_bin(e & 1 ? four[e / 2] >> 16 : four[e / 2] & 0xffffu);
+                    any = any || bin == half;
+                    atomicAdd(counts + bin, 1u);
                 }
+                if (any)  // few: more than 13 binades below the largest
+#pragma unroll 1
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t b = x[k * 8 + e].bits;
+                        if (held_bin(b) == half) near += w(__uint_as_float(b << 16));
+                    }
             }
             near = block_sum(near, sh.warp_mass);
             if (threadIdx.x == 0) sh.near_zero = near;
         }
     }
+    // the bin of a bf16; the one behind all others for what is below them
+    __device__ __forceinline__ int held_bin(uint32_t b) const {
+        const int up = min(most - int(b), half), down = min(max(int(b) - 0x8000 + half + 1 - least, half), bins);
+        return b & 0x8000u ? down : up;
+    }
 
-    // A thread's share of the cluster's bins, added up over its CTAs.
+    // bf16: the weights of the bins that this CTA has something in, and of those of its part, 16 upper bits
+    // apart from the lower ones; near zero 0.
+    __device__ __forceinline__ uint64_t weight(int bin) const {
+        const uint16_t* upper = reinterpret_cast<const uint16_t*>(counts + 2 * kBinsHeld);
+        return uint64_t(upper[bin]) << 32 | counts[kBinsHeld + bin];
+    }
+    __device__ __forceinline__ void tabulate() const {
+        uint16_t* upper = reinterpret_cast<uint16_t*>(counts + 2 * kBinsHeld);
+        const int part = part_bins(), first = rank * part, end = first + part;
+#pragma unroll 2
+        for (int b = threadIdx.x; b <= bins; b += kBlock) {
+            const bool used = b < bins && b != half && (counts[b] || (b >= first && b < end));
+            const uint64_t one = used ? w(value_at(bin_kd(b))) : 0;
+            counts[kBinsHeld + b] = uint32_t(one);
+            upper[b] = uint16_t(one >> 32);
+        }
+        __syncthreads();
+    }
+
+    // The counts and masses of this CTA's part of the bins, over the cluster, in shared
+    // memory; a thread's share of them, their sums and what lies before them in the whole order.
     struct Share {
-        uint32_t first, count[kEach];
-        uint64_t mass[kEach];
-        int each;
-        uint32_t counts;         // of the share
-        uint64_t masses;
-        uint32_t counts_before;  // in the whole order
-        uint64_t masses_before;
+        int first, end;  // of the part
+        uint32_t count, count_before;
+        uint64_t mass, mass_before;
     };
+    __device__ __forceinline__ int part_bins() const { return (bins + C - 1) / C; }
     __device__ __forceinline__ void gather(cg::cluster_group& cluster, bool masses, Share& s) const {
-        s.each = (bins + C * kBlock - 1) / (C * kBlock);
-        s.first = uint32_t((rank * kBlock + int(threadIdx.x)) * s.each);
-        s.counts = 0, s.masses = 0;
+        const int part = part_bins(), each = (part + kBlock - 1) / kBlock;
+        constexpr int U = 2;  // bins on their way
+        for (int i0 = threadIdx.x; i0 < part; i0 += U * kBlock) {
+            uint32_t c[U] = {};
+            uint64_t m[U] = {};
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            s.count[i] = 0, s.mass[i] = 0;
-            const uint32_t bin = s.first + i;
-            if (i < s.each && bin < uint32_t(bins)) {
-                uint64_t mass = 0;
-                for (int r = 0; r < C; ++r) {
+            for (int r = 0; r < kCluster; ++r)
+                if (r < C) {
                     const uint32_t* o = cluster.map_shared_rank(counts, r);
-                    s.count[i] += o[bin];
-                    if (kF32 && masses)
-                        mass += o[kBinsHeld + bin] + (uint64_t(o[2 * kBinsHeld + bin]) << 16) +
-                                (uint64_t(o[3 * kBinsHeld + bin]) << 32);
-                    if (!kF32 && near_zero(bin)) mass += cluster.map_shared_rank(&sh, r)->near_zero;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int i = i0 + u * kBlock, bin = rank * part + i;
+                        if (i < part && bin < bins) {
+                            c[u] += o[bin];
+                            if (kF32 && masses)
+                                m[u] += o[kBinsHeld + bin] + (uint64_t(o[2 * kBinsHeld + bin]) << 16) +
+                                        (uint64_t(o[3 * kBinsHeld + bin]) << 32);
+                        }
+                    }
                 }
-                if (!kF32 && !near_zero(bin) && s.count[i]) mass = s.count[i] * w(value_at(bin_kd(bin)));
-                s.mass[i] = mass;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kBlock, bin = rank * part + i;
+                if (i >= part) break;
+                if (!kF32 && bin < bins) {
+                    m[u] = c[u] * weight(bin);
+                    if (near_zero(bin))
+                        for (int r = 0; r < C; ++r) m[u] += cluster.map_shared_rank(&sh, r)->near_zero;
+                }
+                part_counts[i] = c[u];
+                part_masses[i] = m[u];
             }
-            s.counts += s.count[i];
-            s.masses += s.mass[i];
+        }
+        __syncthreads();
+        s.first = min(int(threadIdx.x) * each, part);
+        s.end = min(s.first + each, part);
+        s.count = 0, s.mass = 0;
+        for (int i = s.first; i < s.end; ++i) {
+            s.count += part_counts[i];
+            s.mass += part_masses[i];
         }
     }
 
     // The thread in whose share the running count (or mass) reaches `goal` tells every CTA.
     template <bool MASS>
     __device__ __forceinline__ void tell(cg::cluster_group& cluster, const Share& s, uint64_t goal) const {
-        uint64_t run = MASS ? s.masses_before : s.counts_before;
-        if (run >= goal || run + (MASS ? s.masses : s.counts) < goal) return;
-        Found f{0, s.counts_before, s.masses_before};
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (i >= s.each) break;
-            run += MASS ? s.mass[i] : s.count[i];
-            if (run >= goal) {
-                f.bin = s.first + i;
-                break;
-            }
-            f.count += s.count[i];
-            f.mass += s.mass[i];
+        uint64_t run = MASS ? s.mass_before : s.count_before;
+        if (run >= goal || run + (MASS ? s.mass : s.count) < goal) return;
+        Found f{uint32_t(rank * part_bins()), s.count_before, s.mass_before};
+        int i = s.first;
+        for (;; ++i) {
+            run += MASS ? part_masses[i] : part_counts[i];
+            if (run >= goal || i + 1 >= s.end) break;
+            f.count += part_counts[i];
+            f.mass += part_masses[i];
         }
+        f.bin += uint32_t(i);
         for (int r = 0; r < C; ++r) cluster.map_shared_rank(&sh, r)->found[MASS] = f;
     }
 
@@ -334,7 +396,7 @@ struct Row {
                     atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[flip][d]), 1ull);
                 }
             });
-            cluster.sync();
+            meet(cluster);
             // a thread has a digit: its sum over the cluster, then what lies before it
             uint64_t mine = 0;
             if (threadIdx.x < kDigit) {
@@ -358,7 +420,7 @@ struct Row {
             before = sh.before;
         }
         // the last digit's bins are read until all have been here
-        cluster.sync();
+        meet(cluster);
         if (threadIdx.x < kDigit) sh.mass[flip ^ 1][threadIdx.x] = 0;
         __syncthreads();
         return reach<MASS>(from + prefix, goal - before, within);
@@ -383,44 +445,114 @@ struct Row {
         });
         mass = block_sum(mass, sh.warp_mass);
         if (int(threadIdx.x) < C) cluster.map_shared_rank(&sh, threadIdx.x)->kept[rank].mass = mass;
-        cluster.sync();
+        meet(cluster);
         mass = 0;
         for (int r = 0; r < C; ++r) mass += sh.kept[r].mass;
-        cluster.sync();  // (written again by the final sums)
+        meet(cluster);  // (written again by the final sums)
         return mass;
     }
 
-    // The sums of what a warp's columns [c0, c1) hold before the cut, and their ties at it.
-    __device__ __forceinline__ void warp_sums(int c0, int c1, Cut cut, uint64_t* mass, uint32_t* ties) const {
+    // The sums of what a warp's columns [c0, c1), whole vectors but for the row's end, hold before
+    // the cut, and their ties at it. table: the cut's bin, if that settles it; else -1.
+    __device__ __forceinline__ void warp_sums(int c0, int c1, Cut cut, int table, uint64_t* mass, uint32_t* ties) const {
         uint64_t m = 0;
         uint32_t t = 0;
-        for (int c = c0 + (threadIdx.x & 31); c < c1; c += 32) {
-            const float v = E::load(x + c);
-            const uint32_t at = kd(v);
-            if (at < cut.kd) m += w(v);
-            t += at == cut.kd;
+        const float at_cut = cut.kd == kNone ? -INFINITY : value_at(cut.kd);
+        for (int c = c0 + (threadIdx.x & 31) * E::kVec; c < c1; c += 32 * E::kVec) {
+            const uint4 u = *reinterpret_cast<const uint4*>(x + c);
+            if (!kF32 && table >= 0) {
+                const uint32_t four[4] = {u.x, u.y, u.z, u.w};
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < E::kVec; ++e) {
+                    const int bin = held_bin(e & 1 ? four[e / 2] >> 16 : four[e / 2] & 0xffffu);
+                    if (bin < table) m += weight(bin);
+                    t += bin == table;
+                    any = any || bin == half;
+                }
+                if (any && table > half)
+#pragma unroll 1
+                    for (int e = 0; e < E::kVec; ++e)
+                        if (held_bin(read_bits(c + e)) == half) m += w(E::load(x + c + e));
+                continue;
+            }
+            float v[E::kVec];
+            E::unpack(u, v);
+            float most_here = v[0];
+#pragma unroll
+            for (int e = 1; e < E::kVec; ++e) most_here = fmaxf(most_here, v[e]);
+            if (most_here < at_cut) continue;
+            if constexpr (kF32) {
+#pragma unroll
+                for (int e = 0; e < E::kVec; ++e) {
+                    const uint32_t at = kd(v[e]);
+                    if (at < cut.kd) m += w(v[e]);
+                    t += at == cut.kd;
+                }
+            } else {
+#pragma unroll 1
+                for (int e = 0; e < E::kVec; ++e) {
+                    const float one = E::load(x + c + e);
+                    const uint32_t at = kd(one);
+                    if (at < cut.kd) m += w(one);
+                    t += at == cut.kd;
+                }
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
         *mass = m;
         *ties = __reduce_add_sync(0xffffffffu, t);
     }
+    __device__ __forceinline__ uint32_t read_bits(int c) const {
+        if constexpr (kF32) return 0;
+        else return x[c].bits;
+    }
 };
 
-// Of the parts i = 0 .. parts - 1, in order, that in which the running sum exceeds *draw; *draw and *left
-// (the ties that still belong) become what they are at its begin.
-template <class Part>
-__device__ __forceinline__ int which(int parts, uint64_t one, uint64_t* draw, uint32_t* left, Part part) {
-    for (int i = 0;; ++i) {
-        uint64_t mass;
-        uint32_t ties;
-        part(i, &mass, &ties);
-        ties = min(ties, *left);
-        mass += ties * one;
-        if (*draw < mass || i + 1 == parts) return i;
-        *draw -= mass;
-        *left -= ties;
+// part * v, rounded down, or up: exact, where 64-bit floating point would do, at two
+// instructions a cycle and SM, what the CTA's every thread needs. part: not negative, at most 1 (above: as 1).
+__device__ __forceinline__ uint64_t part_of(float part, uint64_t v, bool up) {
+    if (part >= 1.f) return v;
+    const uint32_t b = __float_as_uint(part), e = b >> 23;
+    const uint64_t m = e ? (b & 0x7fffffu) | 0x800000u : b;  // part = m 2^-(150 - e)
+    const int s = 150 - int(e ? e : 1);                      // at least 24
+    uint64_t lo = v * m, hi = __umul64hi(v, m);
+    if (up) {  // (a part of 2^-128 and less is more than nothing)
+        if (s >= 128) return m != 0;
+        const uint64_t one = s >= 64 ? ~uint64_t(0) : (uint64_t(1) << s) - 1;
+        lo += one;
+        hi += (lo < one) + (s > 64 ? (uint64_t(1) << (s - 64)) - 1 : 0);
     }
+    return s >= 128 ? 0 : s >= 64 ? hi >> (s - 64) : (hi << (64 - s)) | (lo >> s);
+}
+
+// Of at most 32 parts in order, lane i's with a mass before the cut and ties at it, that in which the
+// running sum exceeds *draw; *draw and *left (the ties that still belong) become what they are at
+// its begin. Every lane of the warp calls it.
+__device__ __forceinline__ int which(uint64_t mass, uint32_t ties, int parts, uint64_t one, uint64_t* draw,
+                                     uint32_t* left) {
+    const int lane = threadIdx.x & 31;
+    if (lane >= parts) mass = 0, ties = 0;
+    uint32_t run_ties = ties;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t other = __shfl_up_sync(0xffffffffu, run_ties, o);
+        if (lane >= o) run_ties += other;
+    }
+    const uint32_t kept = min(run_ties, *left), before = min(run_ties - ties, *left);
+    mass += (kept - before) * one;
+    uint64_t run = mass;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t other = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += other;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, run > *draw);
+    const int i = past ? __ffs(past) - 1 : parts - 1;
+    *draw -= __shfl_sync(0xffffffffu, run - mass, i);
+    *left -= __shfl_sync(0xffffffffu, before, i);
+    return i;
 }
 
 template <typename T>
@@ -431,7 +563,10 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
     __shared__ Shared sh;
     extern __shared__ uint4 dynamic[];
     uint32_t* counts = reinterpret_cast<uint32_t*>(dynamic);
-    T* x = reinterpret_cast<T*>(counts + kBinsHeld * (R::kF32 ? 4 : 1));
+    uint64_t* part_masses = reinterpret_cast<uint64_t*>(counts + kHeldWords<T>);
+    const int part_room = kBinsHeld / int(cg::this_cluster().num_blocks());
+    uint32_t* part_counts = reinterpret_cast<uint32_t*>(part_masses + part_room);
+    T* x = reinterpret_cast<T*>(part_counts + part_room);
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank()), lane = threadIdx.x & 31,
               warp = threadIdx.x >> 5;
@@ -447,19 +582,39 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
         for (int c = whole * E::kVec + threadIdx.x; c < n; c += kBlock) x[c] = from[c];
         for (int c = n + threadIdx.x; c < (n + E::kVec - 1) / E::kVec * E::kVec; c += kBlock) E::store(x + c, -INFINITY);
         if (threadIdx.x < kDigit) sh.mass[0][threadIdx.x] = sh.mass[1][threadIdx.x] = 0;
-        for (int i = threadIdx.x; i < kBinsHeld * (R::kF32 ? 4 : 1); i += kBlock) counts[i] = 0;
+        for (int i = threadIdx.x; i < (R::kF32 ? 4 : 1) * kBinsHeld; i += kBlock) counts[i] = 0;
         if (threadIdx.x < 16) sh.roots[threadIdx.x] = roots.v[threadIdx.x];
-        asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        // what of the row's numbers needs 64 bits, by a thread each while the copies are on their way
+        if (threadIdx.x == 32) {
+            const double c = 1.4426950408889634 / double(temperature);
+            sh.c_hi = float(c);
+            sh.c_lo = float(c - double(sh.c_hi));
+        }
+        if (threadIdx.x == 64 && min_p > 0.f)
+            sh.min_p_below = double(temperature) * log(double(min_p < 1.f ? min_p : 1.f));
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
     }
-    R r{sh, counts, x, n, C, rank, 0, {}, 0, 0, 0, 0};
+    R r{sh, counts, part_masses, part_counts, x, n, C, rank, 0, {}, 0, 0, 0, 0};
 
     // the maximum, NaN where there is one, and the minimum
     float top = -INFINITY, low = INFINITY;
-    r.each([&](float v) {
-        top = max_nan(top, v);
-        low = fminf(low, v);
-    });
+    if constexpr (R::kF32) {
+        r.each([&](float v) {
+            top = max_nan(top, v);
+            low = fminf(low, v);
+        });
+    } else {
+        uint32_t t2 = 0xff80ff80u, l2 = 0x7f807f80u;  // two at a time
+        for (int k = threadIdx.x; k * 8 < n; k += kBlock) {
+            const uint4 u = reinterpret_cast<const uint4*>(x)[k];
+            t2 = max2_nan(t2, max2_nan(max2_nan(u.x, u.y), max2_nan(u.z, u.w)));
+            l2 = min2(l2, min2(min2(u.x, u.y), min2(u.z, u.w)));
+        }
+        top = max_nan(__uint_as_float(t2 << 16), __uint_as_float(t2 & 0xffff0000u));
+        low = fminf(__uint_as_float(l2 << 16), __uint_as_float(l2 & 0xffff0000u));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -467,15 +622,25 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
     }
     if (lane == 0) sh.warp_top[warp] = top, sh.warp_low[warp] = low;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kWarps; ++i) top = max_nan(top, sh.warp_top[i]), low = fminf(low, sh.warp_low[i]);
-        sh.own.top = top, sh.own.low = low;
+    if (warp == 0) {
+        top = sh.warp_top[lane % kWarps], low = sh.warp_low[lane % kWarps];
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+        }
+        if (lane == 0) sh.own.top = top, sh.own.low = low;
     }
-    cluster.sync();
-    top = -INFINITY, low = INFINITY;
-    for (int i = 0; i < C; ++i) {
-        const Told& o = cluster.map_shared_rank(&sh, i)->own;
-        top = max_nan(top, o.top), low = fminf(low, o.low);
+    meet(cluster);
+    {
+        const Told& o = cluster.map_shared_rank(&sh, min(lane, C - 1))->own;
+        top = o.top, low = o.low;
+#pragma unroll
+        for (int d = kCluster / 2; d > 0; d >>= 1) {
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, d));
+        }
+        top = __shfl_sync(0xffffffffu, top, 0), low = __shfl_sync(0xffffffffu, low, 0);
     }
     top += 0.f;
     const bool none = !(top > -INFINITY);  // a NaN, or nothing to draw from
@@ -497,7 +662,7 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
             for (int i = 1; i < kWarps; ++i) first = min(first, int(sh.warp_count[i]));
             cluster.map_shared_rank(&sh, 0)->all[rank].first = first;
         }
-        cluster.sync();
+        meet(cluster);
         if (rank == 0 && threadIdx.x == 0) {
             for (int i = 0; i < C; ++i) first = min(first, sh.all[i].first);
             a.token[row] = none ? -1 : first;
@@ -506,16 +671,11 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
         return;
     }
 
-    // the row's numbers in 64 bits, once
     if (threadIdx.x == 0) {
-        const double c = 1.4426950408889634 / double(temperature);
-        sh.c_hi = float(c);
-        sh.c_lo = float(c - double(sh.c_hi));
-        sh.cutoff = float(double(top) - 43.7 * double(temperature));  // below: weights of 0 (2^-63)
         // the smallest value that min-p keeps: (x - m) / T >= ln(min_p)
         sh.kd_min_p = kNone;
         if (min_p > 0.f) {
-            const double least = double(top) + double(temperature) * log(double(min_p < 1.f ? min_p : 1.f));
+            const double least = double(top) + sh.min_p_below;
             const float up = least > -3.4028234e38 ? __double2float_ru(least) : -INFINITY;
             uint32_t key = ordered(up);
             if (R::kDrop && (key & 0x80000000u)) key += 0xffffu;  // the next bf16 (below zero: cut off, it is that)
@@ -524,38 +684,39 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
     }
     __syncthreads();
     r.w = Weights{top, sh.c_hi, sh.c_lo, sh.roots};
-    r.choose_bins(fmaxf(low, sh.cutoff));
+    r.choose_bins(fmaxf(low, top - 43.7f * temperature));  // below: weights of 0 (2^-63)
     const bool cut_k = top_k > 0 && top_k < a.N, cut_p = top_p < 1.f;
     Cut cut{sh.kd_min_p, kNone}, within{kNone, 0u};
     if (!R::kF32 || cut_k || cut_p) {
         r.count(cut_p);
+        if constexpr (!R::kF32) r.tabulate();
     }
     if (cut_k || cut_p) {
-        cluster.sync();
+        meet(cluster);
         int flip = 0;
         typename R::Share s;
         r.gather(cluster, cut_p, s);
         uint32_t counts_here;
         uint64_t masses_here;
-        s.counts_before = block_before(s.counts, sh.warp_count, &counts_here);
-        s.masses_before = block_before(s.masses, sh.warp_mass, &masses_here);
+        s.count_before = block_before(s.count, sh.warp_count, &counts_here);
+        s.mass_before = block_before(s.mass, sh.warp_mass, &masses_here);
         if (int(threadIdx.x) < C) {
             Told* to = &cluster.map_shared_rank(&sh, threadIdx.x)->all[rank];
             to->count = counts_here;
             to->mass = masses_here;
         }
-        cluster.sync();
+        meet(cluster);
         uint32_t count_all = 0;
         uint64_t mass_all = 0;
         for (int i = 0; i < C; ++i) {
-            if (i < rank) s.counts_before += sh.all[i].count, s.masses_before += sh.all[i].mass;
+            if (i < rank) s.count_before += sh.all[i].count, s.mass_before += sh.all[i].mass;
             count_all += sh.all[i].count;
             mass_all += sh.all[i].mass;
         }
         Found in{kNone, 0, 0};  // the bin of the k-th value
         if (cut_k && uint32_t(top_k) <= count_all) {  // (else the first k are all that have a weight)
             r.template tell<false>(cluster, s, uint64_t(top_k));
-            cluster.sync();
+            meet(cluster);
             in = sh.found[0];
             if (r.single(in.bin)) {
                 within = Cut{r.bin_kd(in.bin), uint32_t(top_k) - in.count};
@@ -568,11 +729,11 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
             cut = shorter(cut, within);
         }
         if (cut_p) {
-            const uint64_t goal = uint64_t(ceil((top_p > 0.f ? double(top_p) : 1e-300) * double(mass_all)));
+            const uint64_t goal = max(part_of(fmaxf(top_p, 0.f), mass_all, true), uint64_t(1));
             Found f = in;
             if (in.bin == kNone || goal <= in.mass) {
                 r.template tell<true>(cluster, s, goal);
-                cluster.sync();
+                meet(cluster);
                 f = sh.found[1];
             }
             cut = shorter(cut, r.single(f.bin)
@@ -583,18 +744,19 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
 
     // What this CTA holds before the cut and at it. bf16: by its own counts, unless the cut
     // lies near zero; else by the columns, warp by warp in their order.
-    const int part = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int part = ((n + kWarps - 1) / kWarps + 32 * E::kVec - 1) / (32 * E::kVec) * (32 * E::kVec);
     const uint64_t one = cut.kd == kNone ? 0 : r.w(r.value_at(cut.kd));
     uint64_t mass = 0;
     uint32_t ties = 0;
     bool by_bins = false;
+    int table = -1;
     if constexpr (!R::kF32) {
         uint32_t end = r.bins;  // the cut's bin
         if (cut.kd != kNone) end = min(end, r.bin_of((r.top_key >> 16) - cut.kd));
         by_bins = !r.near_zero(end);
         if (by_bins) {
-            for (uint32_t b = threadIdx.x; b < end; b += kBlock)
-                if (!r.near_zero(b) && counts[b]) mass += counts[b] * r.w(r.value_at(r.bin_kd(b)));
+            table = int(end);
+            for (uint32_t b = threadIdx.x; b < end; b += kBlock) mass += counts[b] * r.weight(int(b));
             mass = block_sum(mass, sh.warp_mass);
             if (uint32_t(r.half) < end) mass += sh.near_zero;
             ties = end < uint32_t(r.bins) ? counts[end] : 0;
@@ -603,7 +765,7 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
     auto by_warps = [&] {
         uint64_t m;
         uint32_t t;
-        r.warp_sums(warp * part, min(n, (warp + 1) * part), cut, &m, &t);
+        r.warp_sums(warp * part, min(n, (warp + 1) * part), cut, table, &m, &t);
         __syncthreads();
         if (lane == 0) sh.warp_mass[warp] = m, sh.warp_count[warp] = t;
         __syncthreads();
@@ -617,7 +779,7 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
         to->mass = mass;
         to->count = ties;
     }
-    cluster.sync();
+    meet(cluster);
     uint64_t sum = 0;
     ties = 0;
     for (int i = 0; i < C; ++i) {
@@ -626,25 +788,28 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
     }
     sum += uint64_t(min(ties, cut.ties)) * one;
     const float u = a.u[row];
-    uint64_t draw = u > 0.f ? uint64_t(double(u) * double(sum)) : 0;
+    uint64_t draw = u > 0.f ? part_of(u, sum, false) : 0;
     if (draw >= sum) draw = sum - 1;  // u of 1 and above: the last one kept
     // the CTA, the warp's columns, and the 32 columns in which the running sum exceeds the draw
     uint32_t left = cut.ties;
-    if (which(C, one, &draw, &left, [&](int i, uint64_t* m, uint32_t* t) { *m = sh.kept[i].mass, *t = sh.kept[i].count; }) != rank)
-        return;
+    const Told& mine = sh.kept[min(lane, kCluster - 1)];
+    if (which(mine.mass, mine.count, C, one, &draw, &left) != rank) return;
     if (by_bins) by_warps();
-    auto of_warps = [&](int i, uint64_t* m, uint32_t* t) { *m = sh.warp_mass[i], *t = sh.warp_count[i]; };
-    int c0 = which(kWarps, one, &draw, &left, of_warps) * part;
+    auto of_warps = [&] {
+        const int i = min(lane, kWarps - 1);
+        return which(sh.warp_mass[i], sh.warp_count[i], kWarps, one, &draw, &left);
+    };
+    int c0 = of_warps() * part;
     int c1 = min(n, c0 + part);
     if (part > 4 * 32) {  // every warp a sixteenth of them
-        const int less = ((c1 - c0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+        const int less = ((c1 - c0 + kWarps - 1) / kWarps + 31) / 32 * 32;  // (whole vectors)
         uint64_t m;
         uint32_t t;
-        r.warp_sums(c0 + warp * less, min(c1, c0 + (warp + 1) * less), cut, &m, &t);
+        r.warp_sums(c0 + warp * less, min(c1, c0 + (warp + 1) * less), cut, table, &m, &t);
         __syncthreads();
         if (lane == 0) sh.warp_mass[warp] = m, sh.warp_count[warp] = t;
         __syncthreads();
-        c0 += which(kWarps, one, &draw, &left, of_warps) * less;
+        c0 += of_warps() * less;
         c1 = min(c1, c0 + less);
     }
     if (warp != 0) return;
@@ -663,9 +828,9 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
         if (past) {
             if (lane == __ffs(past) - 1) {
                 a.token[row] = lo + c + lane;
-                if (a.logprob)
-                    a.logprob[row] = float((v == top ? 0. : (double(v) - double(top)) / double(temperature)) -
-                                           log(double(sum) * 0x1p-44));
+                if (a.logprob)  // two terms of one sign; sum is at least one
+                    a.logprob[row] = -((v == top ? 0.f : (top - v) / temperature) +
+                                       log1pf(float(sum - kOne) * 0x1p-44f));
             }
             return;
         }
@@ -688,7 +853,7 @@ cudaError_t launch(const SampleArgs& a, const LaunchCfg& cfg) {
                             (a.M * C * 2 <= 2 * cfg.num_sms && a.N >= 2 * C * 4096)))
         C *= 2;
     const int share = ((a.N + C - 1) / C + V - 1) / V * V;
-    const size_t smem = size_t(share) * sizeof(T) + size_t(kBinsHeld) * 4 * (sizeof(T) == 4 ? 4 : 1);
+    const size_t smem = size_t(share) * sizeof(T) + size_t(kHeldWords<T>) * 4 + size_t(kBinsHeld / C) * 12;
     auto k = sample_kernel<T>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, cfg);
     if (e != cudaSuccess) return e;
