@@ -53,9 +53,8 @@ __device__ __forceinline__ bool paged_beyond(const PagedArgs& a, int b) { return
 
 // The tiles of single units over all sequences, and over those before b. `red`: two int64 a
 // warp. Every thread of the CTA calls it.
-template <int TILE>
+template <int TILE, int THREADS>
 __device__ __forceinline__ void paged_count(const PagedArgs& a, int b, int64_t* red, int64_t* total, int64_t* before) {
-    constexpr int THREADS = kPagedBlock;
     int64_t all = 0, some = 0;
     uint32_t n, f, base;
     for (int i = threadIdx.x; i < a.B; i += THREADS) {
@@ -153,10 +152,11 @@ struct PagedCursor {
     }
 };
 
-// What a unit's part is in the workspace: rows of DT weighted values, then a maximum and a sum each.
+// What a unit's part is in the workspace: rows of DT weighted values, then a maximum and a sum each
+// (rounded up to whole vectors).
 template <int DT, int ROWS>
 __device__ __forceinline__ constexpr int paged_part_floats() {
-    return ROWS * (DT + 2);
+    return (ROWS * (DT + 2) + 3) / 4 * 4;
 }
 
 template <class P>
@@ -302,18 +302,22 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
 }
 
 // The units that no CTA has written: those cut by a border, joined from their parts in
-// order, and those without a position. CTA (x, y): sequence x, every gridDim.y-th unit.
+// order, and those without a position. CTA (x, y): sequence x, every gridDim.y-th unit; a warp has a
+// row: first every part's maximum (a lane each), then 32 parts at a time, whose values are
+// loaded eight at a time (one after the other they took 32 us where a unit has 19 parts, of the 185 of a call).
+constexpr int kJoinWarps = 8;
 template <class P>
-__global__ void __launch_bounds__(kPagedBlock) paged_join_kernel(const __grid_constant__ PagedArgs a, const float* parts,
-                                                                 int blocks, int ctas) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedArgs a,
+                                                                     const float* parts, int blocks, int ctas) {
     using T = typename P::T;
     using E = Elem<T>;
-    constexpr int TILE = P::kTokens * kPagedWarps, DT = P::kD, ROWS = P::kRows;
-    __shared__ int64_t red[kPagedWarps * 2];
+    constexpr int TILE = P::kTokens * kPagedWarps, DT = P::kD, ROWS = P::kRows, VECTORS = DT / 4,
+                  EACH = (VECTORS + 31) / 32, FLOATS = paged_part_floats<DT, ROWS>();
+    __shared__ int64_t red[kJoinWarps * 2];
     const int b = blockIdx.x, units = int(a.kv_heads) * blocks, group = int(a.heads / a.kv_heads);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t total, before;
-    paged_count<TILE>(a, b, red, &total, &before);
+    paged_count<TILE, 32 * kJoinWarps>(a, b, red, &total, &before);
     total *= units;
     if (ctas > total) ctas = int(total);
     uint32_t n, first, base;
@@ -323,29 +327,50 @@ __global__ void __launch_bounds__(kPagedBlock) paged_join_kernel(const __grid_co
     for (int j = blockIdx.y; j < units; j += gridDim.y) {
         // tile t is CTA c's where total c / ctas <= t < total (c + 1) / ctas, rounded down
         const int64_t t0 = before * units + j * tiles, t1 = t0 + tiles - 1;
-        const int c0 = tiles ? int(((t0 + 1) * ctas - 1) / total) : 0, c1 = tiles ? int(((t1 + 1) * ctas - 1) / total) : 0;
+        const int c0 = tiles ? int(((t0 + 1) * ctas - 1) / total) : 0, c1 = tiles ? int(((t1 + 1) * ctas - 1) / total) : -1;
         if (tiles && c0 == c1) continue;
         const int head = j / blocks * group + j % blocks * ROWS, rows = min(ROWS, group - j % blocks * ROWS);
-        for (int r = warp; r < rows; r += kPagedWarps) {
-            float m = -INFINITY, l = 0.f, acc[(DT + 31) / 32] = {};
-            if (tiles)
-                for (int c = c0; c <= c1; ++c) {
-                    const float* part = parts + (int64_t(c) * 2 + (c == c0)) * paged_part_floats<DT, ROWS>();
-                    const float pm = part[ROWS * DT + 2 * r], pl = part[ROWS * DT + 2 * r + 1];
-                    const float next = fmaxf(m, pm), zero = next == -INFINITY ? 0.f : next;
-                    const float keep = ex2_approx(m - zero), take = ex2_approx(pm - zero);
-                    l = l * keep + (pm == -INFINITY ? pl : pl * take);
+        // the CTA that the unit begins in left its part behind that of the unit it began with itself
+        auto part = [&](int c) { return parts + (int64_t(c) * 2 + (c == c0)) * FLOATS; };
+        for (int r = warp; r < rows; r += kJoinWarps) {
+            float m = -INFINITY, l = 0.f;
+            for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, part(c)[ROWS * DT + 2 * r]);
 #pragma unroll
-                    for (int i = 0; i < (DT + 31) / 32; ++i)
-                        if (i * 32 + lane < DT) acc[i] = acc[i] * keep + part[r * DT + i * 32 + lane] * take;
-                    m = next;
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float4 acc[EACH] = {};
+            for (int c = c0; c <= c1; c += 32) {
+                const int here = min(32, c1 - c + 1);
+                float take = 0.f;
+                if (lane < here) {
+                    const float* p = part(c + lane) + ROWS * DT + 2 * r;
+                    take = m == -INFINITY ? 0.f : ex2_approx(p[0] - m);
+                    l += m == -INFINITY ? p[1] : p[1] * take;
                 }
+#pragma unroll 8
+                for (int i = 0; i < here; ++i) {
+                    const float w = __shfl_sync(0xffffffffu, take, i);
+                    const float4* p = reinterpret_cast<const float4*>(part(c + i) + r * DT);
+#pragma unroll
+                    for (int e = 0; e < EACH; ++e)
+                        if (lane + 32 * e < VECTORS) {
+                            const float4 v = p[lane + 32 * e];
+                            acc[e].x = fmaf(v.x, w, acc[e].x), acc[e].y = fmaf(v.y, w, acc[e].y);
+                            acc[e].z = fmaf(v.z, w, acc[e].z), acc[e].w = fmaf(v.w, w, acc[e].w);
+                        }
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             if (beyond) l = NAN;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             T* o = static_cast<T*>(a.out) + b * a.ldo + int64_t(head + r) * a.D;
 #pragma unroll
-            for (int i = 0; i < (DT + 31) / 32; ++i)
-                if (i * 32 + lane < a.D) E::store(o + i * 32 + lane, acc[i] * inv);
+            for (int e = 0; e < EACH; ++e) {
+                const float v[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * (lane + 32 * e) + i < a.D) E::store(o + 4 * (lane + 32 * e) + i, v[i] * inv);
+            }
             if (lane == 0 && a.lse) a.lse[b * a.heads + head + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
         }
     }
@@ -373,7 +398,7 @@ cudaError_t paged_launch(const PagedArgs& a, void* workspace, int blocks, const 
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(unsigned(a.B), unsigned(std::min<int64_t>(units, std::max<int64_t>(1, 2048 / a.B))));
-    lc.blockDim = dim3(kPagedBlock);
+    lc.blockDim = dim3(32 * kJoinWarps);
     lc.stream = cfg.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
