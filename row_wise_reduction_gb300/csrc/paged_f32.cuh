@@ -14,7 +14,7 @@ namespace rowops {
 template <int DT, int G>
 struct PagedF32 {
     using T = float;
-    static constexpr int kTokens = 8, kRows = G, kD = DT, kOwn = G;
+    static constexpr int kTokens = 8, kRows = G, kD = DT, kOwn = G, kPitch = DT;
     static constexpr int kVectors = DT / 4, kHalves = kVectors <= 16 ? 2 : 1, kEach = (kVectors + 31) / 32;
     static constexpr int kHeads = G > 4 ? G / 4 : 1;
     static constexpr size_t kScratch = size_t(G) * DT * 4 + size_t(kPagedWarps) * G * 9 * 4 + 16;

@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
     constexpr int TK = P::kTokens, TILE = TK * kPagedWarps, S = Ring::kStages, DT = P::kD, ROWS = P::kRows;
     extern __shared__ uint4 smem[];
     char* ring = reinterpret_cast<char*>(smem) + (threadIdx.x >> 5) * (2 * Ring::kPart) * S;
-    float* joined = reinterpret_cast<float*>(reinterpret_cast<char*>(smem) + Ring::kBytes);  // [ROWS][DT]
-    float* scratch = joined + ROWS * DT;                                                     // P's own
+    float* joined = reinterpret_cast<float*>(reinterpret_cast<char*>(smem) + Ring::kBytes);  // [ROWS][P::kPitch]
+    float* scratch = joined + ROWS * P::kPitch;                                                     // P's own
     __shared__ float tops[kPagedWarps][ROWS], sums[kPagedWarps][ROWS];
     __shared__ int64_t found[kPagedBlock / 32 * 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units = int(a.kv_heads) * blocks;
@@ -189,45 +189,73 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
 
     PagedCursor<TILE> in(a, units, b, begin - before * units, end - begin), at = in;
     uint32_t bad = 0;  // ring slots with a position whose page is none
+    // Where pages are whole pieces, a piece lies within a page: one entry, and rows a stride apart.
+    const uint32_t slots = uint32_t(a.page);
+    const bool paged = whole && slots % TK == 0;
     int page = 0;
-    auto look = [&] {  // the page of this lane's position in the piece to come
-        const uint32_t t = in.base + in.tile * TILE + warp * TK + lane;
-        if (in.left > 0 && lane < TK && t >= in.first && t < in.n)
-            page = a.table[int64_t(in.b) * a.table_ld + t / uint32_t(a.page)];
+    auto look = [&] {  // the page of the piece to come, or of this lane's position of it
+        const uint32_t t = in.base + in.tile * TILE + warp * TK + (paged ? 0 : lane);
+        if (in.left > 0 && (paged ? t + TK > in.first : lane < TK && t >= in.first) && t < in.n)
+            page = a.table[int64_t(in.b) * a.table_ld + t / slots];
     };
+    constexpr int kRow = DT * int(sizeof(T)) / 16, kLanes = kRow > 16 ? 32 : kRow > 8 ? 16 : 8, kRows = 32 / kLanes;
+    const int r0 = lane / kLanes, v0 = lane % kLanes, vectors = int(a.D) / E::kVec;
     auto ask = [&](int slot) {
         if (in.left > 0) {
-            const uint32_t t = in.base + in.tile * TILE + warp * TK + lane;
-            const bool live = lane < TK && t >= in.first && t < in.n, there = live && page >= 0 && page < a.pages;
-            int64_t off = -1;
-            if (there)
-                off = page * a.page_stride + int64_t(t % uint32_t(a.page)) * a.slot_stride +
-                      int64_t(in.j / blocks) * a.head_stride;
-            bad = __any_sync(0xffffffffu, live && !there) ? bad | 1u << slot : bad & ~(1u << slot);
+            const uint32_t t0 = in.base + in.tile * TILE + warp * TK, t = t0 + lane;
             char* to = ring + slot * 2 * Ring::kPart;
-            if (whole) {
-                constexpr int kRow = DT * int(sizeof(T)) / 16, kLanes = kRow > 16 ? 32 : kRow > 8 ? 16 : 8;
-                const int r0 = lane / kLanes, v = lane % kLanes, vectors = int(a.D) / E::kVec;
+            const int64_t head = int64_t(in.j / blocks) * a.head_stride;
+            if (paged) {
+                const int lo = int(in.first) - int(t0), hi = int(in.n) - int(t0);
+                const bool there = page >= 0 && page < a.pages;
+                const bool live = hi > 0 && lo < TK;
+                bad = live && !there ? bad | 1u << slot : bad & ~(1u << slot);
+                const int64_t from = (there && live ? page * a.page_stride + (t0 % slots) * a.slot_stride + head +
+                                                          r0 * a.slot_stride
+                                                    : 0) + v0 * E::kVec;
+                const T* k = static_cast<const T*>(a.k) + from;
+                const T* v = static_cast<const T*>(a.v) + from;
+                const int64_t step = there && live ? kRows * a.slot_stride : 0;
+                char* at = to + r0 * Ring::kPitch + v0 * 16;
 #pragma unroll
-                for (int r = 0; r < TK; r += 32 / kLanes) {
-                    const int64_t o = __shfl_sync(0xffffffffu, off, r + r0);
+                for (int r = 0; r < TK; r += kRows) {
+                    const unsigned bytes = there && r + r0 >= lo && r + r0 < hi ? 16u : 0u;
 #pragma unroll
                     for (int i = 0; i < kRow; i += kLanes)
-                        if (v + i < vectors) {
-                            char* k = to + (r + r0) * Ring::kPitch + (v + i) * 16;
-                            const int64_t from = (o < 0 ? 0 : o) + (v + i) * E::kVec;
-                            copy_async_part(k, static_cast<const T*>(a.k) + from, o < 0 ? 0u : 16u);
-                            copy_async_part(k + Ring::kPart, static_cast<const T*>(a.v) + from, o < 0 ? 0u : 16u);
+                        if (v0 + i < vectors) {
+                            copy_async_part(at + i * 16, k + i * E::kVec, bytes);
+                            copy_async_part(at + i * 16 + Ring::kPart, v + i * E::kVec, bytes);
                         }
+                    at += kRows * Ring::kPitch;
+                    k += step;
+                    v += step;
                 }
             } else {
-                for (int r = 0; r < TK; ++r) {
-                    const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                    T* k = reinterpret_cast<T*>(to + r * Ring::kPitch);
-                    T* v = reinterpret_cast<T*>(to + r * Ring::kPitch + Ring::kPart);
-                    for (int d = lane; d < a.D; d += 32) {
-                        k[d] = o < 0 ? T{} : static_cast<const T*>(a.k)[o + d];
-                        v[d] = o < 0 ? T{} : static_cast<const T*>(a.v)[o + d];
+                const bool live = lane < TK && t >= in.first && t < in.n, there = live && page >= 0 && page < a.pages;
+                const int64_t off = there ? page * a.page_stride + int64_t(t % slots) * a.slot_stride + head : -1;
+                bad = __any_sync(0xffffffffu, live && !there) ? bad | 1u << slot : bad & ~(1u << slot);
+                if (whole) {
+#pragma unroll
+                    for (int r = 0; r < TK; r += kRows) {
+                        const int64_t o = __shfl_sync(0xffffffffu, off, r + r0);
+#pragma unroll
+                        for (int i = 0; i < kRow; i += kLanes)
+                            if (v0 + i < vectors) {
+                                char* k = to + (r + r0) * Ring::kPitch + (v0 + i) * 16;
+                                const int64_t from = (o < 0 ? 0 : o) + (v0 + i) * E::kVec;
+                                copy_async_part(k, static_cast<const T*>(a.k) + from, o < 0 ? 0u : 16u);
+                                copy_async_part(k + Ring::kPart, static_cast<const T*>(a.v) + from, o < 0 ? 0u : 16u);
+                            }
+                    }
+                } else {
+                    for (int r = 0; r < TK; ++r) {
+                        const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                        T* k = reinterpret_cast<T*>(to + r * Ring::kPitch);
+                        T* v = reinterpret_cast<T*>(to + r * Ring::kPitch + Ring::kPart);
+                        for (int d = lane; d < a.D; d += 32) {
+                            k[d] = o < 0 ? T{} : static_cast<const T*>(a.k)[o + d];
+                            v[d] = o < 0 ? T{} : static_cast<const T*>(a.v)[o + d];
+                        }
                     }
                 }
             }
@@ -281,13 +309,13 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
                 for (int w = 0; w < kPagedWarps; ++w)
                     l += m == -INFINITY ? sums[w][r] : sums[w][r] * ex2_approx(tops[w][r] - m);
                 if (part) {
-                    for (int d = lane; d < DT; d += 32) out[r * DT + d] = joined[r * DT + d];
+                    for (int d = lane; d < DT; d += 32) out[r * DT + d] = joined[r * P::kPitch + d];
                     if (lane == 0) out[ROWS * DT + 2 * r] = m, out[ROWS * DT + 2 * r + 1] = l;
                 } else {
                     if (paged_beyond(a, at.b)) l = NAN;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     T* o = static_cast<T*>(a.out) + at.b * a.ldo + int64_t(head + r) * a.D;
-                    for (int d = lane; d < a.D; d += 32) E::store(o + d, joined[r * DT + d] * inv);
+                    for (int d = lane; d < a.D; d += 32) E::store(o + d, joined[r * P::kPitch + d] * inv);
                     if (lane == 0 && a.lse)
                         a.lse[at.b * a.heads + head + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
                 }
@@ -387,7 +415,7 @@ cudaError_t paged_launch(const PagedArgs& a, void* workspace, int blocks, const 
     const int64_t units = a.kv_heads * blocks, room = a.max_pages * a.page,
                   most = a.window > 0 ? std::min(room, a.window + 15) : room;
     const int64_t tiles = std::min<int64_t>((most + TILE - 1) / TILE * units, 1 << 20) * a.B;
-    const size_t smem = P::Ring::kBytes + size_t(P::kRows) * P::kD * 4 + P::kScratch;
+    const size_t smem = P::Ring::kBytes + size_t(P::kRows) * P::kPitch * 4 + P::kScratch;
     auto k = paged_attention_kernel<P>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, cfg);
     if (e != cudaSuccess) return e;

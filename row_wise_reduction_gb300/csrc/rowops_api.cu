@@ -1511,7 +1511,7 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
     const PagedArgs a = {q, k, v, page_table, lengths, out, lse, scale, window, B, heads, kv_heads, D, pages, page,
                          max_pages, ldt, ldq, ldo, page_stride, slot_stride, head_stride};
     const int rows = paged_rows(heads / kv_heads, es);
-    return finish((rows == 16  ? paged_attention_bf16
+    return finish((es == 2     ? paged_attention_bf16
                    : rows == 8 ? paged_attention_f32_g8
                    : rows == 4 ? paged_attention_f32_g4
                                : paged_attention_f32_g1)(a, workspace, cfg));

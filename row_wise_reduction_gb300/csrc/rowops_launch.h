@@ -463,7 +463,7 @@ inline int paged_width(int64_t D) {
         if (D <= w) return w;
     return 0;
 }
-inline int paged_rows(int64_t group, int es) { return es == 2 ? 16 : group > 4 ? 8 : group > 1 ? 4 : 1; }
+inline int paged_rows(int64_t group, int es) { return es == 2 ? (group > 8 ? 16 : 8) : group > 4 ? 8 : group > 1 ? 4 : 1; }
 inline size_t paged_bytes(int64_t group, int64_t D, int es) {
     return size_t(kPagedMaxCtas) * 2 * ((paged_rows(group, es) * (paged_width(D) + 2) + 3) / 4 * 4) * 4;
 }
