@@ -637,8 +637,8 @@ rowops_status_t rowops_rmsnorm_quant(const void* x, const void* residual, void* 
  * on the device, so a captured graph replays with those of the day. k and v at 16-byte
  * aligned heads of whole 16-byte vectors are the fastest.
  */
-size_t rowops_paged_attention_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
-                                              rowops_dtype_t dtype);
+size_t rowops_paged_attention_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t page,
+                                              int64_t max_pages, int64_t window, rowops_dtype_t dtype);
 rowops_status_t rowops_paged_attention(const void* q, const void* k, const void* v, const int32_t* page_table,
                                        const int32_t* lengths, void* out, float* lse, float scale, int64_t window,
                                        int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t ldq, int64_t ldo,

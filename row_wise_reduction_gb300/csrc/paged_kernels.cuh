@@ -12,10 +12,15 @@
 // values) in the workspace, and a second kernel joins them, in order. Which CTA has
 // which tiles follows from the lengths alone, so equal calls give equal bits.
 //
+// Few units of short sequences: a cluster of CTAs a unit instead, which join their parts through distributed
+// shared memory, so that one launch does it.
+//
 // Within a CTA a warp takes every fourth piece of a tile by itself: it copies the piece's keys
 // and values into a ring of its own in shared memory, several pieces ahead and across
 // units, so no barrier stands in the loop; the warps meet at a unit's end only.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "async_ring.cuh"
 #include "rowops_device.cuh"
@@ -159,7 +164,18 @@ __device__ __forceinline__ constexpr int paged_part_floats() {
     return (ROWS * (DT + 2) + 3) / 4 * 4;
 }
 
-template <class P>
+// What a head's row of sums becomes: the maximum m in the exponent of 2, the sum l.
+struct PagedRow {
+    float inv, lse;
+    __device__ __forceinline__ PagedRow(float m, float l, bool beyond) {
+        if (beyond) l = NAN;
+        inv = l == 0.f ? 0.f : 1.f / l;
+        lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+    }
+};
+
+// CLUSTERED: a cluster of CTAs a unit, its tiles shared out evenly; else equal stretches of the line.
+template <class P, bool CLUSTERED>
 __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
     paged_attention_kernel(const __grid_constant__ PagedArgs a, float* parts, int blocks, bool whole) {
     using T = typename P::T;
@@ -174,12 +190,30 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
     __shared__ int64_t found[kPagedBlock / 32 * 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units = int(a.kv_heads) * blocks;
     const int group = int(a.heads / a.kv_heads);
+    __shared__ float told_top[ROWS], told_sum[ROWS];  // CLUSTERED: read by the cluster's CTAs
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = CLUSTERED ? int(cluster.num_blocks()) : 1, rank = CLUSTERED ? int(cluster.block_rank()) : 0;
 
-    let_next_start();
-    int64_t total, begin, end, before;
+    P p(scratch);
+    int64_t begin, end, before = 0;
     int b;
-    paged_find<TILE>(a, units, found, &total, blockIdx.x, gridDim.x, &begin, &end, &b, &before);
-    if (begin >= end) return;
+    if constexpr (CLUSTERED) {
+        const int unit = int(blockIdx.x) / C, j = unit % units, head = j / blocks * group + j % blocks * ROWS;
+        uint32_t n, first, base;
+        b = unit / units;
+        // the queries first: they wait for nothing
+        p.begin(static_cast<const T*>(a.q) + b * a.ldq + int64_t(head) * a.D, min(ROWS, group - j % blocks * ROWS), int(a.D));
+        const int64_t tiles = paged_span<TILE>(a, b, &n, &first, &base);
+        begin = j * tiles + tiles * rank / C;
+        end = j * tiles + tiles * (rank + 1) / C;
+        if (threadIdx.x < ROWS) told_top[threadIdx.x] = -INFINITY, told_sum[threadIdx.x] = 0.f;
+    } else {
+        int64_t total;
+        let_next_start();
+        paged_find<TILE>(a, units, found, &total, blockIdx.x, gridDim.x, &begin, &end, &b, &before);
+        if (begin >= end) return;
+    }
 
     // columns past D stay zero: nothing is copied there
     if (a.D < DT)
@@ -267,9 +301,8 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
     look();
     for (int s = 0; s < S; ++s) ask(s);
 
-    P p(scratch);
     const float scale = a.scale * kLog2eF;
-    bool fresh = true, cut = at.tile != 0;  // a unit begins; it began in another CTA
+    bool fresh = !CLUSTERED, cut = at.tile != 0;  // a unit begins; it began in another CTA
     for (int slot = 0; at.left > 0; slot = slot + 1 == S ? 0 : slot + 1) {
         const int head = at.j / blocks * group + at.j % blocks * ROWS;  // the unit's first
         const int rows = min(ROWS, group - at.j % blocks * ROWS);
@@ -308,16 +341,16 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
                 for (int w = 1; w < kPagedWarps; ++w) m = fmaxf(m, tops[w][r]);
                 for (int w = 0; w < kPagedWarps; ++w)
                     l += m == -INFINITY ? sums[w][r] : sums[w][r] * ex2_approx(tops[w][r] - m);
-                if (part) {
+                if constexpr (CLUSTERED) {
+                    if (lane == 0) told_top[r] = m, told_sum[r] = l;
+                } else if (part) {
                     for (int d = lane; d < DT; d += 32) out[r * DT + d] = joined[r * P::kPitch + d];
                     if (lane == 0) out[ROWS * DT + 2 * r] = m, out[ROWS * DT + 2 * r + 1] = l;
                 } else {
-                    if (paged_beyond(a, at.b)) l = NAN;
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    const PagedRow row(m, l, paged_beyond(a, at.b));
                     T* o = static_cast<T*>(a.out) + at.b * a.ldo + int64_t(head + r) * a.D;
-                    for (int d = lane; d < a.D; d += 32) E::store(o + d, joined[r * P::kPitch + d] * inv);
-                    if (lane == 0 && a.lse)
-                        a.lse[at.b * a.heads + head + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+                    for (int d = lane; d < a.D; d += 32) E::store(o + d, joined[r * P::kPitch + d] * row.inv);
+                    if (lane == 0 && a.lse) a.lse[at.b * a.heads + head + r] = row.lse;
                 }
             }
             cut = false;
@@ -327,6 +360,37 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
         at.next();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (CLUSTERED) {
+        // every C-th row of the unit, joined from the CTAs' parts in order (one without a tile has a sum of 0)
+        const int j = int(blockIdx.x) / C % units, head = j / blocks * group + j % blocks * ROWS;
+        const int rows = min(ROWS, group - j % blocks * ROWS);
+        cluster.sync();
+        for (int r = rank; r < rows; r += C) {
+            const int of = lane & (C - 1);
+            const float pm = cluster.map_shared_rank(told_top, of)[r], pl = cluster.map_shared_rank(told_sum, of)[r];
+            float m = pm;
+#pragma unroll
+            for (int o = kPagedCluster / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float take = m == -INFINITY ? 0.f : ex2_approx(pm - m);
+            float l = 0.f;
+            for (int c = 0; c < C; ++c) l += __shfl_sync(0xffffffffu, m == -INFINITY ? pl : pl * take, c);
+            const PagedRow row(m, l, paged_beyond(a, b));
+            T* o = static_cast<T*>(a.out) + b * a.ldo + int64_t(head + r) * a.D;
+            for (int d0 = 0; d0 < a.D; d0 += kPagedBlock) {
+                const int d = d0 + threadIdx.x;
+                float x = 0.f;
+#pragma unroll
+                for (int c = 0; c < kPagedCluster; ++c)
+                    if (c < C) {
+                        const float w = __shfl_sync(0xffffffffu, take, c), s = __shfl_sync(0xffffffffu, pl, c);
+                        if (s != 0.f && d < a.D) x = fmaf(cluster.map_shared_rank(joined, c)[r * P::kPitch + d], w, x);
+                    }
+                if (d < a.D) E::store(o + d, x * row.inv);
+            }
+            if (threadIdx.x == 0 && a.lse) a.lse[b * a.heads + head + r] = row.lse;
+        }
+        cluster.sync();  // no CTA's shared memory goes while it is read
+    }
 }
 
 // The units that no CTA has written: those cut by a border, joined from their parts in
@@ -389,39 +453,53 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (beyond) l = NAN;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const PagedRow row(m, l, beyond);
             T* o = static_cast<T*>(a.out) + b * a.ldo + int64_t(head + r) * a.D;
 #pragma unroll
             for (int e = 0; e < EACH; ++e) {
                 const float v[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (4 * (lane + 32 * e) + i < a.D) E::store(o + 4 * (lane + 32 * e) + i, v[i] * inv);
+                    if (4 * (lane + 32 * e) + i < a.D) E::store(o + 4 * (lane + 32 * e) + i, v[i] * row.inv);
             }
-            if (lane == 0 && a.lse) a.lse[b * a.heads + head + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+            if (lane == 0 && a.lse) a.lse[b * a.heads + head + r] = row.lse;
         }
     }
 }
 
 template <class P>
 cudaError_t paged_launch(const PagedArgs& a, void* workspace, int blocks, const LaunchCfg& cfg) {
-    constexpr int TILE = P::kTokens * kPagedWarps;
     const int V = 16 / int(sizeof(typename P::T));
     auto even = [&](int64_t count, int64_t stride) { return count <= 1 || stride % V == 0; };
     const bool whole = a.D % V == 0 && even(a.pages, a.page_stride) && even(a.page, a.slot_stride) &&
                        even(a.kv_heads, a.head_stride) && reinterpret_cast<uintptr_t>(a.k) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.v) % 16 == 0;
-    const int64_t units = a.kv_heads * blocks, room = a.max_pages * a.page,
-                  most = a.window > 0 ? std::min(room, a.window + 15) : room;
-    const int64_t tiles = std::min<int64_t>((most + TILE - 1) / TILE * units, 1 << 20) * a.B;
+    const int64_t units = a.kv_heads * blocks;
     const size_t smem = P::Ring::kBytes + size_t(P::kRows) * P::kPitch * 4 + P::kScratch;
-    auto k = paged_attention_kernel<P>;
+    const PagedForm form = paged_form(a.B, a.heads, a.kv_heads, a.D, a.max_pages * a.page, a.window, int(sizeof(typename P::T)));
+    if (form.cluster) {
+        auto k = paged_attention_kernel<P, true>;
+        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, cfg);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3(unsigned(a.B * units * form.cluster));
+        lc.blockDim = dim3(kPagedBlock);
+        lc.dynamicSmemBytes = smem;
+        lc.stream = cfg.stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(form.cluster);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        return cudaLaunchKernelEx(&lc, k, a, static_cast<float*>(nullptr), blocks, whole);
+    }
+    auto k = paged_attention_kernel<P, false>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, cfg);
     if (e != cudaSuccess) return e;
     LaunchCfg one = cfg;
     one.ctas_per_sm = 0;
-    const int ctas = std::min(grid_for(reinterpret_cast<const void*>(k), kPagedBlock, smem, tiles, one), kPagedMaxCtas);
+    const int ctas = std::min(grid_for(reinterpret_cast<const void*>(k), kPagedBlock, smem, form.tiles, one), kPagedMaxCtas);
     k<<<ctas, kPagedBlock, smem, cfg.stream>>>(a, static_cast<float*>(workspace), blocks, whole);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t lc = {};

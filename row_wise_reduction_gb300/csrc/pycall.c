@@ -157,7 +157,7 @@ typedef int (*balance_bwd_fn)(const void*, const void*, const float*, const void
                               int64_t, int64_t, int, void*);
 typedef int (*quant_fn)(const void*, const void*, void*, float*, void*, const void*, float, int64_t, int64_t, int64_t,
                         int64_t, int64_t, int, void*);
-typedef size_t (*paged_bytes_fn)(int64_t, int64_t, int64_t, int64_t, int);
+typedef size_t (*paged_bytes_fn)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int);
 typedef int (*paged_fn)(const void*, const void*, const void*, const void*, const void*, void*, float*, float, int64_t,
                         int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
                         int64_t, int64_t, int64_t, int, void*, size_t, void*);
@@ -224,8 +224,8 @@ BYTES(router_balance_loss_workspace_bytes, 9, "iii",
 CALL(rmsnorm_quant, 10, "ppppppfiiiiiip",
      ((quant_fn)g_bound[10])(v.p[0], v.p[1], v.p[2], (float*)v.p[3], v.p[4], v.p[5], v.f[6], v.i[7], v.i[8], v.i[9],
                              v.i[10], v.i[11], (int)v.i[12], v.p[13]))
-BYTES(paged_attention_workspace_bytes, 11, "iiiii",
-      ((paged_bytes_fn)g_bound[11])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
+BYTES(paged_attention_workspace_bytes, 11, "iiiiiiii",
+      ((paged_bytes_fn)g_bound[11])(v.i[0], v.i[1], v.i[2], v.i[3], v.i[4], v.i[5], v.i[6], (int)v.i[7]))
 CALL(paged_attention, 12, "pppppppfiiiiiiiiiiiiiiipip",
      ((paged_fn)g_bound[12])(v.p[0], v.p[1], v.p[2], v.p[3], v.p[4], v.p[5], (float*)v.p[6], v.f[7], v.i[8], v.i[9],
                              v.i[10], v.i[11], v.i[12], v.i[13], v.i[14], v.i[15], v.i[16], v.i[17], v.i[18], v.i[19],

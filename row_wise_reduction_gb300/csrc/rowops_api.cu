@@ -1458,12 +1458,13 @@ bool spans(int64_t* total, std::initializer_list<std::pair<int64_t, int64_t>> co
 }
 }  // namespace
 
-size_t rowops_paged_attention_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D,
-                                              rowops_dtype_t dtype) {
+size_t rowops_paged_attention_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t page,
+                                              int64_t max_pages, int64_t window, rowops_dtype_t dtype) {
     if (!valid_dtype(dtype) || B < 1 || kv_heads < 1 || heads < 1 || heads % kv_heads != 0 || D < 1 ||
-        D > kPagedMaxD || B > INT32_MAX / heads)
+        D > kPagedMaxD || B > INT32_MAX / heads || page < 1 || max_pages < 0 || window < 0 ||
+        max_pages > (INT32_MAX - 255) / page)
         return 0;
-    return paged_bytes(heads / kv_heads, D, elem_bytes(dtype));
+    return paged_bytes(B, heads, kv_heads, D, page * max_pages, window, elem_bytes(dtype));
 }
 
 rowops_status_t rowops_paged_attention(const void* q, const void* k, const void* v, const int32_t* page_table,
@@ -1500,10 +1501,11 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
     for (const Range& r : in)
         if (!apart_from(r, {o, l})) return ROWOPS_ERR_INVALID_VALUE;
     if (!apart(o.p, o.n, l.p, l.n)) return ROWOPS_ERR_INVALID_VALUE;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < paged_bytes(heads / kv_heads, D, es))
-        return ROWOPS_ERR_WORKSPACE;
-    if (!apart_from({workspace, workspace_bytes}, {in[0], in[1], in[2], in[3], in[4], o, l}))
-        return ROWOPS_ERR_INVALID_VALUE;
+    if (const size_t need = paged_bytes(B, heads, kv_heads, D, page * max_pages, window, es)) {
+        if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return ROWOPS_ERR_WORKSPACE;
+        if (!apart_from({workspace, workspace_bytes}, {in[0], in[1], in[2], in[3], in[4], o, l}))
+            return ROWOPS_ERR_INVALID_VALUE;
+    }
     const Tuning tn = tuning();
     LaunchCfg cfg;
     rowops_status_t st = make_cfg(stream, tn, &cfg);

@@ -156,7 +156,7 @@ def library() -> ctypes.CDLL:
              [_vp, _vp, i32, _vp, f32, _vp, _vp] + [_i64] * 4 + [i32, _vp, size, _vp]),
             ("router_balance_loss_backward", i32, [_vp] * 4 + [f32, _vp] + [_i64] * 4 + [i32, _vp]),
             ("rmsnorm_quant", i32, [_vp] * 6 + [f32] + [_i64] * 5 + [i32, _vp]),
-            ("paged_attention_workspace_bytes", size, [_i64] * 4 + [i32]),
+            ("paged_attention_workspace_bytes", size, [_i64] * 7 + [i32]),
             ("paged_attention", i32, [_vp] * 7 + [f32] + [_i64] * 14 + [i32, _vp, size, _vp]),
             ("sample", i32, [_vp] * 3 + [f32, _vp, ctypes.c_int32, _vp, f32, _vp, f32] + [_vp] * 2 + [_i64] * 3
              + [i32, _vp]),
@@ -1042,8 +1042,10 @@ def _indices(t: torch.Tensor, dev: int, name: str) -> torch.Tensor:
     return t
 
 
-def rowops_paged_attention_workspace_bytes(B: int, heads: int, kv_heads: int, D: int, dtype: torch.dtype) -> int:
-    return int(library().rowops_paged_attention_workspace_bytes(B, heads, kv_heads, D, _DTYPE_CODES.get(dtype, -1)))
+def rowops_paged_attention_workspace_bytes(B: int, heads: int, kv_heads: int, D: int, page: int, max_pages: int,
+                                           window: int, dtype: torch.dtype) -> int:
+    return int(library().rowops_paged_attention_workspace_bytes(B, heads, kv_heads, D, page, max_pages, window,
+                                                                _DTYPE_CODES.get(dtype, -1)))
 
 
 def rowops_paged_attention(
@@ -1099,7 +1101,7 @@ def rowops_paged_attention(
             raise ValueError("out must match q in shape, dtype and device")
         ldo = _heads(out, "out")[3]
     L = _calls or _hot_calls()
-    ws, wp, wn = _scratch(workspace, L.paged_attention_workspace_bytes(B, H, ks[2], D, code), dev)
+    ws, wp, wn = _scratch(workspace, L.paged_attention_workspace_bytes(B, H, ks[2], D, ks[1], width, window, code), dev)
     st = L.paged_attention(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _indices(page_table, dev, "page_table").data_ptr(),
         _indices(lengths, dev, "lengths").data_ptr(), out.data_ptr(),

@@ -38,20 +38,24 @@ def test_rmsnorm_quant_refusals(lib):
 
 def test_paged_attention_refusals(lib):
     f, g = lib.rowops_paged_attention, lib.rowops_paged_attention_workspace_bytes
-    need = g(3, 8, 2, 64, BF16)
-    for bad in ((0, 8, 2, 64, BF16), (3, 7, 2, 64, BF16), (3, 8, 0, 64, BF16), (3, 8, 2, 257, BF16), (3, 8, 2, 0, BF16),
-                (3, 8, 2, 64, 7), (1 << 31, 8, 2, 64, BF16)):
+    assert g(1, 8, 2, 64, 16, 5, 0, BF16) == 0  # one kernel
+    need = g(300, 8, 2, 64, 16, 500, 0, BF16)
+    assert need > 0 and g(300, 8, 2, 64, 16, 500, 10**9, BF16) == need
+    for bad in ((0, 8, 2, 64, 16, 500, 0, BF16), (300, 7, 2, 64, 16, 500, 0, BF16), (300, 8, 0, 64, 16, 500, 0, BF16),
+                (300, 8, 2, 257, 16, 500, 0, BF16), (300, 8, 2, 0, 16, 500, 0, BF16), (300, 8, 2, 64, 16, 500, 0, 7),
+                (1 << 31, 8, 2, 64, 16, 500, 0, BF16), (300, 8, 2, 64, 0, 500, 0, BF16), (300, 8, 2, 64, 16, -1, 0, BF16),
+                (300, 8, 2, 64, 16, 500, -1, BF16), (300, 8, 2, 64, 16, 1 << 30, 0, BF16)):
         assert g(*bad) == 0, bad
 
-    def args(q=X, k=K, v=V, table=TABLE, lengths=LENGTHS, out=OUT, lse=LSE, scale=0.125, window=0, B=3, H=8, KV=2, D=64,
-             ldq=512, ldo=512, pages=10, page=16, ps=2048, ss=128, hs=64, width=5, ldt=5, dt=BF16, ws=WS, nb=None):
+    def args(q=X, k=K, v=V, table=TABLE, lengths=LENGTHS, out=OUT, lse=LSE, scale=0.125, window=0, B=300, H=8, KV=2, D=64,
+             ldq=512, ldo=512, pages=10, page=16, ps=2048, ss=128, hs=64, width=500, ldt=500, dt=BF16, ws=WS, nb=None):
         return (q, k, v, table, lengths, out, lse, scale, window, B, H, KV, D, ldq, ldo, pages, page, ps, ss, hs, width,
-                ldt, dt, ws, max(need, 256) if nb is None else nb, None)
+                ldt, dt, ws, need if nb is None else nb, None)
 
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(table=None), dict(lengths=None), dict(out=None),
                 dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1), dict(B=-1), dict(H=0), dict(KV=0),
                 dict(KV=3), dict(D=0), dict(ldq=511), dict(ldo=511), dict(pages=-1), dict(page=0), dict(ps=-1),
-                dict(ss=-1), dict(hs=-1), dict(width=-1), dict(ldt=4), dict(dt=2), dict(q=X + 1), dict(k=K + 1),
+                dict(ss=-1), dict(hs=-1), dict(width=-1), dict(ldt=499), dict(dt=2), dict(q=X + 1), dict(k=K + 1),
                 dict(v=V + 1), dict(out=OUT + 1), dict(table=TABLE + 2), dict(lengths=LENGTHS + 2), dict(lse=LSE + 2),
                 dict(out=X), dict(out=X + 64), dict(out=K + 64), dict(out=V), dict(out=TABLE), dict(out=LENGTHS),
                 dict(lse=X), dict(lse=K), dict(lse=V + 4), dict(lse=TABLE), dict(lse=LENGTHS), dict(lse=OUT)):
@@ -61,11 +65,10 @@ def test_paged_attention_refusals(lib):
                 dict(ldq=1 << 62), dict(ldt=1 << 62)):
         assert f(*args(**bad)) == UNSUPPORTED, bad
     assert f(*args(B=0, q=None, k=None, v=None, table=None, lengths=None, out=None, ws=None)) == OK
-    if need:
-        for bad in (dict(ws=None), dict(ws=WS + 128), dict(nb=need - 1)):
-            assert f(*args(**bad)) == WORKSPACE, bad
-        for bad in (dict(ws=X), dict(ws=K), dict(ws=V), dict(ws=TABLE), dict(ws=LENGTHS), dict(ws=OUT), dict(ws=LSE)):
-            assert f(*args(**bad)) == INVALID, bad
+    for bad in (dict(ws=None), dict(ws=WS + 128), dict(nb=need - 1)):
+        assert f(*args(**bad)) == WORKSPACE, bad
+    for bad in (dict(ws=X), dict(ws=K), dict(ws=V), dict(ws=TABLE), dict(ws=LENGTHS), dict(ws=OUT), dict(ws=LSE)):
+        assert f(*args(**bad)) == INVALID, bad
 
 
 def test_sample_refusals(lib):

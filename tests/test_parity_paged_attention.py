@@ -83,16 +83,21 @@ def judge(got, lse, q, k, v, table, n, scale=None, window=0):
     assert np.all(np.abs(gl[fine] - rlse[fine]) <= rel[fine] + 2.0**-22 * np.abs(rlse[fine]))
 
 
+LINE = 100000  # a table this wide (most of it unused) makes it equal stretches of tiles, and parts
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 500, 1000, 4097])
 def test_lengths(dtype, n):
     check([n], 8, 2, 64, 16, dtype)
+    check([n], 8, 2, 64, 16, dtype, width=LINE)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("D", [1, 3, 8, 17, 32, 40, 63, 64, 72, 80, 96, 100, 112, 128, 160, 192, 200, 255, 256])
 def test_head_dimensions(dtype, D):
     check([130, 1, 77], 6, 2, D, 16, dtype)
+    check([130, 1, 77], 6, 2, D, 16, dtype, width=LINE)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -100,6 +105,7 @@ def test_head_dimensions(dtype, D):
                                  (71, 1), (128, 8)])
 def test_heads(dtype, H, K):
     check([200, 31], H, K, 64, 16, dtype)
+    check([200, 31], H, K, 64, 16, dtype, width=LINE)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -107,13 +113,15 @@ def test_heads(dtype, H, K):
 @pytest.mark.parametrize("layout", ["slots", "heads"])
 def test_pages_and_layouts(dtype, page, layout):
     check([333, 5, 100], 8, 2, 64, page, dtype, layout=layout)
+    check([333, 5, 100], 8, 2, 64, page, dtype, layout=layout, width=LINE)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
 def test_empty_sequences_and_ragged_batches(dtype):
-    check([0, 700, 0, 1, 64, 0], 8, 4, 64, 16, dtype)
-    check([0, 0], 4, 4, 32, 8, dtype)
-    check([-5, 20], 4, 4, 32, 8, dtype)
+    for width in (50, LINE):
+        check([0, 700, 0, 1, 64, 0], 8, 4, 64, 16, dtype, width=width)
+        check([0, 0], 4, 4, 32, 8, dtype, width=width)
+        check([-5, 20], 4, 4, 32, 8, dtype, width=width)
     check([(i * 37) % 301 for i in range(67)], 4, 2, 64, 16, dtype)
 
 
@@ -121,6 +129,7 @@ def test_empty_sequences_and_ragged_batches(dtype):
 @pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 100, 299, 300, 10**9])
 def test_windows(dtype, window):
     check([300, 64, 1, 0, 150], 8, 2, 64, 16, dtype, window=window)
+    check([300, 64, 1, 0, 150] + [20] * 200, 8, 2, 64, 16, dtype, window=window, width=LINE)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -128,6 +137,7 @@ def test_windows(dtype, window):
 def test_strides_and_alignment(dtype, D, wide, qpad):
     check([90, 200], 4, 2, D, 16, dtype, wide=wide, qpad=qpad)
     check([90, 200], 4, 2, D, 16, dtype, wide=wide, qpad=qpad, layout="heads")
+    check([90, 200], 4, 2, D, 16, dtype, wide=wide, qpad=qpad, width=LINE)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -143,13 +153,16 @@ def test_one_long_sequence_and_many(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_pages_outside_the_pool_and_lengths_beyond_the_table(dtype):
-    q, k, v, table, n = problem([100, 100, 100, 20, 100], 8, 2, 64, 16, dtype)
-    lse = torch.empty(5, 8, device="cuda")
+@pytest.mark.parametrize("page", [16, 12])  # whole pieces of a page, and not
+@pytest.mark.parametrize("more", [0, 200])  # few sequences, and enough for equal stretches
+def test_pages_outside_the_pool_and_lengths_beyond_the_table(dtype, page, more):
+    q, k, v, table, n = problem([100, 100, 100, 20, 100] + [10] * more, 8, 2, 64, page, dtype)
+    lse = torch.empty(5 + more, 8, device="cuda")
+    last = 99 // page
     table[1, 2] = -1
-    table[2, 6] = k.shape[0]
+    table[2, last] = k.shape[0]
     table[3, 2] = 1 << 30  # not reached
-    n[4] = table.shape[1] * 16 + 1
+    n[4] = table.shape[1] * page + 1
     out = ro.rowops_paged_attention(q, k, v, table, n, lse=lse)
     judge(out, lse, q, k, v, table, n)
     n[4] = 2**31 - 1
@@ -158,7 +171,7 @@ def test_pages_outside_the_pool_and_lengths_beyond_the_table(dtype):
     table[1, 2] = table[0, 0]
     n[1] = 40  # the bad page within a window's reach or not
     table[2, 0] = -9
-    table[2, 6] = table[0, 1]
+    table[2, last] = table[0, 1]
     out = ro.rowops_paged_attention(q, k, v, table, n, None, 50, lse=lse)
     judge(out, lse, q, k, v, table, n, None, 50)
 
@@ -185,15 +198,17 @@ def test_scores_far_apart(dtype):
         judge(ro.rowops_paged_attention(q, k, v, table, n, lse=lse), lse, q, k, v, table, n)
 
 
-def test_repeatable_on_a_stream_and_in_a_replayed_graph():
-    q, k, v, table, n = problem([500, 33, 900, 0], 8, 2, 128, 16, "bf16")
+@pytest.mark.parametrize("width", [57, 4000])  # one kernel; two, with a workspace
+def test_repeatable_on_a_stream_and_in_a_replayed_graph(width):
+    q, k, v, table, n = problem([500, 33, 900, 0], 8, 2, 128, 16, "bf16", width=width)
     out = ro.rowops_paged_attention(q, k, v, table, n)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     again = ro.rowops_paged_attention(q, k, v, table, n, stream=s)
     s.synchronize()
     assert torch.equal(out, again)
-    need = ro.rowops_paged_attention_workspace_bytes(4, 8, 2, 128, q.dtype)
+    need = ro.rowops_paged_attention_workspace_bytes(4, 8, 2, 128, 16, width, 0, q.dtype)
+    assert (need > 0) == (width == 4000)
     ws = torch.full((max(need, 256),), 0xff, dtype=torch.uint8, device="cuda")  # its contents do not matter
     y, lse = torch.empty_like(out), torch.empty(4, 8, device="cuda")
     ro.rowops_paged_attention(q, k, v, table, n, out=y, lse=lse, workspace=ws)
