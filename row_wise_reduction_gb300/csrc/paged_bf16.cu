@@ -47,7 +47,7 @@ struct PagedBf16 {
     // Long heads' queries stay in shared memory
     static constexpr bool kKept = DT * H < 320;
     static constexpr size_t kScratch = kKept ? 0 : size_t(DT / 16) * H * 32 * 8;
-    using Ring = PagedRing<T, DT, kTokens>;
+    using Ring = PagedRing<T, DT, kTokens, kRows>;
     uint2 q[kKept ? DT / 16 : 1][H];
     uint2* far;  // [DT / 16][H][32], every warp writes the same
     float o[DT / 16][H][4], m[H][2], l[H][2];

@@ -32,14 +32,17 @@ constexpr int kPagedWarps = 4, kPagedBlock = 32 * kPagedWarps;
 
 // A warp's ring: pieces of TOKENS positions, their keys, then their values. Rows lie an odd number
 // of 16-byte vectors apart, so eight rows' vectors lie in different banks.
-template <typename T, int DT, int TOKENS>
+// As many steps (6 at most) as let three CTAs share an SM, if those are two and the registers allow it (ROWS at most 8),
+// else two CTAs, else three steps in one. Three for two: D 64, heads before slots, 64 sequences of up to 8192, bf16 131 to 110 us,
+// fp32 268 to 213; D 128 186 to 182.
+template <typename T, int DT, int TOKENS, int ROWS>
 struct PagedRing {
     static constexpr int kPitch = (DT * int(sizeof(T)) / 16 | 1) * 16;
-    static constexpr int kPart = TOKENS * kPitch;                 // keys, or values
-    static constexpr int kStep = 2 * kPart * kPagedWarps;         // of the CTA
-    static constexpr int kHalf = 104448;                          // what lets two CTAs share an SM
-    static constexpr bool kTwo = kHalf / kStep >= 2;
-    static constexpr int kStages = !kTwo ? 3 : kHalf / kStep > 6 ? 6 : kHalf / kStep;
+    static constexpr int kPart = TOKENS * kPitch;          // keys, or values
+    static constexpr int kStep = 2 * kPart * kPagedWarps;  // of the CTA
+    static constexpr int kCtas = ROWS <= 8 && 72000 / kStep >= 2 ? 3 : 104448 / kStep >= 2 ? 2 : 1;
+    static constexpr int kFit = (kCtas == 3 ? 72000 : 104448) / kStep;
+    static constexpr int kStages = kCtas == 1 ? 3 : kFit > 6 ? 6 : kFit;
     static constexpr int kBytes = kStep * kStages;
 };
 
@@ -176,7 +179,7 @@ struct PagedRow {
 
 // CLUSTERED: a cluster of CTAs a unit, its tiles shared out evenly; else equal stretches of the line.
 template <class P, bool CLUSTERED>
-__global__ void __launch_bounds__(kPagedBlock, P::Ring::kTwo ? 2 : 1)
+__global__ void __launch_bounds__(kPagedBlock, P::Ring::kCtas)
     paged_attention_kernel(const __grid_constant__ PagedArgs a, float* parts, int blocks, bool whole) {
     using T = typename P::T;
     using E = Elem<T>;

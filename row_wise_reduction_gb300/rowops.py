@@ -996,30 +996,44 @@ def rowops_rmsnorm_quant(
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_rmsnorm_quant, stream, dev, x, residual, w, eps, group, q, scales, residual_out)
-    M, N, ld = _rows(x, "x")
-    code = _dtype_code(x)
+    sh, xs, dt = x.shape, x.stride(), x.dtype
+    if len(sh) != 2:
+        raise ValueError("x must be 2-D (M, N)")
+    M, N = sh
+    if N > 0 and xs[1] != 1:
+        raise ValueError("x must have unit column stride")
+    code = _DTYPE_CODES.get(dt)
+    if code is None:
+        raise TypeError(f"rowops supports float32 and bfloat16, not {dt}")
+    whole = x.is_contiguous()
     pr = po = None
     if residual is not None:
-        _out_like(x, residual)  # same shape, dtype, device and row stride
-        residual_out = _out_like(x, residual_out)
+        if residual.dtype is not dt or residual.get_device() != dev or residual.shape != sh:
+            raise ValueError("residual must match x in shape, dtype and device")
+        if residual.stride() != xs and (M > 1 or (M == 1 and N > 1 and residual.stride(1) != 1)):
+            raise ValueError("x and residual must share the row stride")
+        if residual_out is None and whole:
+            residual_out = torch.empty_like(x)
+        else:
+            residual_out = _out_like(x, residual_out)
         pr, po = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out is given but residual is not")
     groups = 1 if group <= 0 else -(-N // group)
     if q is None:
-        q = torch.empty(M, N, dtype=_E4M3, device=x.device)
+        q = torch.empty_like(x, dtype=_E4M3) if whole else torch.empty(M, N, dtype=_E4M3, device=x.device)
         ldq = N
     else:
-        if q.dtype is not _E4M3 or q.shape != x.shape or q.get_device() != dev or (N > 1 and q.stride(1) != 1):
+        if q.dtype is not _E4M3 or q.shape != sh or q.get_device() != dev or (N > 1 and q.stride(1) != 1):
             raise ValueError("q must be a float8_e4m3fn CUDA tensor of x's shape with unit column stride")
         ldq = q.stride(0) if M > 1 else max(N, q.stride(0))
     if scales is None:
-        scales = torch.empty(M, groups, dtype=torch.float32, device=x.device)
-    elif scales.numel() != M * groups:
-        raise ValueError("scales must have M * ceil(N / group) entries")
+        scales = torch.empty((M, groups), dtype=torch.float32, device=x.device)
+    else:
+        _floats(scales, M * groups, dev, "scales")
     st = (_calls or _hot_calls()).rmsnorm_quant(
-        x.data_ptr(), pr, q.data_ptr(), _floats(scales, M * groups, dev, "scales").data_ptr(), po,
-        _affine(w, x, N, dev, "w"), eps, M, N, ld, ldq, group, code, _current_raw_stream(dev))
+        x.data_ptr(), pr, q.data_ptr(), scales.data_ptr(), po, _affine(w, x, N, dev, "w"), eps, M, N,
+        xs[0] if M > 1 else max(N, xs[0]), ldq, group, code, _current_raw_stream(dev))
     if st:
         raise RowopsError("rowops_rmsnorm_quant", st)
     return q, scales, residual_out
@@ -1034,12 +1048,6 @@ def _heads(t: torch.Tensor, name: str):
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"{name}'s heads must follow one another")
     return B, H, D, (sb if B > 1 else max(H * D, sb))
-
-
-def _indices(t: torch.Tensor, dev: int, name: str) -> torch.Tensor:
-    if t.dtype is not torch.int32 or t.get_device() != dev:
-        raise ValueError(f"{name} must be an int32 CUDA tensor on the device of the call's tensors")
-    return t
 
 
 def rowops_paged_attention_workspace_bytes(B: int, heads: int, kv_heads: int, D: int, page: int, max_pages: int,
@@ -1077,10 +1085,10 @@ def rowops_paged_attention(
                           out, lse, workspace=workspace)
     B, H, D, ldq = _heads(q, "q")
     code = _dtype_code(q)
-    ks = k_cache.shape
+    ks, dt = k_cache.shape, q.dtype
     if len(ks) != 4 or ks != v_cache.shape or ks[3] != D:
         raise ValueError("k_cache and v_cache must both be (pages, slots, kv_heads, D)")
-    if (k_cache.dtype is not q.dtype or v_cache.dtype is not q.dtype or k_cache.get_device() != dev
+    if (k_cache.dtype is not dt or v_cache.dtype is not dt or k_cache.get_device() != dev
             or v_cache.get_device() != dev):
         raise ValueError("k_cache and v_cache must match q in dtype and device")
     kt, vt = k_cache.stride(), v_cache.stride()
@@ -1088,23 +1096,26 @@ def rowops_paged_attention(
         raise ValueError("k_cache and v_cache must share their strides")
     if D > 1 and kt[3] != 1:
         raise ValueError("k_cache and v_cache must have unit stride in D")
-    if page_table.dim() != 2 or page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    ts = page_table.shape
+    if len(ts) != 2 or ts[0] != B or (ts[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("page_table must be (B, max_pages) with unit column stride")
     if lengths.shape != (B,) or not lengths.is_contiguous():
         raise ValueError("lengths must be a contiguous (B,) tensor")
-    width = page_table.shape[1]
+    if (page_table.dtype is not torch.int32 or lengths.dtype is not torch.int32 or page_table.get_device() != dev
+            or lengths.get_device() != dev):
+        raise ValueError("page_table and lengths must be int32 CUDA tensors on the device of the call's tensors")
+    width = ts[1]
     if out is None:
-        out = torch.empty(B, H, D, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q) if ldq == H * D and q.is_contiguous() else torch.empty(B, H, D, dtype=dt, device=q.device)
         ldo = H * D
     else:
-        if out.dtype is not q.dtype or out.shape != q.shape or out.get_device() != dev:
+        if out.dtype is not dt or out.shape != q.shape or out.get_device() != dev:
             raise ValueError("out must match q in shape, dtype and device")
         ldo = _heads(out, "out")[3]
     L = _calls or _hot_calls()
     ws, wp, wn = _scratch(workspace, L.paged_attention_workspace_bytes(B, H, ks[2], D, ks[1], width, window, code), dev)
     st = L.paged_attention(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _indices(page_table, dev, "page_table").data_ptr(),
-        _indices(lengths, dev, "lengths").data_ptr(), out.data_ptr(),
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
         None if lse is None else _floats(lse, B * H, dev, "lse").data_ptr(), D ** -0.5 if scale is None else scale,
         window, B, H, ks[2], D, ldq, ldo, ks[0], ks[1], kt[0], kt[1], kt[2], width,
         page_table.stride(0) if B > 1 else max(width, page_table.stride(0)), code, wp, wn, _current_raw_stream(dev))
