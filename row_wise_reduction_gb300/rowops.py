@@ -1162,6 +1162,8 @@ def rowops_sample(
         token = torch.empty(M, dtype=torch.int64, device=logits.device)
     elif token.dtype is not torch.int64 or token.shape != (M,) or not token.is_contiguous() or token.get_device() != dev:
         raise ValueError("token must be a contiguous int64 CUDA tensor of one entry a row")
+    if not isinstance(top_k, torch.Tensor):
+        top_k = min(max(top_k, -1), N)  # (32 bits in the call)
     st = (_calls or _hot_calls()).sample(
         logits.data_ptr(), u.data_ptr(), *_knob(temperature, M, f32, dev, "temperature"),
         *_knob(top_k, M, torch.int32, dev, "top_k"), *_knob(top_p, M, f32, dev, "top_p"),

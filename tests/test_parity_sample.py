@@ -268,3 +268,14 @@ def test_refusals():
     with pytest.raises(TypeError):
         S(x.half(), u)
     assert S(x[:0], u[:0]).shape == (0,)
+
+
+def test_top_k_of_more_than_32_bits():
+    x, u = place(rows(4, 300, 31), "f32"), uniform(4, 32)
+    for k in (300, 2**31, 2**32 + 1, 2**63 - 1, 2**64 + 1):
+        assert torch.equal(ro.rowops_sample(x, u, top_k=k), ro.rowops_sample(x, u))
+    for k in (-1, -(2**32), -(2**64)):
+        with pytest.raises(ro.RowopsError):
+            ro.rowops_sample(x, u, top_k=k)
+    with pytest.raises(TypeError):
+        ro.rowops_sample(x, u, top_k=50.5)
