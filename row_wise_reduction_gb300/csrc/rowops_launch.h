@@ -477,7 +477,7 @@ struct PagedForm {
 // sequence, clusters and line: room for 512 8.1 and 9.5 us, 4096 16.1 and 18.8, 8192 26.6 and 22.0.
 inline PagedForm paged_form(int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t room, int64_t window, int es) {
     const int64_t rows = paged_rows(heads / kv_heads, es), units = B * kv_heads * ((heads / kv_heads + rows - 1) / rows);
-    const int64_t tile = es == 2 ? 64 : 32, most = window > 0 ? std::min(room, window + 15) : room;
+    const int64_t tile = es == 2 ? 64 : 32, most = window > 0 && window < room ? std::min(room, window + 15) : room;
     const int64_t each = (most + tile - 1) / tile, slots = 152 * (D > 192 ? 1 : 2);
     PagedForm f = {0, std::min<int64_t>(each, 1 << 20) * units};
     int C = kPagedCluster;

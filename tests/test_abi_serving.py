@@ -41,6 +41,8 @@ def test_paged_attention_refusals(lib):
     assert g(1, 8, 2, 64, 16, 5, 0, BF16) == 0  # one kernel
     need = g(300, 8, 2, 64, 16, 500, 0, BF16)
     assert need > 0 and g(300, 8, 2, 64, 16, 500, 10**9, BF16) == need
+    for window in (8000, 2**63 - 15, 2**63 - 1):  # as none
+        assert g(4, 8, 2, 64, 16, 500, window, BF16) == g(4, 8, 2, 64, 16, 500, 0, BF16) > 0, window
     for bad in ((0, 8, 2, 64, 16, 500, 0, BF16), (300, 7, 2, 64, 16, 500, 0, BF16), (300, 8, 0, 64, 16, 500, 0, BF16),
                 (300, 8, 2, 257, 16, 500, 0, BF16), (300, 8, 2, 0, 16, 500, 0, BF16), (300, 8, 2, 64, 16, 500, 0, 7),
                 (1 << 31, 8, 2, 64, 16, 500, 0, BF16), (300, 8, 2, 64, 0, 500, 0, BF16), (300, 8, 2, 64, 16, -1, 0, BF16),
