@@ -1116,7 +1116,7 @@ def rowops_paged_attention(
     ws, wp, wn = _scratch(workspace, L.paged_attention_workspace_bytes(B, H, ks[2], D, ks[1], width, window, code), dev)
     st = L.paged_attention(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
-        None if lse is None else _floats(lse, B * H, dev, "lse").data_ptr(), D ** -0.5 if scale is None else scale,
+        None if lse is None else _floats(lse, B * H, dev, "lse").data_ptr(), max(D, 1) ** -0.5 if scale is None else scale,
         window, B, H, ks[2], D, ldq, ldo, ks[0], ks[1], kt[0], kt[1], kt[2], width,
         page_table.stride(0) if B > 1 else max(width, page_table.stride(0)), code, wp, wn, _current_raw_stream(dev))
     if st:

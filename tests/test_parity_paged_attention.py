@@ -246,3 +246,9 @@ def test_refusals():
     with pytest.raises(ro.RowopsError):
         P(q, k, v, table, n, scale=float("nan"))
     assert P(q[:0], k, v, table[:0], n[:0]).shape == (0, 4, 32)
+
+
+def test_no_columns_are_refused():
+    q, k, v, table, n = problem([20, 9], 4, 2, 32, 8, "f32")
+    with pytest.raises(ro.RowopsError):
+        ro.rowops_paged_attention(q[..., :0].contiguous(), k[..., :0], v[..., :0], table, n)
