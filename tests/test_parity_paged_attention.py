@@ -250,5 +250,6 @@ def test_refusals():
 
 def test_no_columns_are_refused():
     q, k, v, table, n = problem([20, 9], 4, 2, 32, 8, "f32")
-    with pytest.raises(ro.RowopsError):
-        ro.rowops_paged_attention(q[..., :0].contiguous(), k[..., :0], v[..., :0], table, n)
+    for heads in (1, 4):
+        with pytest.raises((ro.RowopsError, ValueError)):
+            ro.rowops_paged_attention(q[:, :heads, :0].contiguous(), k[:, :, :1, :0], v[:, :, :1, :0], table, n)
