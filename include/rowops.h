@@ -631,7 +631,9 @@ rowops_status_t rowops_rmsnorm_quant(const void* x, const void* residual, void* 
  *            rowops_paged_attention_workspace_bytes(...) bytes (overwritten; 0: NULL
  *            will do), apart from the other tensors; calls sharing it must be ordered
  *            on one stream.
- * D is at most 256 (ROWOPS_ERR_UNSUPPORTED beyond). Statistics and sums in fp32, added
+ * D is at most 256, B at most 2^24, B * heads, pages and max_pages * page below 2^31 (the
+ * last by 256; ROWOPS_ERR_UNSUPPORTED beyond). An infinite value makes its column of out
+ * infinite or NaN. Statistics and sums in fp32, added
  * up in an order that the lengths of all the call's sequences decide: equal calls give
  * equal bits, other company may change a sequence's last bits. The lengths are read
  * on the device, so a captured graph replays with those of the day. k and v at 16-byte

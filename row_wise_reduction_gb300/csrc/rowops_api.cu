@@ -1461,7 +1461,7 @@ bool spans(int64_t* total, std::initializer_list<std::pair<int64_t, int64_t>> co
 size_t rowops_paged_attention_workspace_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t page,
                                               int64_t max_pages, int64_t window, rowops_dtype_t dtype) {
     if (!valid_dtype(dtype) || B < 1 || kv_heads < 1 || heads < 1 || heads % kv_heads != 0 || D < 1 ||
-        D > kPagedMaxD || B > INT32_MAX / heads || page < 1 || max_pages < 0 || window < 0 ||
+        D > kPagedMaxD || B > kPagedMaxB || B > INT32_MAX / heads || page < 1 || max_pages < 0 || window < 0 ||
         max_pages > (INT32_MAX - 255) / page)
         return 0;
     return paged_bytes(B, heads, kv_heads, D, page * max_pages, window, elem_bytes(dtype));
@@ -1477,8 +1477,8 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
         page < 1 || max_pages < 0 || ldt < max_pages || window < 0 || !std::isfinite(scale) || page_stride < 0 ||
         slot_stride < 0 || head_stride < 0)
         return ROWOPS_ERR_INVALID_VALUE;
-    if (D > kPagedMaxD || heads > INT32_MAX / D || B > INT32_MAX / heads || page > INT32_MAX || pages > INT32_MAX ||
-        max_pages > (INT32_MAX - 255) / page)
+    if (D > kPagedMaxD || heads > INT32_MAX / D || B > kPagedMaxB || B > INT32_MAX / heads || page > INT32_MAX ||
+        pages > INT32_MAX || max_pages > (INT32_MAX - 255) / page)
         return ROWOPS_ERR_UNSUPPORTED;
     if (ldq < heads * D || ldo < heads * D) return ROWOPS_ERR_INVALID_VALUE;
     if (B == 0) return ROWOPS_OK;

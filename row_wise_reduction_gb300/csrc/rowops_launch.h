@@ -445,6 +445,7 @@ cudaError_t rms_quant_bf16(const QuantArgs& a, int piece, const LaunchCfg& cfg);
 
 // Attention over a paged cache. Strides in elements.
 constexpr int kPagedMaxD = 256;
+constexpr int64_t kPagedMaxB = int64_t(1) << 24;  // every CTA counts the sequences' tiles, in 32 bits of sequences
 struct PagedArgs {
     const void *q, *k, *v;
     const int32_t *table, *lengths;

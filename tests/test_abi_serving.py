@@ -45,7 +45,7 @@ def test_paged_attention_refusals(lib):
         assert g(4, 8, 2, 64, 16, 500, window, BF16) == g(4, 8, 2, 64, 16, 500, 0, BF16) > 0, window
     for bad in ((0, 8, 2, 64, 16, 500, 0, BF16), (300, 7, 2, 64, 16, 500, 0, BF16), (300, 8, 0, 64, 16, 500, 0, BF16),
                 (300, 8, 2, 257, 16, 500, 0, BF16), (300, 8, 2, 0, 16, 500, 0, BF16), (300, 8, 2, 64, 16, 500, 0, 7),
-                (1 << 31, 8, 2, 64, 16, 500, 0, BF16), (300, 8, 2, 64, 0, 500, 0, BF16), (300, 8, 2, 64, 16, -1, 0, BF16),
+                (1 << 31, 8, 2, 64, 16, 500, 0, BF16), ((1 << 24) + 1, 2, 2, 64, 16, 500, 0, BF16), (300, 8, 2, 64, 0, 500, 0, BF16), (300, 8, 2, 64, 16, -1, 0, BF16),
                 (300, 8, 2, 64, 16, 500, -1, BF16), (300, 8, 2, 64, 16, 1 << 30, 0, BF16)):
         assert g(*bad) == 0, bad
 
@@ -62,7 +62,7 @@ def test_paged_attention_refusals(lib):
                 dict(out=X), dict(out=X + 64), dict(out=K + 64), dict(out=V), dict(out=TABLE), dict(out=LENGTHS),
                 dict(lse=X), dict(lse=K), dict(lse=V + 4), dict(lse=TABLE), dict(lse=LENGTHS), dict(lse=OUT)):
         assert f(*args(**bad)) == INVALID, bad
-    for bad in (dict(D=257, ldq=4096, ldo=4096), dict(B=1 << 31), dict(page=1 << 31), dict(pages=1 << 32),
+    for bad in (dict(D=257, ldq=4096, ldo=4096), dict(B=1 << 31), dict(B=(1 << 24) + 1, H=2), dict(page=1 << 31), dict(pages=1 << 32),
                 dict(width=1 << 31, ldt=1 << 31), dict(ps=1 << 62), dict(ss=1 << 62), dict(hs=1 << 62),
                 dict(ldq=1 << 62), dict(ldt=1 << 62)):
         assert f(*args(**bad)) == UNSUPPORTED, bad
