@@ -1487,7 +1487,10 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
     if (!spans(&qn, {{B, ldq}}, heads * D) || !spans(&on, {{B, ldo}}, heads * D) || !spans(&tn_, {{B, ldt}}, max_pages) ||
         !spans(&cn, {{pages, page_stride}, {page, slot_stride}, {kv_heads, head_stride}}, D))
         return ROWOPS_ERR_UNSUPPORTED;
-    if (pages == 0) cn = 0;
+    if (pages == 0) {  // copies of no bytes still name an address
+        cn = 0;
+        k = v = q;
+    }
     if (!q || !out || !lengths || (max_pages > 0 && !page_table) || (cn > 0 && (!k || !v)))
         return ROWOPS_ERR_INVALID_VALUE;
     for (const void* p : {q, k, v, static_cast<const void*>(out)})

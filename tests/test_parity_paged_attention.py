@@ -253,3 +253,15 @@ def test_no_columns_are_refused():
     for heads in (1, 4):
         with pytest.raises((ro.RowopsError, ValueError)):
             ro.rowops_paged_attention(q[:, :heads, :0].contiguous(), k[:, :, :1, :0], v[:, :, :1, :0], table, n)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [2, LINE])
+def test_a_cache_without_pages(dtype, width):
+    q, k, v, table, n = problem([20, 0], 4, 2, 32, 16, dtype, width=width)
+    lse = torch.empty(2, 4, device="cuda")
+    out = ro.rowops_paged_attention(q, k[:0], v[:0], table, n, lse=lse)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.all(out[1] == 0) and torch.all(lse[1] == -float("inf"))
+    none = ro.rowops_paged_attention(q, k, v, table[:, :0], n, lse=lse)  # and a table without columns
+    assert torch.isnan(none[0]).all() and torch.all(none[1] == 0) and torch.all(lse[1] == -float("inf"))
