@@ -157,8 +157,15 @@ __global__ void __launch_bounds__(quant_threads(PIECE, VPT), quant_threads(PIECE
         if constexpr (kRing) return ring[place * blockDim.x];
         else return load_vector<PIECE>(static_cast<const T*>(tensor) + at, bytes(k));
     };
-    if constexpr (PIECE == 4)  // what lies behind a row's end counts as 0
-        for (int i = 0; i < D * VPT * S; ++i) ring[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+    // What lies behind a row's end, which no copy reaches, counts as 0. (The braces matter: without them nvcc 13.0 drops
+    // the loop behind the pragma together with this statement, where that is not instantiated.)
+    if constexpr (PIECE == 4) {
+        for (int i = 0; i < D * VPT * S; ++i) {
+            const int k = t + i % VPT * tpr;
+            if (k == vectors - 1)
+                for (int e = bytes(k) / 4; e < 4; ++e) reinterpret_cast<uint32_t*>(ring + i * blockDim.x)[e] = 0;
+        }
+    }
 #pragma unroll
     for (int d = 0; d < D; ++d) ask(d);
     uint4 w[kKept ? VPT : 1];
