@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kPagedBlock, P::Ring::kCtas)
     // columns past D stay zero: nothing is copied there
     if (a.D < DT)
         for (int i = lane; i < S * 2 * Ring::kPart / 16; i += 32)
-            reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+            if (i % (Ring::kPitch / 16) >= a.D / E::kVec) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
     __syncwarp();
 
     PagedCursor<TILE> in(a, units, b, begin - before * units, end - begin), at = in;
