@@ -3,8 +3,10 @@
 //   scale = max(max|y| / 448, 2^-126) over a row or `group` columns;  q = e4m3(y / scale)
 // y itself is never rounded nor stored: with inv = 1 / sqrt(...), max|y| = inv max|s w|,
 // so the sum of squares and the largest magnitudes are one pass over the row and one
-// reduction, and the quotients follow from the registers that hold s. Bound by the
-// traffic: x (and the residual, in and out) and one byte out.
+// reduction, and the quotients follow from the registers that hold s w. Bound by the
+// traffic: x (and the residual, in and out) and one byte out. Measured: bf16 16384 x 8192 with
+// residual, groups of 128, 149 us (139 at the rate of a copy); 256 x 8192 4.1 us; fp32 rows off a 16-byte
+// boundary, 1501 x 4099 in groups of 64, 14.6 us for 4.6, bound by the instructions of their small pieces.
 #pragma once
 
 #include <algorithm>
@@ -98,7 +100,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, const float (&f)[N], bool
 enum QuantMode { kQuantRow, kQuantLanes, kQuantGroups };
 
 // The most threads of a CTA. Four vectors a thread in small pieces: fewer, so that two CTAs share an SM's registers
-// (fp32 1501 x 4099, 288 threads a row: 14 us instead of 18).
+// (fp32 1501 x 4099, 288 threads a row: 14.6 us instead of 18).
 constexpr int kQuantThreads = 512;
 __host__ __device__ constexpr int quant_threads(int piece, int vpt) { return piece < 16 && vpt == 4 ? 320 : kQuantThreads; }
 

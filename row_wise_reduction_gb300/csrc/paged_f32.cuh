@@ -1,6 +1,8 @@
 // Attention over a paged cache, fp32 (paged_kernels.cuh), by fused multiply-adds: G heads
 // take 2 G operations for each element read, 16 cycles a position, head dimension of 128 and 8
-// heads, where the memory takes 44 for its 1 KB.
+// heads, where the memory takes 44 for its 1 KB. Few warps an SM and chains of shuffles between the two
+// products leave it bound by latency all the same: one sequence of 32768 positions, 8 heads of 128 with 4 queries
+// each, 57.9 us (39.5 at the rate of a copy); 9 sequences, a window of 1999, 3 heads of 80 with 5 each, 20.6 us (3.9).
 #pragma once
 
 #include "paged_kernels.cuh"

@@ -178,7 +178,7 @@ static PyObject* bind_operators(PyObject* self, PyObject* const* a, Py_ssize_t n
         args_t v;                                                                                             \
         int r;                                                                                                \
         (void)self;                                                                                           \
-        if (!g_bound[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");          \
+        if (!g_bound[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");             \
         if (take(#name, form, a, n, &v)) return NULL;                                                         \
         Py_BEGIN_ALLOW_THREADS                                                                                \
         r = (expr);                                                                                           \
@@ -189,7 +189,7 @@ static PyObject* bind_operators(PyObject* self, PyObject* const* a, Py_ssize_t n
     static PyObject* name(PyObject* self, PyObject* const* a, Py_ssize_t n) {                                 \
         args_t v;                                                                                             \
         (void)self;                                                                                           \
-        if (!g_bound[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");          \
+        if (!g_bound[slot]) return PyErr_Format(PyExc_RuntimeError, "_rowops_call is not bound");             \
         if (take(#name, form, a, n, &v)) return NULL;                                                         \
         return PyLong_FromSize_t(expr);                                                                       \
     }
@@ -198,27 +198,27 @@ BYTES(groupnorm_act_workspace_bytes, 0, "iiiii",
       ((gn_bytes_fn)g_bound[0])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
 CALL(groupnorm_act, 1, "ppppfiiiiiipipip",
      ((gn_fn)g_bound[1])(v.p[0], v.p[1], v.p[2], v.p[3], v.f[4], v.i[5], v.i[6], v.i[7], v.i[8], v.i[9],
-                            (int)v.i[10], (float*)v.p[11], (int)v.i[12], v.p[13], (size_t)v.i[14], v.p[15]))
+                         (int)v.i[10], (float*)v.p[11], (int)v.i[12], v.p[13], (size_t)v.i[14], v.p[15]))
 BYTES(groupnorm_act_backward_workspace_bytes, 2, "iiiii",
       ((gn_bytes_fn)g_bound[2])(v.i[0], v.i[1], v.i[2], v.i[3], (int)v.i[4]))
 CALL(groupnorm_act_backward, 3, "ppppppppiiiiiiipip",
      ((gn_bwd_fn)g_bound[3])(v.p[0], v.p[1], v.p[2], v.p[3], (float*)v.p[4], v.p[5], (float*)v.p[6],
-                                (float*)v.p[7], v.i[8], v.i[9], v.i[10], v.i[11], v.i[12], (int)v.i[13],
-                                (int)v.i[14], v.p[15], (size_t)v.i[16], v.p[17]))
+                             (float*)v.p[7], v.i[8], v.i[9], v.i[10], v.i[11], v.i[12], (int)v.i[13],
+                             (int)v.i[14], v.p[15], (size_t)v.i[16], v.p[17]))
 CALL(bias_dropout_residual, 4, "ppppfuupiiiip",
      ((drop_fn)g_bound[4])(v.p[0], v.p[1], v.p[2], v.p[3], v.f[4], v.u[5], v.u[6], v.p[7], v.i[8], v.i[9],
-                              v.i[10], (int)v.i[11], v.p[12]))
+                           v.i[10], (int)v.i[11], v.p[12]))
 BYTES(bias_dropout_residual_backward_workspace_bytes, 5, "iii",
       ((rows_bytes_fn)g_bound[5])(v.i[0], v.i[1], (int)v.i[2]))
 CALL(bias_dropout_residual_backward, 6, "pppfuupiiiipip",
      ((drop_bwd_fn)g_bound[6])(v.p[0], v.p[1], (float*)v.p[2], v.f[3], v.u[4], v.u[5], v.p[6], v.i[7], v.i[8],
-                                  v.i[9], (int)v.i[10], v.p[11], (size_t)v.i[12], v.p[13]))
+                               v.i[9], (int)v.i[10], v.p[11], (size_t)v.i[12], v.p[13]))
 CALL(router_balance_loss, 7, "ppipfppiiiiipip",
      ((balance_fn)g_bound[7])(v.p[0], v.p[1], (int)v.i[2], v.p[3], v.f[4], (float*)v.p[5], v.p[6], v.i[7],
-                                 v.i[8], v.i[9], v.i[10], (int)v.i[11], v.p[12], (size_t)v.i[13], v.p[14]))
+                              v.i[8], v.i[9], v.i[10], (int)v.i[11], v.p[12], (size_t)v.i[13], v.p[14]))
 CALL(router_balance_loss_backward, 8, "ppppfpiiiiip",
      ((balance_bwd_fn)g_bound[8])(v.p[0], v.p[1], (float*)v.p[2], v.p[3], v.f[4], v.p[5], v.i[6], v.i[7], v.i[8],
-                                     v.i[9], (int)v.i[10], v.p[11]))
+                                  v.i[9], (int)v.i[10], v.p[11]))
 BYTES(router_balance_loss_workspace_bytes, 9, "iii",
       ((rows_bytes_fn)g_bound[9])(v.i[0], v.i[1], (int)v.i[2]))
 CALL(rmsnorm_quant, 10, "ppppppfiiiiiip",

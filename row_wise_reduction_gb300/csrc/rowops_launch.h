@@ -475,7 +475,7 @@ struct PagedForm {
 // One cluster a unit, where all fit on the GPU at once, saves the second launch and the parts' way through memory;
 // the line shares the tiles out evenly. In times of a tile (of 64 positions in bf16, 32 in fp32), by the table's
 // room: a cluster's share of its unit against the line's share and eight more. 32 heads over 8, D 128, one
-// sequence, clusters and line: room for 512 8.1 and 9.5 us, 4096 16.1 and 18.8, 8192 26.6 and 22.0.
+// sequence, clusters and line: room for 512 7.7 and 10.1 us, 4096 14.9 and 15.4, 8192 24.0 and 17.9.
 inline PagedForm paged_form(int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t room, int64_t window, int es) {
     const int64_t rows = paged_rows(heads / kv_heads, es), units = B * kv_heads * ((heads / kv_heads + rows - 1) / rows);
     const int64_t tile = es == 2 ? 64 : 32, most = window > 0 && window < room ? std::min(room, window + 15) : room;

@@ -24,6 +24,12 @@
 // own masses follow from their own counts. fp32 values differ within a bin: masses are
 // added up beside the counts (in three words of 16 bits and more, each a native 32-bit
 // atomic; 64-bit ones in shared memory took fifteen times as long), and the cut's bin is searched digit by digit.
+//
+// Bound, for many rows, by shared memory: an atomic an element into the histogram and a look-up an element in the
+// CTA that has the draw, banks in conflict (bf16 256 x 131072 with top-p: 112 us, 9.9 of them the reading of
+// the logits; 512 rows without cuts 175; fp32 61 x 50021 with every cut 47). For few, by its steps one after
+// another, up to eight exchanges within the row's cluster, and the fetching of their instructions (bf16 1 x 32000
+// with every cut: 16.5 us on the device). Compact code with the steps as functions is slower in both: 20.5 and 120.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,6 +44,8 @@ namespace cg = cooperative_groups;
 namespace rowops {
 namespace {
 
+// 512 threads a CTA and shares of 64 KB at most: 112 us for 256 rows of 131072 bf16 with top-p, 175 for 512 without
+// cuts; 256 threads and 32 KB 125 and 188, 512 threads and 32 KB 172 and 236 (twice the CTAs in a row's exchanges).
 constexpr int kBlock = 512, kWarps = kBlock / 32;
 constexpr int kCluster = 8;  // the most CTAs of a row
 constexpr int kDigit = 256;  // bins of a digit
