@@ -626,6 +626,7 @@ rowops_status_t rowops_rmsnorm_quant(const void* x, const void* residual, void* 
  *            -infinity. One beyond max_pages * page, or a page outside [0, pages) that
  *            the sequence attends to, makes its out and lse NaN; nothing outside is read.
  *   lse      NULL, or B * heads floats.
+ *   scale    at most 2^127 in magnitude.
  *   window   0, or how many of the last positions are attended to.
  *   workspace, workspace_bytes   device memory, 256-byte aligned, at least
  *            rowops_paged_attention_workspace_bytes(...) bytes (overwritten; 0: NULL
@@ -663,6 +664,7 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
  *   logits   device pointer to M rows of `ld` elements of `dtype`. A column of -inf is
  *            never drawn. If there is nothing else in the row, or a NaN in it, its token
  *            is -1 and its logprob NaN. Columns of +inf are drawn from alone, evenly.
+ *            A difference x_j - m beyond the range of fp32 counts as -infinity.
  *   u        device pointer to M floats in [0, 1) (below: as 0; 1 and more: the last kept).
  *   temperature, top_k, top_p, min_p   device pointers to M numbers, one a row, or NULL:
  *            the `_all` number then holds for every row. (On the device, numbers below

@@ -1474,7 +1474,7 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
                                        int64_t head_stride, int64_t max_pages, int64_t ldt, rowops_dtype_t dtype,
                                        void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (!valid_dtype(dtype) || B < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || D < 1 || pages < 0 ||
-        page < 1 || max_pages < 0 || ldt < max_pages || window < 0 || !std::isfinite(scale) || page_stride < 0 ||
+        page < 1 || max_pages < 0 || ldt < max_pages || window < 0 || !(std::fabs(scale) <= 0x1p127f) || page_stride < 0 ||
         slot_stride < 0 || head_stride < 0)
         return ROWOPS_ERR_INVALID_VALUE;
     if (D > kPagedMaxD || heads > INT32_MAX / D || B > kPagedMaxB || B > INT32_MAX / heads || page > INT32_MAX ||

@@ -55,7 +55,8 @@ def test_paged_attention_refusals(lib):
                 ldt, dt, ws, need if nb is None else nb, None)
 
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(table=None), dict(lengths=None), dict(out=None),
-                dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1), dict(B=-1), dict(H=0), dict(KV=0),
+                dict(scale=float("nan")), dict(scale=float("inf")),
+                dict(scale=-3e38), dict(window=-1), dict(B=-1), dict(H=0), dict(KV=0),
                 dict(KV=3), dict(D=0), dict(ldq=511), dict(ldo=511), dict(pages=-1), dict(page=0), dict(ps=-1),
                 dict(ss=-1), dict(hs=-1), dict(width=-1), dict(ldt=499), dict(dt=2), dict(q=X + 1), dict(k=K + 1),
                 dict(v=V + 1), dict(out=OUT + 1), dict(table=TABLE + 2), dict(lengths=LENGTHS + 2), dict(lse=LSE + 2),
