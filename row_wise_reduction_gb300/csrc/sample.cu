@@ -565,14 +565,14 @@ __device__ __forceinline__ int which(uint64_t mass, uint32_t ties, int parts, ui
 
 template <typename T>
 __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ SampleArgs a,
-                                                        const __grid_constant__ Roots roots, int share) {
+                                                        const __grid_constant__ Roots roots, int share, bool held) {
     using E = Elem<T>;
     using R = Row<T>;
     __shared__ Shared sh;
     extern __shared__ uint4 dynamic[];
     uint32_t* counts = reinterpret_cast<uint32_t*>(dynamic);
-    uint64_t* part_masses = reinterpret_cast<uint64_t*>(counts + kHeldWords<T>);
-    const int part_room = kBinsHeld / int(cg::this_cluster().num_blocks());
+    uint64_t* part_masses = reinterpret_cast<uint64_t*>(counts + (held ? kHeldWords<T> : 0));
+    const int part_room = held ? kBinsHeld / int(cg::this_cluster().num_blocks()) : 0;
     uint32_t* part_counts = reinterpret_cast<uint32_t*>(part_masses + part_room);
     T* x = reinterpret_cast<T*>(part_counts + part_room);
     cg::cluster_group cluster = cg::this_cluster();
@@ -590,7 +590,8 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
         for (int c = whole * E::kVec + threadIdx.x; c < n; c += kBlock) x[c] = from[c];
         for (int c = n + threadIdx.x; c < (n + E::kVec - 1) / E::kVec * E::kVec; c += kBlock) E::store(x + c, -INFINITY);
         if (threadIdx.x < kDigit) sh.mass[0][threadIdx.x] = sh.mass[1][threadIdx.x] = 0;
-        for (int i = threadIdx.x; i < (R::kF32 ? 4 : 1) * kBinsHeld; i += kBlock) counts[i] = 0;
+        if (held)
+            for (int i = threadIdx.x; i < (R::kF32 ? 4 : 1) * kBinsHeld; i += kBlock) counts[i] = 0;
         if (threadIdx.x < 16) sh.roots[threadIdx.x] = roots.v[threadIdx.x];
         asm volatile("cp.async.commit_group;" ::: "memory");
         // what of the row's numbers needs 64 bits, by a thread each while the copies are on their way
@@ -861,7 +862,9 @@ cudaError_t launch(const SampleArgs& a, const LaunchCfg& cfg) {
                             (a.M * C * 2 <= 2 * cfg.num_sms && a.N >= 2 * C * 4096)))
         C *= 2;
     const int share = ((a.N + C - 1) / C + V - 1) / V * V;
-    const size_t smem = size_t(share) * sizeof(T) + size_t(kHeldWords<T>) * 4 + size_t(kBinsHeld / C) * 12;
+    // fp32 rows without top-k and top-p need no histogram, whose room a second CTA of the SM can have
+    const bool held = sizeof(T) == 2 || a.top_k || a.top_p || a.top_p_all < 1.f || (a.top_k_all > 0 && a.top_k_all < a.N);
+    const size_t smem = size_t(share) * sizeof(T) + (held ? size_t(kHeldWords<T>) * 4 + size_t(kBinsHeld / C) * 12 : 0);
     auto k = sample_kernel<T>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, cfg);
     if (e != cudaSuccess) return e;
@@ -876,7 +879,7 @@ cudaError_t launch(const SampleArgs& a, const LaunchCfg& cfg) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, k, a, roots, share);
+    return cudaLaunchKernelEx(&lc, k, a, roots, share, held);
 }
 
 }  // namespace
