@@ -23,13 +23,14 @@
 // times its value's weight, so weights are computed by the bin and not by the element, and the CTAs'
 // own masses follow from their own counts. fp32 values differ within a bin: masses are
 // added up beside the counts (in three words of 16 bits and more, each a native 32-bit
-// atomic; 64-bit ones in shared memory took fifteen times as long), and the cut's bin is searched digit by digit.
+// atomic; 64-bit ones in shared memory took fifteen times as long), and the cut's bin is searched: its elements are compared
+// with one another if they are few, else digit by digit (61 x 50021 with every cut 37 us, by digits always 46).
 //
 // Bound, for many rows, by shared memory: an atomic an element into the histogram and a look-up an element in the
-// CTA that has the draw, banks in conflict (bf16 256 x 131072 with top-p: 112 us, 9.9 of them the reading of
-// the logits; 512 rows without cuts 175; fp32 61 x 50021 with every cut 47). For few, by its steps one after
+// CTA that has the draw, banks in conflict (bf16 256 x 131072 with top-p: 110 us, 9.9 of them the reading of
+// the logits; 512 rows without cuts 170; fp32 61 x 50021 with every cut 37). For few, by its steps one after
 // another, up to eight exchanges within the row's cluster, and the fetching of their instructions (bf16 1 x 32000
-// with every cut: 16.5 us on the device). Compact code with the steps as functions is slower in both: 20.5 and 120.
+// with every cut: 16.5 us on the device). Compact code with the steps as functions is slower in both: 20.5 and 120 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -44,8 +45,9 @@ namespace cg = cooperative_groups;
 namespace rowops {
 namespace {
 
-// 512 threads a CTA and shares of 64 KB at most: 112 us for 256 rows of 131072 bf16 with top-p, 175 for 512 without
-// cuts; 256 threads and 32 KB 125 and 188, 512 threads and 32 KB 172 and 236 (twice the CTAs in a row's exchanges).
+// 512 threads a CTA and shares of 64 KB at most: 110 us for 256 rows of 131072 bf16 with top-p, 170 for 512 without
+// cuts; an earlier form of it took 112 and 175, with 256 threads
+// and 32 KB 125 and 188, with 512 threads and 32 KB 172 and 236 (twice the CTAs in a row's exchanges).
 constexpr int kBlock = 512, kWarps = kBlock / 32;
 constexpr int kCluster = 8;  // the most CTAs of a row
 constexpr int kDigit = 256;  // bins of a digit
@@ -68,10 +70,10 @@ struct Weights {
     // past the fifth are below 2^-36. The difference and the product carry their errors
     // along: what is lost is f's own rounding and the series', about 2^-29.
     __device__ __forceinline__ uint64_t operator()(float x) const {
-        if (x == m) return kOne;
         const float d = m - x, bb = d - m, dl = (m - (d - bb)) - (x + bb);
-        const float t = -d * c_hi;
-        if (!(t > -62.f) || x == -INFINITY) return 0;
+        float t = -d * c_hi;
+        const bool some = t > -62.f;  // (false for a NaN, which -inf times a c of 0 gives)
+        t = some ? t : 0.f;
         const float tl = -(fmaf(d, c_hi, t) + fmaf(d, c_lo, dl * c_hi));
         const float r = fmaf(t, 16.f, 12582912.f);
         const int z = __float_as_int(r) - 0x4b400000;
@@ -80,8 +82,9 @@ struct Weights {
                                  0.69314718f);
         const uint64_t root = roots[z & 15];
         const int64_t w = int64_t(root) + ((int64_t(int32_t(root >> 14)) * __float2int_rn(g * 0x1p35f)) >> 21);
-        const int s = -(z >> 4);
-        return (uint64_t(w) + ((uint64_t(1) << s) >> 1)) >> s;
+        const int s = some ? -(z >> 4) : 0;
+        const uint64_t rounded = (uint64_t(w) + ((uint64_t(1) << s) >> 1)) >> s;
+        return x == m ? kOne : some ? rounded : 0;  // (no branches: the weights of a vector overlap)
     }
 };
 
@@ -121,7 +124,15 @@ struct Found {
 
 struct Shared {
     uint64_t roots[16];
-    uint64_t mass[2][kDigit];  // digits: masses, or counts
+    union {
+        uint64_t mass[2][kDigit];  // digits: masses, or counts
+        struct {                   // or the elements of a cut's bin, by their distance from its largest key
+            uint32_t list[2][kDigit];  // top-k's, top-p's: read by the others
+            uint64_t mass[kDigit];     // of the elements of all CTAs
+        } few;
+    };
+    uint32_t listed[2];
+    uint64_t mass_before;
     uint64_t warp_mass[kWarps];
     uint32_t warp_count[kWarps];
     float warp_top[kWarps], warp_low[kWarps];
@@ -251,18 +262,30 @@ struct Row {
     // This CTA's histogram. bf16: counts, and the mass near zero; fp32: what is asked for.
     __device__ __forceinline__ void count(bool masses) {
         if constexpr (kF32) {
-            each([&](float v) {
-                const uint32_t bin = bin_of(ordered(v) >> 16);
-                if (bin >= uint32_t(bins)) return;
+            for (int k = threadIdx.x; k * E::kVec < n; k += kBlock) {
+                float v[E::kVec];
+                E::unpack(reinterpret_cast<const uint4*>(x)[k], v);
+                uint32_t bin[E::kVec];
+#pragma unroll
+                for (int e = 0; e < E::kVec; ++e) bin[e] = bin_of(ordered(v[e]) >> 16);
                 if (masses) {
-                    const uint64_t m = w(v);
-                    if (m == 0) return;
-                    atomicAdd(counts + kBinsHeld + bin, uint32_t(m) & 0xffffu);
-                    atomicAdd(counts + 2 * kBinsHeld + bin, uint32_t(m >> 16) & 0xffffu);
-                    if (m >> 32) atomicAdd(counts + 3 * kBinsHeld + bin, uint32_t(m >> 32));
+                    uint64_t m[E::kVec];
+#pragma unroll
+                    for (int e = 0; e < E::kVec; ++e) m[e] = w(v[e]);
+#pragma unroll
+                    for (int e = 0; e < E::kVec; ++e) {
+                        if (bin[e] >= uint32_t(bins) || m[e] == 0) continue;
+                        atomicAdd(counts + kBinsHeld + bin[e], uint32_t(m[e]) & 0xffffu);
+                        atomicAdd(counts + 2 * kBinsHeld + bin[e], uint32_t(m[e] >> 16) & 0xffffu);
+                        if (m[e] >> 32) atomicAdd(counts + 3 * kBinsHeld + bin[e], uint32_t(m[e] >> 32));
+                        atomicAdd(counts + bin[e], 1u);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E::kVec; ++e)
+                        if (bin[e] < uint32_t(bins)) atomicAdd(counts + bin[e], 1u);
                 }
-                atomicAdd(counts + bin, 1u);
-            });
+            }
         } else {
             uint64_t near = 0;
             for (int k = threadIdx.x; k * E::kVec < n; k += kBlock) {
@@ -381,11 +404,81 @@ struct Row {
     }
 
     // The cut in a bin whose elements differ, where the counts (or the masses, of what
-    // `within` keeps) reach `goal`, `before` of it in the bins before: digit by digit of the distance
-    // from the bin's largest key. `flip`: which digit's bins are next; both sets
-    // are zero here and when it returns.
+    // `within` keeps) reach `goal`, `before` of it in the bins before; *mass becomes the mass of the bin's elements before
+    // the cut. Of at most kDigit elements: each CTA lists its own, and every CTA compares each with all, a thread
+    // each. Of more: digit by digit (the mass by a sweep, if `want`).
     template <bool MASS>
-    __device__ Cut find(cg::cluster_group& cluster, uint32_t bin, uint64_t goal, uint64_t before, Cut within, int& flip) {
+    __device__ Cut find(cg::cluster_group& cluster, uint32_t bin, uint64_t goal, uint64_t before, Cut within, int& flip,
+                        bool want, uint64_t* mass) {
+        const uint32_t top = kF32 ? bin_top(bin) << 16 | 0xffffu : bin_top(bin);
+        const uint32_t width = near_zero(bin) ? (2u * least << (16 - kDrop)) - 1 : 0xffffu;
+        const uint32_t from = (top_key >> kDrop) - top;  // kd of the bin's largest key (mod 2^32: it may be past the maximum's)
+        each([&](float v) {
+            const uint32_t at = top - key(v);
+            if (at > width || (MASS && from + at >= within.kd)) return;
+            const uint32_t i = atomicAdd(&sh.listed[MASS], 1u);
+            if (i < kDigit) sh.few.list[MASS][i] = at;
+        });
+        meet(cluster);
+        const int i = threadIdx.x;
+        uint32_t n = 0, at = 0;
+        bool mine = false;
+        uint32_t here[kCluster];
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) here[r] = r < C ? cluster.map_shared_rank(&sh, r)->listed[MASS] : 0;
+        int of = 0;
+        uint32_t place = 0;
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) {
+            if (uint32_t(i) - n < here[r] && i < kDigit) of = r, place = uint32_t(i) - n, mine = true;
+            n += here[r];
+        }
+        if (mine) at = cluster.map_shared_rank(&sh, of)->few.list[MASS][place % kDigit];
+        // those equal to the k-th value that are among the first k: one more element, of their mass
+        const uint32_t tie = within.kd - from;
+        const bool ties = MASS && within.ties && tie <= width;
+        if (n + ties > kDigit) {
+            meet(cluster);  // the lists' place becomes the digits'
+            if (i < kDigit) sh.mass[0][i] = sh.mass[1][i] = 0;
+            __syncthreads();
+            const Cut cut = find_digits<MASS>(cluster, bin, goal, before, within, flip);
+            if (want) *mass = mass_in(cluster, bin, cut.kd);
+            return cut;
+        }
+        uint32_t* all = sh.few.list[!MASS];
+        if (mine) {
+            all[i] = at;
+            sh.few.mass[i] = w(value_at(from + at));
+        } else if (ties && uint32_t(i) == n) {
+            at = all[i] = tie;
+            sh.few.mass[i] = uint64_t(within.ties) * w(value_at(within.kd));
+        }
+        n += ties;
+        __syncthreads();
+        if (uint32_t(i) < n) {
+            uint64_t less = 0, equal = 0, mass_less = 0;
+            for (uint32_t j = 0; j < n; ++j) {
+                const uint32_t other = all[j];
+                const uint64_t m = sh.few.mass[j], one = MASS ? m : 1;
+                less += other < at ? one : 0;
+                equal += other == at ? one : 0;
+                if constexpr (!MASS) mass_less += other < at ? m : 0;
+            }
+            if (before + less < goal && before + less + equal >= goal) {  // (equal ones tell the same)
+                sh.bin = at;
+                sh.before = before + less;
+                sh.mass_before = mass_less;
+            }
+        }
+        __syncthreads();
+        if (want) *mass = sh.mass_before;
+        return reach<MASS>(from + sh.bin, goal - sh.before, within);
+    }
+    // The same, of any number of elements, digit by digit of the distance from the bin's largest key. `flip`: which
+    // digit's bins are next; both sets are zero here and when it returns.
+    template <bool MASS>
+    __device__ Cut find_digits(cg::cluster_group& cluster, uint32_t bin, uint64_t goal, uint64_t before, Cut within,
+                               int& flip) {
         const uint32_t top = kF32 ? bin_top(bin) << 16 | 0xffffu : bin_top(bin);
         const uint32_t width = near_zero(bin) ? (2u * least << (16 - kDrop)) - 1 : 0xffffu;
         const uint32_t from = (top_key >> kDrop) - top;  // kd of the bin's largest key (mod 2^32: it may be past the maximum's)
@@ -564,7 +657,7 @@ __device__ __forceinline__ int which(uint64_t mass, uint32_t ties, int parts, ui
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ SampleArgs a,
+__global__ void __launch_bounds__(kBlock, 2) sample_kernel(const __grid_constant__ SampleArgs a,
                                                         const __grid_constant__ Roots roots, int share, bool held) {
     using E = Elem<T>;
     using R = Row<T>;
@@ -589,7 +682,7 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
         for (int k = threadIdx.x; k < whole; k += kBlock) copy_async<16>(x + k * E::kVec, from + k * E::kVec);
         for (int c = whole * E::kVec + threadIdx.x; c < n; c += kBlock) x[c] = from[c];
         for (int c = n + threadIdx.x; c < (n + E::kVec - 1) / E::kVec * E::kVec; c += kBlock) E::store(x + c, -INFINITY);
-        if (threadIdx.x < kDigit) sh.mass[0][threadIdx.x] = sh.mass[1][threadIdx.x] = 0;
+        if (threadIdx.x < 2) sh.listed[threadIdx.x] = 0;
         if (held)
             for (int i = threadIdx.x; i < (R::kF32 ? 4 : 1) * kBinsHeld; i += kBlock) counts[i] = 0;
         if (threadIdx.x < 16) sh.roots[threadIdx.x] = roots.v[threadIdx.x];
@@ -731,8 +824,9 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
                 within = Cut{r.bin_kd(in.bin), uint32_t(top_k) - in.count};
                 mass_all = in.mass;
             } else {
-                within = r.template find<false>(cluster, in.bin, uint64_t(top_k), in.count, within, flip);
-                if (cut_p) mass_all = in.mass + r.mass_in(cluster, in.bin, within.kd);
+                uint64_t mass_before = 0;
+                within = r.template find<false>(cluster, in.bin, uint64_t(top_k), in.count, within, flip, cut_p, &mass_before);
+                if (cut_p) mass_all = in.mass + mass_before;
             }
             mass_all += uint64_t(within.ties) * r.w(r.value_at(within.kd));
             cut = shorter(cut, within);
@@ -747,7 +841,7 @@ __global__ void __launch_bounds__(kBlock) sample_kernel(const __grid_constant__ 
             }
             cut = shorter(cut, r.single(f.bin)
                                    ? r.template reach<true>(r.bin_kd(f.bin), goal - f.mass, within)
-                                   : r.template find<true>(cluster, f.bin, goal, f.mass, within, flip));
+                                   : r.template find<true>(cluster, f.bin, goal, f.mass, within, flip, false, nullptr));
         }
     }
 

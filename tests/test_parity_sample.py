@@ -279,3 +279,38 @@ def test_top_k_of_more_than_32_bits():
             ro.rowops_sample(x, u, top_k=k)
     with pytest.raises(TypeError):
         ro.rowops_sample(x, u, top_k=50.5)
+
+
+@pytest.mark.parametrize("N", [3000, 70000])
+@pytest.mark.parametrize("n", [1, 2, 100, 254, 255, 256, 257, 258, 1500])
+@pytest.mark.parametrize("equal", [1, 3])
+def test_cuts_among_values_close_together(n, equal, N):
+    """n values within 2^-8 of one another, groups of `equal` the same, all others far below."""
+    M = 6
+    g = torch.Generator().manual_seed(33)
+    x = -6 + 0.5 * torch.randn(M, N, generator=g)
+    for i in range(M):
+        x[i, torch.randperm(N, generator=g)[:n]] = 1 + torch.randperm(n, generator=g).div(equal, rounding_mode="floor") * 2.0**-20
+    x, u = place(x, "f32"), uniform(M, 34)
+    for k in sorted({1, (n + 1) // 2, max(1, n - 1), n, n + 1}):
+        check(x, u, top_k=k)
+        check(x, u, top_k=k, top_p=0.45)
+    for p in (0.3, 0.999):
+        check(x, u, top_p=p)
+        check(x, u, top_p=p, top_k=n + 5, temperature=0.5)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N", [40, 257, 5000, 70000])
+def test_cuts_among_values_near_zero(dtype, N):
+    """One large logit, the others so far below it that they share the place of zero, of both signs, and 0 itself."""
+    x = rows(6, N, 35, 0.5)
+    x[:, ::7] = 0
+    x[:, 1::14] = -0.0
+    x[:, 5] = 30000.0
+    x, u = place(x, dtype), 1 - uniform(6, 36) * 2.0**-4
+    for k in (2, N // 3, N // 2, N - 1):
+        check(x, u, temperature=20000.0, top_k=k)
+        check(x, u, temperature=20000.0, top_k=k, top_p=0.6)
+    check(x, u, temperature=20000.0, top_p=0.9)
+    check(x, u, temperature=1e6, top_p=0.37)
