@@ -58,11 +58,11 @@ def check(lengths, H, K, D, page, dtype, window=0, scale=None, **more):
     lse = torch.full((B + 2, H), 3.0, device="cuda")
     got = ro.rowops_paged_attention(q, k, v, table, n, scale, window, out[1:-1], lse[1:-1])
     assert torch.all(out[0] == 3) and torch.all(out[-1] == 3) and torch.all(lse[0] == 3) and torch.all(lse[-1] == 3)
-    judge(got, lse[1:-1], q, k, v, table, n, scale, window)
+    hold(got, lse[1:-1], q, k, v, table, n, scale, window)
     return got, lse[1:-1], (q, k, v, table, n)
 
 
-def judge(got, lse, q, k, v, table, n, scale=None, window=0):
+def hold(got, lse, q, k, v, table, n, scale=None, window=0):
     D = q.shape[2]
     dtype = "f32" if q.dtype == torch.float32 else "bf16"
     ref, rlse, size, steps = O.paged_attention(*(C.to_f64(t) for t in (q, k, v)), table.cpu().numpy(), n.cpu().numpy(),
@@ -164,16 +164,16 @@ def test_pages_outside_the_pool_and_lengths_beyond_the_table(dtype, page, more):
     table[3, 2] = 1 << 30  # not reached
     n[4] = table.shape[1] * page + 1
     out = ro.rowops_paged_attention(q, k, v, table, n, lse=lse)
-    judge(out, lse, q, k, v, table, n)
+    hold(out, lse, q, k, v, table, n)
     n[4] = 2**31 - 1
     out = ro.rowops_paged_attention(q, k, v, table, n, lse=lse)
-    judge(out, lse, q, k, v, table, n)
+    hold(out, lse, q, k, v, table, n)
     table[1, 2] = table[0, 0]
     n[1] = 40  # the bad page within a window's reach or not
     table[2, 0] = -9
     table[2, last] = table[0, 1]
     out = ro.rowops_paged_attention(q, k, v, table, n, None, 50, lse=lse)
-    judge(out, lse, q, k, v, table, n, None, 50)
+    hold(out, lse, q, k, v, table, n, None, 50)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -195,7 +195,7 @@ def test_scores_far_apart(dtype):
         q, k, v, table, n = problem([300], 2, 1, 64, 16, dtype)
         k[table[0, where // 16].long(), where % 16, 0] = 40 * torch.sign(q[0, 0])
         lse = torch.empty(1, 2, device="cuda")
-        judge(ro.rowops_paged_attention(q, k, v, table, n, lse=lse), lse, q, k, v, table, n)
+        hold(ro.rowops_paged_attention(q, k, v, table, n, lse=lse), lse, q, k, v, table, n)
 
 
 @pytest.mark.parametrize("width", [57, 4000])  # one kernel; two, with a workspace
@@ -223,7 +223,7 @@ def test_repeatable_on_a_stream_and_in_a_replayed_graph(width):
         n.copy_(m)
         ws.fill_(0x7f)
         g.replay()
-        judge(y, lse, q, k, v, table, n)
+        hold(y, lse, q, k, v, table, n)
 
 
 def test_refusals():

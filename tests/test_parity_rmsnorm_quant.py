@@ -34,7 +34,7 @@ def relative(N):
     return ((max(64, N / 512) + 32) / 2 + 8) * 2.0**-24
 
 
-def judge(q, scales, s, w, group, eps=1e-5):
+def hold(q, scales, s, w, group, eps=1e-5):
     """q and scales for the summed rows s (as stored)."""
     M, N = s.shape
     y = O.rmsnorm(s, w, eps)
@@ -61,7 +61,7 @@ def check(M, N, dtype, group=0, residual=True, weight=True, pad=0, offset=0, qpa
         gu.assert_guard_untouched(buf, inside)
     else:
         assert s is None
-    judge(q, scales, C.to_f64(s if residual else x), None if w is None else C.to_f64(w), group)
+    hold(q, scales, C.to_f64(s if residual else x), None if w is None else C.to_f64(w), group)
     mark = torch.full_like(base, 0)
     torch.as_strided(mark, (M, N), (N + qpad, 1), qoffset + 16).fill_(1)
     assert torch.all(base[mark == 0] == 0x55), "a kernel wrote outside q's rows"
@@ -149,7 +149,7 @@ def test_nothing_and_not_a_number(dtype, N):
         assert torch.isnan(n[3, last:]).all() and torch.isnan(scales[3, -1])
         assert torch.all(n[3, :last] == 0) and torch.all(scales[3, :-1] == 2.0**-126)
         rows = [0, 4, 5]
-        judge(q[rows], scales[rows], C.to_f64(x[rows]), None, group)
+        hold(q[rows], scales[rows], C.to_f64(x[rows]), None, group)
 
 
 def test_a_long_tail_of_small_numbers_keeps_its_own_scale():
@@ -157,7 +157,7 @@ def test_a_long_tail_of_small_numbers_keeps_its_own_scale():
     x = place(normal(4, 512, 6), "f32")
     x[:, 5] = 1e4
     q, scales, _ = ro.rowops_rmsnorm_quant(x, group=128)
-    judge(q, scales, C.to_f64(x), None, 128)
+    hold(q, scales, C.to_f64(x), None, 128)
     y = O.rmsnorm(C.to_f64(x), None, 1e-5)
     back = q.double().cpu().numpy() * np.repeat(scales.double().cpu().numpy(), 128, axis=1)
     assert np.all(np.abs(back - y)[:, 128:] <= 2.0**-4 * 1.001 * np.abs(y[:, 128:]) + scales.max().item() * 2.0**-10)

@@ -6,7 +6,7 @@ import torch
 import row_wise_reduction_gb300 as ro
 from tests import _compare as C
 from tests import gpu_util as gu
-from tests.test_parity_rmsnorm_quant import judge
+from tests.test_parity_rmsnorm_quant import hold
 
 pytestmark = [pytest.mark.gpu, gu.requires_gpu]
 
@@ -18,7 +18,7 @@ def test_rmsnorm_quant(N):
     x[-64:] = torch.randn(64, N, device="cuda")
     q, s, out = ro.rowops_rmsnorm_quant(x, x, None, 1e-5, 128)
     # few rows are summed in another order than many: the rows are held to the 64-bit form
-    judge(q[-64:], s[-64:], C.to_f64(out[-64:]), None, 128)
+    hold(q[-64:], s[-64:], C.to_f64(out[-64:]), None, 128)
     assert torch.equal(out[-64:], x[-64:] + x[-64:])
     assert torch.all(q[: 1 << 17].view(torch.uint8) == 0)
 

@@ -11,8 +11,8 @@ import row_wise_reduction_gb300 as ro
 from oracle import serving as O
 from tests import _compare as C
 from tests import gpu_util as gu
-from tests.test_parity_paged_attention import judge as judge_attention
-from tests.test_parity_rmsnorm_quant import judge as judge_norm
+from tests.test_parity_paged_attention import hold as hold_attention
+from tests.test_parity_rmsnorm_quant import hold as hold_norm
 
 pytestmark = [pytest.mark.gpu, gu.requires_gpu]
 
@@ -70,10 +70,10 @@ class Decoder:
         logits = self.product(q2, s2, N, self.head)
         ro.rowops_sample(logits, self.u, **KNOBS, token=self.token, logprob=self.logprob)
         if check:
-            judge_norm(q1, s1, C.to_f64(x), C.to_f64(self.w1), 64)
-            judge_attention(out, self.lse, heads, self.k, self.v, self.table, self.lengths)
+            hold_norm(q1, s1, C.to_f64(x), C.to_f64(self.w1), 64)
+            hold_attention(out, self.lse, heads, self.k, self.v, self.table, self.lengths)
             assert torch.equal(x2, (a.float() + x.float()).to(a.dtype))
-            judge_norm(q2, s2, C.to_f64(x2), C.to_f64(self.w2), 0)
+            hold_norm(q2, s2, C.to_f64(x2), C.to_f64(self.w2), 0)
             knobs = {n: float(np.float32(v)) if n != "top_k" else v for n, v in KNOBS.items()}
             for b in range(B):
                 want, lp, margin = O.sample_row(C.to_f64(logits[b]), float(self.u[b]), **knobs)
