@@ -43,11 +43,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 template <int DT, int H>
 struct PagedBf16 {
     using T = bf16_t;
-    static constexpr int kTokens = 16, kRows = 8 * H, kD = DT, kOwn = 2 * H, kPitch = DT + 4;
-    // Long heads' queries stay in shared memory
-    static constexpr bool kKept = DT * H < 320;
-    static constexpr size_t kScratch = kKept ? 0 : size_t(DT / 16) * H * 32 * 8;
-    using Ring = PagedRing<T, DT, kTokens, kRows>;
+    static constexpr int kRows = 8 * H, kD = DT, kOwn = 2 * H;
+    using Ring = PagedRing<T, DT, kRows>;
+    static constexpr int kTokens = Ring::kShape.tokens, kPitch = Ring::kShape.joined, kScratch = Ring::kShape.scratch;
+    static constexpr bool kKept = kScratch == 0;  // long heads' queries stay in shared memory
+    static_assert(kKept || kScratch == DT / 16 * H * 32 * 8);
     uint2 q[kKept ? DT / 16 : 1][H];
     uint2* far;  // [DT / 16][H][32], every warp writes the same
     float o[DT / 16][H][4], m[H][2], l[H][2];

@@ -16,11 +16,12 @@ namespace rowops {
 template <int DT, int G>
 struct PagedF32 {
     using T = float;
-    static constexpr int kTokens = 8, kRows = G, kD = DT, kOwn = G, kPitch = DT;
+    static constexpr int kRows = G, kD = DT, kOwn = G;
+    using Ring = PagedRing<T, DT, kRows>;
+    static constexpr int kTokens = Ring::kShape.tokens, kPitch = Ring::kShape.joined, kScratch = Ring::kShape.scratch;
+    static_assert(kTokens == 8 && kPitch == DT);
     static constexpr int kVectors = DT / 4, kHalves = kVectors <= 16 ? 2 : 1, kEach = (kVectors + 31) / 32;
     static constexpr int kHeads = G > 4 ? G / 4 : 1;
-    static constexpr size_t kScratch = size_t(G) * DT * 4 + size_t(kPagedWarps) * G * 9 * 4 + 16;
-    using Ring = PagedRing<T, DT, kTokens, kRows>;
     float *q, *weights, *keeps;  // [G][DT] of the CTA; [G][8] and [G] of the warp
     float o[G][kEach][4], m[kHeads], l[kHeads];
 

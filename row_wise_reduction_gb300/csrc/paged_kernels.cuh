@@ -31,22 +31,17 @@
 
 namespace rowops {
 
-constexpr int kPagedWarps = 4, kPagedBlock = 32 * kPagedWarps;
+constexpr int kPagedBlock = 32 * kPagedWarps;
 
-// A warp's ring: pieces of TOKENS positions, their keys, then their values. Rows lie an odd number
-// of 16-byte vectors apart, so eight rows' vectors lie in different banks.
-// As many steps (6 at most) as let three CTAs share an SM, if those are two and the registers allow it (ROWS at most 8),
-// else two CTAs, else three steps in one. Three for two: D 64, heads before slots, 64 sequences of up to 8192, bf16 131 to 110 us,
-// fp32 268 to 213; D 128 186 to 182.
-template <typename T, int DT, int TOKENS, int ROWS>
+// A warp's ring: pieces of a few positions, their keys, then their values.
+template <typename T, int DT, int ROWS>
 struct PagedRing {
-    static constexpr int kPitch = (DT * int(sizeof(T)) / 16 | 1) * 16;
-    static constexpr int kPart = TOKENS * kPitch;          // keys, or values
-    static constexpr int kStep = 2 * kPart * kPagedWarps;  // of the CTA
-    static constexpr int kCtas = ROWS <= 8 && 72000 / kStep >= 2 ? 3 : 104448 / kStep >= 2 ? 2 : 1;
-    static constexpr int kFit = (kCtas == 3 ? 72000 : 104448) / kStep;
-    static constexpr int kStages = kCtas == 1 ? 3 : kFit > 6 ? 6 : kFit;
-    static constexpr int kBytes = kStep * kStages;
+    static constexpr PagedShape kShape = paged_shape(sizeof(T), DT, ROWS);
+    static constexpr int kPitch = kShape.pitch;
+    static constexpr int kPart = kShape.tokens * kPitch;  // keys, or values
+    static constexpr int kCtas = kShape.ctas, kStages = kShape.stages;
+    static constexpr int kBytes = kShape.step * kStages;
+    static_assert((kBytes + kShape.fixed) * kCtas <= kSmShared);
 };
 
 // The tiles of one unit of sequence b, which attends to the positions [first, n); they

@@ -8,6 +8,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "paged_plan.h"
+
 namespace rowops {
 
 // Rows of stride `row_bytes` start at offsets that repeat modulo 16 bytes with
@@ -444,7 +446,6 @@ cudaError_t rms_quant_f32(const QuantArgs& a, int piece, const LaunchCfg& cfg);
 cudaError_t rms_quant_bf16(const QuantArgs& a, int piece, const LaunchCfg& cfg);
 
 // Attention over a paged cache. Strides in elements.
-constexpr int kPagedMaxD = 256;
 constexpr int64_t kPagedMaxB = int64_t(1) << 24;  // every CTA counts the sequences' tiles, in 32 bits of sequences
 struct PagedArgs {
     const void *q, *k, *v;
@@ -455,41 +456,6 @@ struct PagedArgs {
     int64_t window, B, heads, kv_heads, D, pages, page, max_pages, table_ld, ldq, ldo, page_stride, slot_stride,
         head_stride;
 };
-// At most kPagedMaxCtas CTAs (three a SM), each of which leaves two parts: for a block of heads their
-// weighted values, a maximum and a sum each, D rounded up to one of the kernels' widths.
-constexpr int kPagedMaxCtas = 3 * 152;
-constexpr int kPagedWidths[] = {64, 80, 96, 128, 160, 192, 256};
-inline int paged_width(int64_t D) {
-    for (int w : kPagedWidths)
-        if (D <= w) return w;
-    return 0;
-}
-inline int paged_rows(int64_t group, int es) { return es == 2 ? (group > 8 ? 16 : 8) : group > 4 ? 8 : group > 1 ? 4 : 1; }
-constexpr int kPagedCluster = 8;
-// Clusters of this many CTAs, one a unit (0: the line of tiles, with parts in the workspace); the most tiles that
-// the sequences can have.
-struct PagedForm {
-    int cluster;
-    int64_t tiles;
-};
-// One cluster a unit, where all fit on the GPU at once, saves the second launch and the parts' way through memory;
-// the line shares the tiles out evenly. In times of a tile (of 64 positions in bf16, 32 in fp32), by the table's
-// room: a cluster's share of its unit against the line's share and eight more. 32 heads over 8, D 128, one
-// sequence, clusters and line: room for 512 7.7 and 10.1 us, 4096 14.9 and 15.4, 8192 24.0 and 17.9.
-inline PagedForm paged_form(int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t room, int64_t window, int es) {
-    const int64_t rows = paged_rows(heads / kv_heads, es), units = B * kv_heads * ((heads / kv_heads + rows - 1) / rows);
-    const int64_t tile = es == 2 ? 64 : 32, most = window > 0 && window < room ? std::min(room, window + 15) : room;
-    const int64_t each = (most + tile - 1) / tile, slots = 152 * (D > 192 ? 1 : 2);
-    PagedForm f = {0, std::min<int64_t>(each, 1 << 20) * units};
-    int C = kPagedCluster;
-    while (C > 1 && (units * C > slots || C >= 2 * each)) C /= 2;
-    if (units * C <= slots && (each + C - 1) / C <= each * units / slots + 8) f.cluster = C;
-    return f;
-}
-inline size_t paged_bytes(int64_t B, int64_t heads, int64_t kv_heads, int64_t D, int64_t room, int64_t window, int es) {
-    if (paged_form(B, heads, kv_heads, D, room, window, es).cluster) return 0;
-    return size_t(kPagedMaxCtas) * 2 * ((paged_rows(heads / kv_heads, es) * (paged_width(D) + 2) + 3) / 4 * 4) * 4;
-}
 cudaError_t paged_attention_bf16(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
 cudaError_t paged_attention_f32_g1(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
 cudaError_t paged_attention_f32_g4(const PagedArgs& a, void* workspace, const LaunchCfg& cfg);
