@@ -585,7 +585,7 @@ rowops_status_t rowops_router_balance_loss_backward(const void* logits, const in
  * RMSNorm, with the residual's addition, whose result leaves in 8 bits with scales
  * (for a product in 8 bits):
  *   residual_out = x + residual, rounded to `dtype`;  s = that (x without a residual)
- *   y     = s / sqrt(sum_j s_j^2 / N + eps) * w        (as rowops_rmsnorm, not rounded)
+ *   y     = s / sqrt(sum_j s_j^2 / N + eps) * w        (not rounded)
  *   scale = max(max |y| / 448, 2^-126) over a row, or over `group` columns of it
  *   q     = e4m3(y / scale), nearest even, so that y is about q * scale
  * (No counterpart on the source pages: the output form of rowops_fused_residual_rmsnorm.)
@@ -599,6 +599,9 @@ rowops_status_t rowops_router_balance_loss_backward(const void* logits, const in
  *   w, eps   as for rowops_rmsnorm.
  * q and scales lie apart from each other and from all else. A NaN in a row makes its
  * scales and its q NaN, an infinity those of its group (y is 0 in the row's others).
+ * s_j w_j is taken before the division by the root (by rowops_rmsnorm after it) and has to
+ * stay in fp32: one of 2^128 or more makes its group's scale infinite, its own q NaN and
+ * the group's others 0; one below 2^-126 is right to 2^-150, and y to 2^-150 / root.
  * 16-byte aligned rows of whole 16-byte vectors (and w, and q rows aligned to as many
  * bytes as a vector has elements) are the fastest.
  */

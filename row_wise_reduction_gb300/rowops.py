@@ -992,7 +992,8 @@ def rowops_rmsnorm_quant(
     q float8_e4m3fn (M, N), scales float32 (M, groups), one for every ``group``
     columns (a multiple of 32; 0: one a row), so that the norm is about q * scale,
     and residual_out = x + residual (None without a residual), which may be ``x``
-    or ``residual`` themselves. A given ``q`` may have a row stride of its own."""
+    or ``residual`` themselves. A given ``q`` may have a row stride of its own. The
+    products of rows and ``w`` have to stay in fp32's range."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(rowops_rmsnorm_quant, stream, dev, x, residual, w, eps, group, q, scales, residual_out)
