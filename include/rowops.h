@@ -587,7 +587,7 @@ rowops_status_t rowops_router_balance_loss_backward(const void* logits, const in
  *   residual_out = x + residual, rounded to `dtype`;  s = that (x without a residual)
  *   y     = s / sqrt(sum_j s_j^2 / N + eps) * w        (not rounded)
  *   scale = max(max |y| / 448, 2^-126) over a row, or over `group` columns of it
- *   q     = e4m3(y / scale), nearest even, so that y is about q * scale
+ *   q     = e4m3(y / scale), so that y is about q * scale
  * (No counterpart on the source pages: the output form of rowops_fused_residual_rmsnorm.)
  *
  *   x, residual, residual_out   device pointers to M rows of `ld` elements; residual
@@ -597,6 +597,9 @@ rowops_status_t rowops_router_balance_loss_backward(const void* logits, const in
  *   group    0: one scale a row; else a multiple of 32 columns, the last group of a row
  *            may be shorter. (More than N columns are as N.)
  *   w, eps   as for rowops_rmsnorm.
+ * y / scale is right to 9 * 2^-24 of it (at the least scale, to y's own error) before it
+ * is rounded to the nearest: where it lies as near as that to the middle of two e4m3
+ * numbers, q is either. Equal calls give equal bits.
  * q and scales lie apart from each other and from all else. A NaN in a row makes its
  * scales and its q NaN, an infinity those of its group (y is 0 in the row's others).
  * s_j w_j is taken before the division by the root (by rowops_rmsnorm after it) and has to
