@@ -676,6 +676,7 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
  *            the `_all` number then holds for every row. (On the device, numbers below
  *            the ranges are as 0, above them as the largest; a NaN temperature is 0, of
  *            the others no cut.)
+ *            Temperatures between 0 and 2^-126 are as 2^-126.
  *   token    device pointer to M int64.
  *   logprob  NULL, or M floats: the log-probability of the token among those kept.
  * N is at most 327680 and M at most 2^27 (ROWOPS_ERR_UNSUPPORTED beyond). w is held in

@@ -673,7 +673,8 @@ __global__ void __launch_bounds__(kBlock, 2) sample_kernel(const __grid_constant
               warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x / C;
     const int lo = rank * share, n = a.N - lo < share ? (a.N > lo ? a.N - lo : 0) : share;
-    const float temperature = a.temperature ? a.temperature[row] : a.temperature_all;
+    const float given = a.temperature ? a.temperature[row] : a.temperature_all;
+    const float temperature = given > 0.f ? fmaxf(given, 0x1p-126f) : given;  // (log2(e) / T is finite)
     const float min_p = a.min_p ? a.min_p[row] : a.min_p_all, top_p = a.top_p ? a.top_p[row] : a.top_p_all;
     const int top_k = a.top_k ? a.top_k[row] : a.top_k_all;
     {
