@@ -680,8 +680,9 @@ rowops_status_t rowops_paged_attention(const void* q, const void* k, const void*
  *   token    device pointer to M int64.
  *   logprob  NULL, or M floats: the log-probability of the token among those kept.
  * N is at most 327680 and M at most 2^27 (ROWOPS_ERR_UNSUPPORTED beyond). w is held in
- * fixed point, 44 bits behind the point and right to 2^-29 of its value, and added up
- * exactly: the same token for the same row, whatever the batch around it.
+ * fixed point, 44 bits behind the point, right to 2^-29 of its value and 2^-45 (a column
+ * of less than 2^-45 is not drawn, whatever is kept), and added up exactly: the same token
+ * for the same row, whatever the batch around it.
  */
 rowops_status_t rowops_sample(const void* logits, const float* u, const float* temperature, float temperature_all,
                               const int32_t* top_k, int32_t top_k_all, const float* top_p, float top_p_all,

@@ -10,7 +10,8 @@
 //
 // A cut or a draw lies next to a border in some row, where sums in 32 bits, or in
 // another order, give another token. So weights are fixed-point numbers of 44
-// fractional bits (right to 2^-29 of their value), whose 64-bit sums are exact and
+// fractional bits (right to 2^-29 of their value and 2^-45, half of the last bit: what is below that
+// of the maximum's weight is 0 and not drawn), whose 64-bit sums are exact and
 // the same in any order, and a cut is an exact pair: a place in the order of the
 // values, as the distance `kd` of a logit's ordered bits from the maximum's, and how
 // many of the equal ones, by index, still belong.
@@ -68,7 +69,7 @@ struct Weights {
     const uint64_t* roots;
     // (m - x) c = zi / 16 - f with |f| <= 1/32 and 2^f - 1 by its series, whose terms
     // past the fifth are below 2^-36. The difference and the product carry their errors
-    // along: what is lost is f's own rounding and the series', about 2^-29.
+    // along: what is lost is f's own rounding and the series', about 2^-29 of the weight, and its last bit.
     __device__ __forceinline__ uint64_t operator()(float x) const {
         const float d = m - x, bb = d - m, dl = (m - (d - bb)) - (x + bb);
         float t = -d * c_hi;

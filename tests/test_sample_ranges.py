@@ -34,3 +34,37 @@ def test_equal_maxima_at_a_subnormal_temperature():
     want = 25 * (torch.arange(8, device="cuda") // 2)
     for temperature in (2.0**-149, 1e-39):
         assert torch.equal(ro.rowops_sample(x, u, temperature=temperature), want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [500, 70000])
+@pytest.mark.parametrize("knobs", [{}, dict(top_k=400), dict(min_p=1e-16), dict(temperature=torch.ones(6))])
+def test_the_least_weight_that_is_drawn(dtype, N, knobs):
+    """u = 0 draws the first column that has a weight: of 2^-45 of the maximum's at least."""
+    x = torch.full((6, N), -200.0)
+    x[:, 300:303] = 0.0
+    x[:3, 7], x[3:, 7] = -30.75, -31.5  # 2^-44.4, 2^-45.4
+    knobs = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in knobs.items()}
+    logprob = torch.empty(6, device="cuda")
+    got = ro.rowops_sample(place(x, dtype), torch.zeros(6, device="cuda"), **knobs, logprob=logprob)
+    assert got.tolist() == [7] * 3 + [300] * 3
+    want = torch.tensor([-30.75] * 3 + [0.0] * 3) - torch.log(torch.tensor(3.0))
+    assert torch.all((logprob.cpu() - want).abs() <= 2.0**-22 * want.abs() + 2.0**-28)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("depth", [10, 20, 30, 40])
+def test_small_weights_are_right_to_their_bound(dtype, depth):
+    """Among n columns of 2^-depth each beside one maximum, the draw's border lies where the sum of the small weights says:
+    off by n (2^-29 of a weight, and 2^-45)."""
+    N = 60000
+    x = torch.full((1, N), -depth * 0.6931471805599453)
+    x[0, N - 1] = 0.0
+    x = place(x, dtype)
+    w = torch.exp(x[0, 0].double())
+    mass = float(w) * (N - 1)
+    bound = (N - 1) * (float(w) * 2.0**-29 + 2.0**-45) / (1 + mass) + 2.0**-24  # (u itself, at most 1 + 2^-24 of its value)
+    part = mass / (1 + mass)
+    u = torch.tensor([max(part - bound, 0.0), min(part + bound, 1 - 2.0**-24)], dtype=torch.float64).float().cuda()
+    last = ro.rowops_sample(x.expand(2, -1).contiguous(), u).tolist()
+    assert last[1] == N - 1 and (last[0] < N - 1 or float(u[0]) == 0)
