@@ -7,7 +7,9 @@
 // not, done again as s inv w, would have cost the kernels registers, fp32 8192 x 8192 131 to 159 us). Bound by the
 // traffic: x (and the residual, in and out) and one byte out. Measured: bf16 16384 x 8192 with
 // residual, groups of 128, 149 us (139 at the rate of a copy); 256 x 8192 4.1 us; fp32 rows off a 16-byte
-// boundary, 1501 x 4099 in groups of 64, 14.6 us for 4.6, bound by the instructions of their small pieces.
+// boundary, 1501 x 4099 in groups of 64, 14.6 to 15.6 us for 4.6; bf16 16384 x 4097 with residual 156 (a scale a row) to 178
+// (groups of 128) for 69: neither memory nor issue (50% of it) is the bound there, but chains of dependent steps in few
+// warps (27% of an SM's), a word of 4 or 2 bytes at a time.
 #pragma once
 
 #include <algorithm>
@@ -106,7 +108,8 @@ constexpr int kQuantThreads = 512;
 __host__ __device__ constexpr int quant_threads(int piece, int vpt) { return piece < 16 && vpt == 4 ? 320 : kQuantThreads; }
 
 // A row for every `tpr` threads, VPT vectors a thread; the vectors come through rings of copies,
-// each thread's its own (single bf16 straight to the registers), the weights stay in registers.
+// each thread's its own (single bf16 straight to the registers). The weights stay in registers, at eight vectors a thread
+// they are read again for every row.
 // kQuantLanes: a group is 2^lanes_log2 lanes of a warp. kQuantGroups:
 // any multiple of 32 columns; the maxima of every 32 columns meet in shared memory, in one of three
 // arrays: a row's is cleared two barriers before it is used again. `aligned`: q's rows start at multiples of V.

@@ -40,6 +40,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 // rows a group of 8 took twice the products, exponentials and accumulators (64 sequences of up to 8192: 190 us).
 // A lane holds the heads 2 (lane mod 4) and one more, of every 8. The weights, positions by
 // heads as they come, are transposed for the second product.
+// Long heads in blocks of 16 are bound by one CTA an SM with four warps: 32 sequences of up to 8192, 96 heads over 8, D 192
+// 427 us and D 256 647, whose accumulators take 255 registers and spill 250 to 300 bytes; blocks of 8 (64 heads over 8)
+// take 171 and 249.
 template <int DT, int H>
 struct PagedBf16 {
     using T = bf16_t;
