@@ -604,7 +604,8 @@ rowops_status_t rowops_router_balance_loss_backward(const void* logits, const in
  * scales and its q NaN, an infinity those of its group (y is 0 in the row's others).
  * s_j w_j is taken before the division by the root (by rowops_rmsnorm after it) and has to
  * stay in fp32: one of 2^128 or more makes its group's scale infinite, its own q NaN and
- * the group's others 0; one below 2^-126 is right to 2^-150, and y to 2^-150 / root.
+ * the group's others 0 (all NaN where the sum of squares is beyond fp32 as well); one below
+ * 2^-126 is right to 2^-150, and y to 2^-150 / root.
  * 16-byte aligned rows of whole 16-byte vectors (and w, and q rows aligned to as many
  * bytes as a vector has elements) are the fastest.
  */

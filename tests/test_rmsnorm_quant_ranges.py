@@ -84,3 +84,17 @@ def test_the_smallest_products(dtype, size, weight, eps, N, pad):
         v, n = y / each, q.float().cpu().numpy().astype(np.float64)
         beside = 4 * lost / each  # the product's and the scale's, this less than half of the scale; else at most 448
         assert np.all(np.abs(n - v) <= O.e4m3_half_step(np.abs(v) + beside) + 2 * relative(N) * np.abs(v) + beside)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,pad", SHAPES)
+def test_a_product_and_the_sum_of_squares_beyond(dtype, N, pad):
+    """1 / root is 0: finite products give 0, as in rowops_rmsnorm, and a group with an infinite one is not a number."""
+    x, w = rows(9, N, dtype, 1.0, pad, 7), weights(N, dtype, 1.0, 8)
+    x[:, 200], w[200] = 1e25, 1e25
+    for group in GROUPS:
+        q, scales, _ = ro.rowops_rmsnorm_quant(x, None, w, 1e-5, group)
+        g = torch.arange(scales.shape[1], device="cuda") == (200 // group if group else 0)
+        columns = torch.arange(N, device="cuda") // (group or N) == (200 // group if group else 0)
+        assert torch.isnan(scales[:, g]).all() and torch.isnan(q.float()[:, columns]).all()
+        assert torch.all(scales[:, ~g] == 2.0**-126) and torch.all(q.float()[:, ~columns] == 0)
